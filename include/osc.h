@@ -106,6 +106,7 @@ typedef OSC_ENUM(osc_ytype_e) {
 
 #define OSC_MAX_GROUPS 1024
 #define OSC_MAX_CHANNELS 3 /* protected channels per group in the *_multi calls */
+#define OSC_MAX_REQUESTS 4096 /* requests of one step in the paged-cache calls */
 
 /*
  * osc_pack_weights -- offline weight preparation (§3.2 weight side, §3.3).
@@ -291,6 +292,118 @@ osc_status osc_swiglu_quant(const void* GU, int S, int F, int G, const int32_t* 
  * Constraints: S >= 0, F > 0, F % 8 == 0, S < 2^24, S * 2F < 2^34.
  */
 osc_status osc_swiglu(const void* GU, int S, int F, void* Hout, void* stream);
+
+/*
+ * ---- What lies between the projections of a transformer block (not OSC steps of their own).
+ *
+ * osc_rmsnorm_quant -- residual add + RMS norm, quantized: the operand of the projection
+ * that follows (QKV, or the MLP's up-projection), without the normed rows in memory.
+ *   X    [S][H] bf16, device, read only: the previous projection's output (or the
+ *        block's input, without RES).
+ *   RES  [S][H] bf16 residual stream or NULL; RES_OUT [S][H] bf16, written, NULL
+ *        exactly when RES is.  RES_OUT may be RES itself (updated in place); no other
+ *        operand may overlap an output.
+ *   W    [H] bf16 norm weight.
+ *   r = RES ? bf16(X + RES) : X, to RES_OUT;  y = bf16(r * (1 / sqrt(mean(r^2) + eps)) * w)
+ *   with the mean, the root and the products in binary32 and one rounding (nearest,
+ *   ties to even) to y.  L, m, afmt, QX, SX, B as osc_quant_act_multi on y, bit for
+ *   bit.  The sum of squares of a row must stay below 2^128.
+ * Constraints: as osc_quant_act_multi, and eps positive and finite (OSC_E_SHAPE).
+ */
+osc_status osc_rmsnorm_quant(const void* X, const void* RES, const void* W, int S, int H, float eps, int G,
+                             const int32_t* L, int m, osc_fmt afmt, void* RES_OUT, void* QX, uint8_t* SX, void* B,
+                             void* stream);
+
+/*
+ * osc_rmsnorm -- the same y written out: Y [S][H] bf16 row-major (device, written), bit
+ * for bit the y that osc_rmsnorm_quant quantizes.  For calibration rows and the norm
+ * behind the last block.
+ * Constraints: S >= 0, S < 2^24, H % 256 == 0, 0 < H <= 65536, S * H < 2^34, eps
+ * positive and finite.
+ */
+osc_status osc_rmsnorm(const void* X, const void* RES, const void* W, int S, int H, float eps, void* RES_OUT, void* Y,
+                       void* stream);
+
+/*
+ * ---- The paged key / value cache.
+ * NP pages of `page` token slots (16, 32, 64, 128 or 256); slot s is slot s % page of page
+ * s / page.  With HKV key heads of D channels (64 or 128), bf16:
+ *   KC  [NP][HKV][page][D]      VC  [NP][HKV][D][page]
+ * (V turned, so that the attention reads the keys of one channel as contiguous bytes).
+ * TABLE int32 [R][MB]: row r lists request r's pages in order; entries outside [0, NP)
+ * name no page.  int32 and single-value arrays of these calls need 4-byte alignment only,
+ * every other pointer 16-byte.  Device-side values are checked on the device: none of
+ * them makes a call read or write outside its buffers.
+ *
+ * osc_page_plan -- page tables and slot maps of one step, from request lengths.
+ *   CTX, NEW  int32 [R]: tokens of request r in the cache before the step, and new ones
+ *        (0 for an idle row; negative counts as 0).
+ *   FREE int32 [F] page ids, used in order from FREE[*HEAD] (HEAD NULL: from FREE[0]; below
+ *        0 counts as 0), by the requests in order: request r takes
+ *        ceil((CTX + NEW) / page) - ceil(CTX / page) pages into TABLE's entries behind
+ *        its ceil(CTX / page) first.  No other entry is touched.
+ *   CU   int32 [R + 1], written: new tokens before request r.   KV int32 [R]: CTX + NEW.
+ *   SLOT, POS int32 [T], written: slot and position (CTX + i) of new token CU[r] + i;
+ *        both -1 for the padding rows t >= CU[R].
+ *   USED int32 [1], written: pages this step takes.
+ * What does not fit: a page behind FREE's end or outside [0, NP) is entered as -1, and
+ * tokens in it, or at positions >= MB * page, get slot -1 (osc_qkv_append skips them; USED
+ * > F - *HEAD tells).  Tokens >= T are counted in CU but not mapped.  Sums saturate at 2^31 - 1.
+ * The call reads no entry that it writes: repeated on the same inputs (a replayed graph) it
+ * gives the same tables.  One launch.
+ * Constraints: 0 <= R <= OSC_MAX_REQUESTS, F, T >= 0, NP, MB >= 1, NP * page < 2^31,
+ * MB * page < 2^31, R * MB < 2^31.  CU and USED are required even when R or T is 0.
+ */
+osc_status osc_page_plan(const int32_t* CTX, const int32_t* NEW, int R, int page, int NP, const int32_t* FREE, int F,
+                         const int32_t* HEAD, int T, int32_t* TABLE, int MB, int32_t* CU, int32_t* KV, int32_t* SLOT,
+                         int32_t* POS, int32_t* USED, void* stream);
+
+/*
+ * osc_qkv_append -- a step's QKV rows: queries out, keys and values into the cache.
+ *   QKV  [S][(HQ + 2 HKV) D] bf16, device, read only: the HQ query, HKV key and HKV value
+ *        heads of each token (the QKV projection's Y).
+ *   WQ, WK  [D] bf16 or both NULL: x = x * (1 / sqrt(mean(x^2) + eps)) * w over each query /
+ *        key head, in binary32, unrounded.
+ *   CS   fp32 [P][D] or NULL (no rotation): D/2 cosines, then D/2 sines of each position's
+ *        angles; with (x1, x2) the halves of a head, x1 cos - x2 sin and x2 cos + x1 sin.
+ *   POS, SLOT  int32 [S]: position (read only with CS) and cache slot of each token.
+ *   Q    [S][HQ][D] bf16, written (rounded once); KC, VC: the slots of the S tokens written.
+ * A token whose slot is outside [0, NP * page), or whose position is outside [0, P), writes
+ * nothing: its row of Q stays as it was.  Slots must be distinct: of two tokens with one slot
+ * the cache holds channels of either.
+ * Constraints: S >= 0, S < 2^24, 1 <= HQ, HKV <= 1024, D in {64, 128}, S (HQ + 2 HKV) D <
+ * 2^34, NP >= 1, NP * page < 2^31, eps positive and finite with WQ, P >= 1 with CS.
+ */
+osc_status osc_qkv_append(const void* QKV, int S, int HQ, int HKV, int D, const void* WQ, const void* WK, float eps,
+                          const float* CS, int P, const int32_t* POS, const int32_t* SLOT, void* Q, void* KC, void* VC,
+                          int NP, int page, void* stream);
+
+/*
+ * osc_attn_paged -- attention of R requests' new tokens over the paged cache, causal:
+ * token i of the n = CU[r+1] - CU[r] new tokens of request r sees the keys j <= KV[r] - n + i
+ * (its own included; KV counts the new ones, already appended), and
+ *   O = sum_j softmax_j(scale q . k_j) v_j,   query head h on key head h / (HQ / HKV),
+ * with scores, softmax and sums in binary32 and the weights rounded to bf16 for the second
+ * product.  n = 1 is a decode step, KV = n a whole prompt, anything between a chunk; the
+ * requests of one call may differ.
+ *   Q, O [S][HQ][D] bf16; CU int32 [R + 1] ascending (values are taken into [0, S]),
+ *   KV int32 [R] (taken into [0, MB * page]).
+ * A token that sees no key (KV < n, or no page of its keys exists) gets zeros; keys whose
+ * page does not exist are left out.  Rows of O outside [CU[0], CU[R]) stay as they were.
+ * What the cache holds behind a request's KV keys is never used, whatever it is; NaN in a
+ * key reaches the rows that see it, NaN in a value may reach every row of its request.
+ *   WS, ws_bytes: device workspace of at least osc_attn_workspace's bytes for the same
+ *   sizes (WS may be NULL when that is 0), free again when the call's work is done: calls
+ *   that can overlap, two graphs replayed on two streams included, need one each.
+ * The result does not depend on what else runs (sums are joined in a fixed order).
+ * Constraints: S >= 0, S < 2^24, 0 <= R <= OSC_MAX_REQUESTS, HQ a multiple of HKV, both in
+ * 1..1024, D in {64, 128}, S * HQ * D < 2^34, NP, MB >= 1, NP * page and MB * page < 2^31, scale
+ * positive and finite; too small a workspace is OSC_E_SHAPE.
+ */
+osc_status osc_attn_workspace(int S, int R, int HQ, int HKV, int D, int page, int MB, int64_t* bytes);
+osc_status osc_attn_paged(const void* Q, const void* KC, const void* VC, int S, int R, int HQ, int HKV, int D, int page,
+                          int MB, int NP, const int32_t* TABLE, const int32_t* CU, const int32_t* KV, float scale,
+                          void* O, void* WS, int64_t ws_bytes, void* stream);
 
 /* Human-readable name of a status code (static storage). */
 const char* osc_status_str(osc_status s);

@@ -32,13 +32,15 @@ OSC_Y_BF16 = 0
 OSC_Y_F32 = 1
 OSC_MAX_GROUPS = 1024
 OSC_MAX_CHANNELS = 3
+OSC_MAX_REQUESTS = 4096
 
 STATUS = {0: "OSC_OK", 1: "OSC_E_NULL", 2: "OSC_E_SHAPE", 3: "OSC_E_TABLE", 4: "OSC_E_ALIGN",
           5: "OSC_E_FORMAT", 6: "OSC_E_DEVICE"}
 
 EXPORTS = ("osc_pack_weights", "osc_quant_act", "osc_gemm", "osc_gemm_fp8", "osc_build_table",
            "osc_pack_weights_multi", "osc_quant_act_multi", "osc_gemm_multi", "osc_build_table_multi",
-           "osc_swiglu_quant", "osc_swiglu", "osc_linear_decode", "osc_gemm_fp6p", "osc_status_str",
+           "osc_swiglu_quant", "osc_swiglu", "osc_linear_decode", "osc_gemm_fp6p", "osc_rmsnorm_quant",
+           "osc_rmsnorm", "osc_page_plan", "osc_qkv_append", "osc_attn_workspace", "osc_attn_paged", "osc_status_str",
            "osc_last_device_error")
 
 if not os.path.exists(LIB_PATH):
@@ -48,6 +50,8 @@ _lib = ctypes.CDLL(LIB_PATH)
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _D = ctypes.c_double
+_F = ctypes.c_float
+_L = ctypes.c_int64
 _lib.osc_pack_weights.argtypes = [_P, _I, _I, _I, _P, _I, _P, _P, _P, _P]
 _lib.osc_quant_act.argtypes = [_P, _I, _I, _I, _P, _I, _P, _P, _P, _P]
 _lib.osc_gemm.argtypes = [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _I, _P]
@@ -61,6 +65,12 @@ _lib.osc_swiglu_quant.argtypes = [_P, _I, _I, _I, _P, _I, _I, _P, _P, _P, _P]
 _lib.osc_swiglu.argtypes = [_P, _I, _I, _P, _P]
 _lib.osc_linear_decode.argtypes = [_P, _I, _I, _I, _P, _I, _P, _P, _P, _I, _P, _I, _P]
 _lib.osc_gemm_fp6p.argtypes = [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _I, _P]
+_lib.osc_rmsnorm_quant.argtypes = [_P, _P, _P, _I, _I, _F, _I, _P, _I, _I, _P, _P, _P, _P, _P]
+_lib.osc_rmsnorm.argtypes = [_P, _P, _P, _I, _I, _F, _P, _P, _P]
+_lib.osc_page_plan.argtypes = [_P, _P, _I, _I, _I, _P, _I, _P, _I, _P, _I, _P, _P, _P, _P, _P, _P]
+_lib.osc_qkv_append.argtypes = [_P, _I, _I, _I, _I, _P, _P, _F, _P, _I, _P, _P, _P, _P, _P, _I, _I, _P]
+_lib.osc_attn_workspace.argtypes = [_I, _I, _I, _I, _I, _I, _I, _P]
+_lib.osc_attn_paged.argtypes = [_P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _P, _P, _P, _F, _P, _P, _L, _P]
 for _f in EXPORTS[:-2]:
     getattr(_lib, _f).restype = _I
 _lib.osc_status_str.argtypes = [_I]
@@ -87,9 +97,11 @@ def side_elems(rows: int, H: int, G: int, m: int = 1) -> int:
 
 
 class OscError(RuntimeError):
-    def __init__(self, status: int, call: str):
+    def __init__(self, status: int, call: str, detail: str = ""):
         self.status = status
         msg = f"{call}: {osc_status_str(status)}"
+        if detail:
+            msg += f" ({detail})"
         if status == 6:
             msg += f" ({_lib.osc_last_device_error().decode()})"
         super().__init__(msg)
@@ -203,3 +215,76 @@ def osc_build_table_multi(Xcal, R: int, H: int, G: int, alpha: float, rho: float
                           stream=None) -> None:
     _check(_lib.osc_build_table_multi(_ptr(Xcal), R, H, G, float(alpha), float(rho), m, _ptr(L), _ptr(hits),
                                       _ptr(events), _stream(stream)), "osc_build_table_multi")
+
+
+# ---- between the projections: norm, paged cache, attention
+
+def _fits(call: str, *pairs) -> None:
+    """The tensors of ``pairs`` (tensor or None or address, bytes the call reads or writes) lie
+    contiguously on the current device and hold that many bytes."""
+    dev = torch.cuda.current_device()
+    for t, need in pairs:
+        if t is None or isinstance(t, int):
+            continue
+        if t.get_device() != dev:
+            raise OscError(2, call, f"a tensor on {t.device}, the current device is cuda:{dev}")
+        if not t.is_contiguous() or t.nbytes < need:
+            raise OscError(2, call, f"a tensor of {t.nbytes} bytes, strides {tuple(t.stride())}, where {need} contiguous "
+                                    "bytes are needed")
+
+
+def osc_rmsnorm_quant(X, RES, W, S: int, H: int, eps: float, G: int, L, m: int, afmt: int, RES_OUT, QX, SX, B,
+                      stream=None) -> None:
+    """r = X + RES to RES_OUT (both None: r = X); the RMS norm of r, quantized as osc_quant_act_multi."""
+    keep, lp = _table(L)
+    n = 2 * S * H
+    g = max(G, 1)  # the library refuses a group size it does not have
+    if keep is not None and keep.size < H // g * m:
+        raise OscError(3, "osc_rmsnorm_quant", f"{keep.size} table entries for {H // g} groups of {m}")
+    _fits("osc_rmsnorm_quant", (X, n), (RES, n), (W, 2 * H), (RES_OUT, n), (QX, code_bytes(S, H, afmt)),
+          (SX, scale_bytes(S, H, g, afmt)), (B, 2 * side_elems(S, H, g, m)))
+    _check(_lib.osc_rmsnorm_quant(_ptr(X), _ptr(RES), _ptr(W), S, H, eps, G, lp, m, afmt, _ptr(RES_OUT), _ptr(QX), _ptr(SX),
+                                  _ptr(B), _stream(stream)), "osc_rmsnorm_quant")
+
+
+def osc_rmsnorm(X, RES, W, S: int, H: int, eps: float, RES_OUT, Y, stream=None) -> None:
+    """The same norm written out: Y [S, H] bf16."""
+    n = 2 * S * H
+    _fits("osc_rmsnorm", (X, n), (RES, n), (W, 2 * H), (RES_OUT, n), (Y, n))
+    _check(_lib.osc_rmsnorm(_ptr(X), _ptr(RES), _ptr(W), S, H, eps, _ptr(RES_OUT), _ptr(Y), _stream(stream)), "osc_rmsnorm")
+
+
+def osc_page_plan(CTX, NEW, R: int, page: int, NP: int, FREE, F: int, HEAD, T: int, TABLE, MB: int, CU, KV, SLOT, POS, USED,
+                  stream=None) -> None:
+    """Page tables and slot maps of one step from request lengths (all int32 device tensors)."""
+    _fits("osc_page_plan", (CTX, 4 * R), (NEW, 4 * R), (FREE, 4 * F), (HEAD, 4), (TABLE, 4 * R * MB), (CU, 4 * R + 4), (KV, 4 * R),
+          (SLOT, 4 * T), (POS, 4 * T), (USED, 4))
+    _check(_lib.osc_page_plan(_ptr(CTX), _ptr(NEW), R, page, NP, _ptr(FREE), F, _ptr(HEAD), T, _ptr(TABLE), MB, _ptr(CU), _ptr(KV),
+                              _ptr(SLOT), _ptr(POS), _ptr(USED), _stream(stream)), "osc_page_plan")
+
+
+def osc_qkv_append(QKV, S: int, HQ: int, HKV: int, D: int, WQ, WK, eps: float, CS, P: int, POS, SLOT, Q, KC, VC, NP: int,
+                   page: int, stream=None) -> None:
+    """QKV rows [S, (HQ + 2 HKV) D]: normed and rotated queries to Q, keys and values to their slots."""
+    c = 2 * NP * HKV * page * D
+    _fits("osc_qkv_append", (QKV, 2 * S * (HQ + 2 * HKV) * D), (WQ, 2 * D), (WK, 2 * D), (CS, 4 * P * D), (POS, 4 * S), (SLOT, 4 * S),
+          (Q, 2 * S * HQ * D), (KC, c), (VC, c))
+    _check(_lib.osc_qkv_append(_ptr(QKV), S, HQ, HKV, D, _ptr(WQ), _ptr(WK), eps, _ptr(CS), P, _ptr(POS), _ptr(SLOT), _ptr(Q),
+                               _ptr(KC), _ptr(VC), NP, page, _stream(stream)), "osc_qkv_append")
+
+
+def osc_attn_workspace(S: int, R: int, HQ: int, HKV: int, D: int, page: int, MB: int) -> int:
+    """Bytes of the workspace that osc_attn_paged needs at these sizes."""
+    n = _L(0)
+    _check(_lib.osc_attn_workspace(S, R, HQ, HKV, D, page, MB, ctypes.byref(n)), "osc_attn_workspace")
+    return n.value
+
+
+def osc_attn_paged(Q, KC, VC, S: int, R: int, HQ: int, HKV: int, D: int, page: int, MB: int, NP: int, TABLE, CU, KV,
+                   scale: float, O, WS, stream=None) -> None:
+    """Causal attention of the new tokens of R requests over the paged cache; WS: a tensor of at least
+    osc_attn_workspace bytes, or None where that is 0."""
+    c, n = 2 * NP * HKV * page * D, 2 * S * HQ * D
+    _fits("osc_attn_paged", (Q, n), (KC, c), (VC, c), (TABLE, 4 * R * MB), (CU, 4 * R + 4), (KV, 4 * R), (O, n), (WS, 0))
+    _check(_lib.osc_attn_paged(_ptr(Q), _ptr(KC), _ptr(VC), S, R, HQ, HKV, D, page, MB, NP, _ptr(TABLE), _ptr(CU), _ptr(KV), scale,
+                               _ptr(O), _ptr(WS), 0 if WS is None else WS.nbytes, _stream(stream)), "osc_attn_paged")

@@ -3,6 +3,7 @@
 // §3.1 table (osc_build_table), §3.2 extraction + microscaling quantization (osc_quant_act),
 // §3.2-§3.3 offline weight preparation (osc_pack_weights), §3.2 dual-path GEMM (osc_gemm),
 // §4 FP8 fallback (osc_gemm_fp8).
+#include <math.h>
 #include <stdint.h>
 
 #include "osc_internal.h"
@@ -53,6 +54,22 @@ bool valid_m(int m) { return m >= 1 && m <= osc::kMaxChannels; }
 // compensation path (osc_gemm_fp8 takes neither B nor W_L), so a table with MXFP8 is refused
 // rather than having its channels zeroed and then dropped.
 bool fmt_takes_table(osc_fmt f, const int32_t* L) { return !(f == OSC_MXFP8 && L != nullptr); }
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+bool positive(float v) { return v > 0.0f && isfinite(v); }
+
+// the page sizes of the cache: log2 of it, or -1
+int page_shift(int page) {
+  for (int sh = 4; sh <= 8; ++sh)
+    if (page == 1 << sh) return sh;
+  return -1;
+}
+
+// heads of a projection row or of the cache
+bool valid_heads(int HQ, int HKV, int D) {
+  return HQ >= 1 && HKV >= 1 && HQ <= 1024 && HKV <= 1024 && (D == 64 || D == 128);
+}
 
 // the HIP error behind the calling thread's most recent OSC_E_DEVICE
 thread_local hipError_t g_last_error = hipSuccess;
@@ -260,6 +277,111 @@ osc_status osc_build_table_multi(const void* Xcal, int R, int H, int G, double a
 osc_status osc_build_table(const void* Xcal, int R, int H, int G, double alpha, double rho, int32_t* L,
                            int32_t* hits, int32_t* events, void* stream) {
   return osc_build_table_multi(Xcal, R, H, G, alpha, rho, 1, L, hits, events, stream);
+}
+
+osc_status osc_rmsnorm_quant(const void* X, const void* RES, const void* W, int S, int H, float eps, int G,
+                             const int32_t* L, int m, osc_fmt afmt, void* RES_OUT, void* QX, uint8_t* SX, void* B,
+                             void* stream) {
+  if (!valid_fmt(afmt, G) || !fmt_takes_table(afmt, L)) return OSC_E_FORMAT;
+  osc_status st = check_tiled(S, H, G);
+  if (st != OSC_OK) return st;
+  if (!valid_m(m) || (H / G) * m > OSC_MAX_GROUPS || !positive(eps)) return OSC_E_SHAPE;
+  if (S == 0) return OSC_OK;
+  if (!X || !W || !QX || !SX) return OSC_E_NULL;
+  if ((RES == nullptr) != (RES_OUT == nullptr) || (L == nullptr) != (B == nullptr)) return OSC_E_NULL;
+  if (!aligned16(X) || !aligned16(RES) || !aligned16(W) || !aligned16(RES_OUT) || !aligned16(QX) || !aligned16(SX) ||
+      !aligned16(B))
+    return OSC_E_ALIGN;
+  osc::TableArg tab;
+  if (L) {
+    st = pack_table(L, H / G, m, G, &tab);
+    if (st != OSC_OK) return st;
+  }
+  osc::NormArgs a{X, RES, W, S, H, eps, G, m, L ? &tab : nullptr, afmt, RES_OUT, QX, SX, B};
+  return from_hip(osc::launch_rmsnorm(a, static_cast<hipStream_t>(stream)));
+}
+
+osc_status osc_rmsnorm(const void* X, const void* RES, const void* W, int S, int H, float eps, void* RES_OUT, void* Y,
+                       void* stream) {
+  const osc_status st = check_tiled(S, H, 64);
+  if (st != OSC_OK) return st;
+  if (!positive(eps)) return OSC_E_SHAPE;
+  if (S == 0) return OSC_OK;
+  if (!X || !W || !Y || (RES == nullptr) != (RES_OUT == nullptr)) return OSC_E_NULL;
+  if (!aligned16(X) || !aligned16(RES) || !aligned16(W) || !aligned16(RES_OUT) || !aligned16(Y)) return OSC_E_ALIGN;
+  osc::NormArgs a{X, RES, W, S, H, eps, 64, 1, nullptr, OSC_MXFP4, RES_OUT, Y, nullptr, nullptr};
+  return from_hip(osc::launch_rmsnorm(a, static_cast<hipStream_t>(stream)));
+}
+
+osc_status osc_page_plan(const int32_t* CTX, const int32_t* NEW, int R, int page, int NP, const int32_t* FREE, int F,
+                         const int32_t* HEAD, int T, int32_t* TABLE, int MB, int32_t* CU, int32_t* KV, int32_t* SLOT,
+                         int32_t* POS, int32_t* USED, void* stream) {
+  const int sh = page_shift(page);
+  if (sh < 0 || R < 0 || R > OSC_MAX_REQUESTS || NP < 1 || F < 0 || T < 0 || MB < 1) return OSC_E_SHAPE;
+  if (((long long)NP << sh) > 0x7FFFFFFFLL || ((long long)MB << sh) > 0x7FFFFFFFLL) return OSC_E_SHAPE;
+  if ((long long)R * MB > 0x7FFFFFFFLL) return OSC_E_SHAPE;
+  if (!CU || !USED) return OSC_E_NULL;
+  if (R > 0 && (!CTX || !NEW || !TABLE || !KV)) return OSC_E_NULL;
+  if ((F > 0 && !FREE) || (T > 0 && (!SLOT || !POS))) return OSC_E_NULL;
+  if (!aligned4(CTX) || !aligned4(NEW) || !aligned4(FREE) || !aligned4(HEAD) || !aligned4(TABLE) || !aligned4(CU) ||
+      !aligned4(KV) || !aligned4(SLOT) || !aligned4(POS) || !aligned4(USED))
+    return OSC_E_ALIGN;
+  osc::PlanArgs a{CTX, NEW, R, sh, NP, FREE, F, HEAD, T, TABLE, MB, CU, KV, SLOT, POS, USED};
+  return from_hip(osc::launch_page_plan(a, static_cast<hipStream_t>(stream)));
+}
+
+osc_status osc_qkv_append(const void* QKV, int S, int HQ, int HKV, int D, const void* WQ, const void* WK, float eps,
+                          const float* CS, int P, const int32_t* POS, const int32_t* SLOT, void* Q, void* KC, void* VC,
+                          int NP, int page, void* stream) {
+  const int sh = page_shift(page);
+  if (sh < 0 || S < 0 || S >= (1 << 24) || !valid_heads(HQ, HKV, D) || NP < 1) return OSC_E_SHAPE;
+  if ((long long)S * (HQ + 2 * HKV) * D >= (1LL << 34) || ((long long)NP << sh) > 0x7FFFFFFFLL) return OSC_E_SHAPE;
+  if ((WQ || WK) && !positive(eps)) return OSC_E_SHAPE;
+  if (CS && P < 1) return OSC_E_SHAPE;
+  if (S == 0) return OSC_OK;
+  if (!QKV || !SLOT || !Q || !KC || !VC || (CS && !POS) || (WQ == nullptr) != (WK == nullptr)) return OSC_E_NULL;
+  if (!aligned16(QKV) || !aligned16(WQ) || !aligned16(WK) || !aligned16(CS) || !aligned16(Q) || !aligned16(KC) ||
+      !aligned16(VC) || !aligned4(POS) || !aligned4(SLOT))
+    return OSC_E_ALIGN;
+  osc::AppendArgs a{QKV, S, HQ, HKV, D, WQ, WK, eps, CS, P, POS, SLOT, Q, KC, VC, NP, sh};
+  return from_hip(osc::launch_qkv_append(a, static_cast<hipStream_t>(stream)));
+}
+
+static osc_status check_attn(int S, int R, int HQ, int HKV, int D, int page, int MB) {
+  const int sh = page_shift(page);
+  if (sh < 0 || S < 0 || S >= (1 << 24) || R < 0 || R > OSC_MAX_REQUESTS || MB < 1) return OSC_E_SHAPE;
+  if (!valid_heads(HQ, HKV, D) || HQ % HKV != 0) return OSC_E_SHAPE;
+  if ((long long)S * HQ * D >= (1LL << 34) || ((long long)MB << sh) > 0x7FFFFFFFLL) return OSC_E_SHAPE;
+  return OSC_OK;
+}
+
+osc_status osc_attn_workspace(int S, int R, int HQ, int HKV, int D, int page, int MB, int64_t* bytes) {
+  const osc_status st = check_attn(S, R, HQ, HKV, D, page, MB);
+  if (st != OSC_OK) return st;
+  if (!bytes) return OSC_E_NULL;
+  *bytes = S == 0 || R == 0 ? 0 : osc::attn_plan(S, R, HQ, HKV, D, page, MB).ws_bytes;
+  return OSC_OK;
+}
+
+osc_status osc_attn_paged(const void* Q, const void* KC, const void* VC, int S, int R, int HQ, int HKV, int D, int page,
+                          int MB, int NP, const int32_t* TABLE, const int32_t* CU, const int32_t* KV, float scale,
+                          void* O, void* WS, int64_t ws_bytes, void* stream) {
+  const osc_status st = check_attn(S, R, HQ, HKV, D, page, MB);
+  if (st != OSC_OK) return st;
+  const int sh = page_shift(page);
+  if (NP < 1 || ((long long)NP << sh) > 0x7FFFFFFFLL || !positive(scale)) return OSC_E_SHAPE;
+  if (S == 0 || R == 0) return OSC_OK;
+  if (!Q || !KC || !VC || !TABLE || !CU || !KV || !O) return OSC_E_NULL;
+  const osc::AttnPlan p = osc::attn_plan(S, R, HQ, HKV, D, page, MB);
+  if (p.ws_bytes > 0 && !WS) return OSC_E_NULL;
+  if (ws_bytes < p.ws_bytes) return OSC_E_SHAPE;
+  if (!aligned16(Q) || !aligned16(KC) || !aligned16(VC) || !aligned16(O) || !aligned16(WS) || !aligned4(TABLE) ||
+      !aligned4(CU) || !aligned4(KV))
+    return OSC_E_ALIGN;
+  float* ws = static_cast<float*>(WS);
+  osc::AttnArgs a{Q,  KC, VC, S, R, HQ, HKV, HQ / HKV, sh, page - 1, MB, NP, TABLE, CU, KV, scale * 1.4426950408889634f,
+                  O,  ws, ws ? ws + (long)p.nsplit * S * HQ * D : nullptr, p.large_tiles, p.nsplit};
+  return from_hip(osc::launch_attn(a, D, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

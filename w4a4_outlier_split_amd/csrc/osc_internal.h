@@ -83,4 +83,67 @@ struct FusedArgs {
 long fused_lds_bytes(int H, int G, int kc);
 hipError_t launch_linear_dec(const FusedArgs& a, hipStream_t st);
 
+// Residual add + RMS norm of S rows of H bf16; SX == nullptr: y itself to QX (row-major bf16), else its
+// quantization, tab == nullptr without extraction.
+struct NormArgs {
+  const void *X, *RES, *W;
+  int S, H;
+  float eps;
+  int G, m;
+  const TableArg* tab;
+  osc_fmt afmt;
+  void* RES_OUT;
+  void* QX;
+  uint8_t* SX;
+  void* B;
+};
+hipError_t launch_rmsnorm(const NormArgs& a, hipStream_t st);
+
+// Page tables and slot maps of one step (osc_page_plan); sh = log2(page).
+struct PlanArgs {
+  const int32_t *CTX, *NEW;
+  int R, sh, NP;
+  const int32_t* FREE;
+  int F;
+  const int32_t* HEAD;
+  int T;
+  int32_t* TABLE;
+  int MB;
+  int32_t *CU, *KV, *SLOT, *POS, *USED;
+};
+hipError_t launch_page_plan(const PlanArgs& a, hipStream_t st);
+
+// Head norm, rotary embedding and cache write (osc_qkv_append); sh = log2(page).
+struct AppendArgs {
+  const void* QKV;
+  int S, HQ, HKV, D;
+  const void *WQ, *WK;
+  float eps;
+  const float* CS;
+  int P;
+  const int32_t *POS, *SLOT;
+  void *Q, *KC, *VC;
+  int NP, sh;
+};
+hipError_t launch_qkv_append(const AppendArgs& a, hipStream_t st);
+
+// Attention over the paged cache (osc_attn_paged).
+struct AttnPlan {
+  int large_tiles;  // upper bound on the 128-row tiles of one key head
+  int nsplit;       // ranges the keys of a tile are cut into
+  long ws_bytes;
+};
+AttnPlan attn_plan(int S, int R, int HQ, int HKV, int D, int page, int MB);
+struct AttnArgs {
+  const void *Q, *KC, *VC;
+  int S, R, HQ, HKV, g;  // g = HQ / HKV
+  int sh, mask, MB, NP;  // page = 1 << sh, mask = page - 1
+  const int32_t *TABLE, *CU, *KV;
+  float scale_log2;  // scale * log2(e)
+  void* O;
+  float *PO, *PM;  // [nsplit][S*HQ][D] unnormalised outputs, [nsplit][S*HQ][2] scaled maximum and sum
+  int large_tiles, nsplit;
+};
+hipError_t launch_attn(const AttnArgs& a, int D, hipStream_t st);
+
 }  // namespace osc
