@@ -1,10 +1,11 @@
-"""The linear layers of a Qwen3-8B-shaped transformer block run through libosc, each on the path
-its input calls for (OSC page "W4A4量化技术：OSC框架如何实现高效LLM部署", §2.3 Table 1 and the
-per-module rule that follows it, §4 for W2).
+"""A Qwen3-8B-shaped transformer block run through libosc, each linear layer on the path its input
+calls for (OSC page "W4A4量化技术：OSC框架如何实现高效LLM部署", §2.3 Table 1 and the per-module rule
+that follows it, §4 for W2).
 
 Host-side orchestration only: buffers are torch tensors (device memory), every step of every
-layer runs in the library's kernels through the C ABI.  Attention itself (between QKV and Wo) and
-the norms and residual adds are not part of this block: the Wo layer takes its input as given.
+layer runs in the library's kernels through the C ABI.  ``Linear`` and ``MLP`` are the projections;
+``Pages``, ``LayerCache``, ``Attention`` and ``Block`` put the residual adds, the norms and the attention
+over the paged cache between them.
 
 Per-module rule (§2.3): a module input's clustering density C is the share of a group's outlier
 events captured by its statically indexed channel (§2.2), averaged over the groups that saw an
@@ -20,9 +21,10 @@ from typing import Optional
 
 import numpy as np
 
-from . import (OSC_MAX_GROUPS, OSC_MXFP4, OSC_MXFP8, OSC_Y_BF16, code_bytes, osc_build_table_multi, osc_gemm_fp8,
-               osc_gemm_multi, osc_pack_weights_multi, osc_quant_act_multi, osc_swiglu, osc_swiglu_quant,
-               scale_bytes, side_elems)
+from . import (OSC_MAX_GROUPS, OSC_MXFP4, OSC_MXFP8, OSC_Y_BF16, code_bytes, osc_attn_paged, osc_attn_workspace,
+               osc_build_table_multi, osc_gemm_fp8, osc_gemm_multi, osc_pack_weights_multi, osc_page_plan,
+               osc_qkv_append, osc_quant_act_multi, osc_rmsnorm_quant, osc_swiglu, osc_swiglu_quant, scale_bytes,
+               side_elems)
 
 DENSITY_THRESHOLD = 0.35  # §2.3: below it the module falls back to FP8 microscaling
 ALPHA, RHO = 5.0, 0.35    # table-builder defaults (§3.1 / §5.2; rho: the 35 % line of §2.3)
@@ -140,6 +142,11 @@ class Linear:
         QX, SX, B = act
         osc_quant_act_multi(X, S, self.H, self.G, self.L, self.m, self.afmt, QX, SX, B, stream)
 
+    def norm_quantize(self, X, res, w, eps: float, S: int, act, stream=None) -> None:
+        """Residual add (in place on ``res``, or none) and RMS norm on the way into the quantization."""
+        QX, SX, B = act
+        osc_rmsnorm_quant(X, res, w, S, self.H, eps, self.G, self.L, self.m, self.afmt, res, QX, SX, B, stream)
+
     def gemm(self, act, S: int, Y, yt: int = OSC_Y_BF16, stream=None) -> None:
         QX, SX, B = act
         if self.path == "osc":
@@ -170,7 +177,12 @@ class MLP:
                 "h": self.down.act_buffers(S, device)}
 
     def forward(self, X, S: int, bufs, Y, yt: int = OSC_Y_BF16, stream=None) -> None:
-        self.up.forward(X, S, bufs["x"], bufs["gu"], OSC_Y_BF16, stream)
+        self.up.quantize(X, S, bufs["x"], stream)
+        self.forward_quantized(S, bufs, Y, yt, stream)
+
+    def forward_quantized(self, S: int, bufs, Y, yt: int = OSC_Y_BF16, stream=None) -> None:
+        """From the up-projection's quantized input in bufs["x"]."""
+        self.up.gemm(bufs["x"], S, bufs["gu"], OSC_Y_BF16, stream)
         QX, SX, B = bufs["h"]
         d = self.down
         osc_swiglu_quant(bufs["gu"], S, self.F, d.G, d.L, d.m, d.afmt, QX, SX, B, stream)
@@ -191,3 +203,122 @@ class MLP:
                        threshold: float = DENSITY_THRESHOLD) -> Calibration:
         """The per-module rule on W2's calibration rows (glue_rows)."""
         return calibrate(torch, self.glue_rows(torch, Xcal, stream), self.F, G, m, stream, threshold)
+
+
+# ------------------------------------------------------------------ the rest of the block
+
+
+def rope_table(torch, P: int, D: int, theta: float, device):
+    """fp32 [P, D]: D/2 cosines and D/2 sines of each position's angles p * theta^(-2i/D), taken in
+    64 bits (at position 10^5 a 32-bit angle is off by 2^-8 already)."""
+    i = torch.arange(D // 2, dtype=torch.float64, device=device)
+    angle = torch.arange(P, dtype=torch.float64, device=device)[:, None] * theta ** (-2.0 * i / D)[None, :]
+    return torch.cat([angle.cos(), angle.sin()], 1).float().contiguous()
+
+
+class Pages:
+    """The page tables of R requests, shared by all layers: NP pages of ``page`` tokens, at most MB
+    pages a request, steps of at most T new tokens.  One step: set ``new`` (int32 [R], device), call
+    ``plan``, run the blocks, call ``advance``.  All three are captureable in a graph."""
+
+    def __init__(self, torch, R: int, NP: int, page: int, MB: int, T: int, device):
+        self.torch, self.R, self.NP, self.page, self.MB, self.T = torch, R, NP, page, MB, T
+        i32 = lambda *n: torch.zeros(n, dtype=torch.int32, device=device)
+        self.ctx, self.new, self.kv, self.cu = i32(R), i32(R), i32(R), i32(R + 1)
+        self.slot, self.pos, self.used, self.head = i32(T), i32(T), i32(1), i32(1)
+        self.table = torch.full((R, MB), -1, dtype=torch.int32, device=device)
+        self.free = torch.arange(NP, dtype=torch.int32, device=device)
+
+    def plan(self, stream=None) -> None:
+        osc_page_plan(self.ctx, self.new, self.R, self.page, self.NP, self.free, self.free.numel(), self.head, self.T, self.table,
+                      self.MB, self.cu, self.kv, self.slot, self.pos, self.used, stream)
+
+    def advance(self) -> None:
+        """The step's tokens are in the cache now (on torch's current stream)."""
+        self.ctx.add_(self.new)
+        self.head.add_(self.used)
+
+    def release(self, rows) -> None:
+        """The pages of the finished requests ``rows`` go back to the free list and their rows become
+        empty.  Waits for the device; not inside a captured graph."""
+        t = self.torch
+        rows = [int(r) for r in rows]
+        if len(set(rows)) != len(rows) or any(not 0 <= r < self.R for r in rows):
+            raise ValueError("rows are distinct requests of this table")
+        ctx, head = self.ctx.tolist(), int(self.head)
+        back = [self.table[r, :-(-ctx[r] // self.page)] for r in rows]
+        left = t.cat([self.free[head:], *[b[b >= 0] for b in back]])
+        # the list keeps its address and length (a captured plan reads them): the pages in use stand first
+        used = self.free.numel() - left.numel()
+        self.free[used:] = left
+        self.free[:used] = -1
+        self.head.fill_(used)
+        at = t.tensor(rows, dtype=t.long, device=self.ctx.device)
+        self.table[at] = -1
+        self.ctx[at] = 0
+
+
+class LayerCache:
+    """One layer's keys and values: KC [NP, HKV, page, D] and VC [NP, HKV, D, page] bf16."""
+
+    def __init__(self, torch, pages: Pages, HKV: int, D: int, device):
+        self.KC = torch.zeros((pages.NP, HKV, pages.page, D), dtype=torch.bfloat16, device=device)
+        self.VC = torch.zeros((pages.NP, HKV, D, pages.page), dtype=torch.bfloat16, device=device)
+
+
+class Attention:
+    """QKV projection -> head norms, rotary embedding, cache write -> attention over the paged cache
+    -> output projection.  qkv: [(HQ + 2 HKV) D, H], out: [H, HQ D]; wq, wk: [D] bf16 head norm weights
+    or None; cs: rope_table or None."""
+
+    def __init__(self, qkv: Linear, out: Linear, HQ: int, HKV: int, D: int, wq=None, wk=None, cs=None, eps: float = 1e-6):
+        if qkv.N != (HQ + 2 * HKV) * D or out.H != HQ * D:
+            raise ValueError("the projections do not have these heads")
+        self.qkv, self.out, self.HQ, self.HKV, self.D = qkv, out, HQ, HKV, D
+        self.wq, self.wk, self.cs, self.eps = wq, wk, cs, eps
+        self.scale = D ** -0.5
+
+    def buffers(self, S: int, pages: Pages, device):
+        t = self.qkv.torch
+        bf = lambda *n: t.zeros(n, dtype=t.bfloat16, device=device)  # padding rows stay finite through the output projection
+        ws = osc_attn_workspace(S, pages.R, self.HQ, self.HKV, self.D, pages.page, pages.MB)
+        return {"x": self.qkv.act_buffers(S, device), "qkv": bf(S, self.qkv.N), "q": bf(S, self.HQ, self.D), "o": bf(S, self.HQ, self.D),
+                "ws": t.empty((ws,), dtype=t.uint8, device=device), "ox": self.out.act_buffers(S, device)}
+
+    def forward_quantized(self, S: int, pages: Pages, cache: LayerCache, bufs, Y, stream=None) -> None:
+        """From the QKV projection's quantized input in bufs["x"], by the plan in ``pages``."""
+        if S > pages.T:
+            raise ValueError(f"{S} rows, and a plan of {pages.T}")
+        self.qkv.gemm(bufs["x"], S, bufs["qkv"], OSC_Y_BF16, stream)
+        osc_qkv_append(bufs["qkv"], S, self.HQ, self.HKV, self.D, self.wq, self.wk, self.eps, self.cs,
+                       0 if self.cs is None else self.cs.shape[0], pages.pos, pages.slot, bufs["q"], cache.KC, cache.VC, pages.NP,
+                       pages.page, stream)
+        osc_attn_paged(bufs["q"], cache.KC, cache.VC, S, pages.R, self.HQ, self.HKV, self.D, pages.page, pages.MB, pages.NP, pages.table,
+                       pages.cu, pages.kv, self.scale, bufs["o"], bufs["ws"], stream)
+        self.out.forward(bufs["o"], S, bufs["ox"], Y, OSC_Y_BF16, stream)
+
+
+class Block:
+    """One pre-norm transformer block on the residual stream: stream += x; attention(norm(stream));
+    stream += that; MLP(norm(stream)), whose output is the next block's x."""
+
+    def __init__(self, attention: Attention, mlp: MLP, w_attn, w_mlp, eps: float = 1e-6):
+        if attention.out.N != mlp.up.H or attention.qkv.H != mlp.up.H or mlp.down.N != mlp.up.H:
+            raise ValueError("the projections do not share the residual stream's width")
+        self.attention, self.mlp, self.w_attn, self.w_mlp, self.eps = attention, mlp, w_attn, w_mlp, eps
+
+    def buffers(self, S: int, pages: Pages, device):
+        t = self.mlp.up.torch
+        return {"attn": self.attention.buffers(S, pages, device), "mlp": self.mlp.buffers(S, device),
+                "y": t.empty((S, self.mlp.up.H), dtype=t.bfloat16, device=device)}
+
+    def forward(self, X, res, S: int, pages: Pages, cache: LayerCache, bufs, Y, stream=None):
+        """X: [S, H] bf16, the block before's Y; res: the residual stream, updated in place.  The first
+        block takes res = None: X is the stream then, and is updated in place.  Writes the MLP's
+        output to Y (not X) and returns the stream."""
+        self.attention.qkv.norm_quantize(X, res, self.w_attn, self.eps, S, bufs["attn"]["x"], stream)
+        stream_rows = X if res is None else res
+        self.attention.forward_quantized(S, pages, cache, bufs["attn"], bufs["y"], stream)
+        self.mlp.up.norm_quantize(bufs["y"], stream_rows, self.w_mlp, self.eps, S, bufs["mlp"]["x"], stream)
+        self.mlp.forward_quantized(S, bufs["mlp"], Y, OSC_Y_BF16, stream)
+        return stream_rows
