@@ -124,7 +124,7 @@ def test_attn_workspace():
     assert ws(S=0) == (0, 0) and ws(R=0) == (0, 0)
     assert ws(S=8192, R=1, HQ=32, HKV=8, page=64, MB=128) == (0, 0)    # tiles enough: no split
     st, need = ws(S=1, R=1, HQ=32, HKV=8, page=64, MB=128)             # one token over a long table: split
-    assert st == 0 and need > 0 and need % (32 * 130 * 4) == 0
+    assert st == 0 and need >= 2 * 32 * 130 * 4
     big = dict(S=1, R=1, HQ=32, HKV=8, page=64, MB=128)
     assert attn(**big, WS=None) == 1 and attn(**big, n=need - 1) == 2 and attn(**big, n=-1) == 2
 

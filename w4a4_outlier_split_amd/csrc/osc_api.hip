@@ -378,10 +378,14 @@ osc_status osc_attn_paged(const void* Q, const void* KC, const void* VC, int S, 
   if (!aligned16(Q) || !aligned16(KC) || !aligned16(VC) || !aligned16(O) || !aligned16(WS) || !aligned4(TABLE) ||
       !aligned4(CU) || !aligned4(KV))
     return OSC_E_ALIGN;
-  float* ws = static_cast<float*>(WS);
-  osc::AttnArgs a{Q,  KC, VC, S, R, HQ, HKV, HQ / HKV, sh, page - 1, MB, NP, TABLE, CU, KV, scale * 1.4426950408889634f,
-                  O,  ws, ws ? ws + (long)p.nsplit * S * HQ * D : nullptr, p.large_tiles, p.nsplit};
-  return from_hip(osc::launch_attn(a, D, static_cast<hipStream_t>(stream)));
+  osc::AttnArgs a{Q,  KC,   VC, S,  R,  HQ, HKV, HQ / HKV, sh, page - 1, MB, NP, TABLE, CU, KV, scale * 1.4426950408889634f,
+                  O,  nullptr, nullptr, nullptr, p.cap, p.target};
+  if (p.cap > 1) {
+    a.PO = static_cast<float*>(WS);
+    a.PM = a.PO + (long)p.cap * S * HQ * D;
+    a.CNT = reinterpret_cast<int32_t*>(a.PM + (long)p.cap * S * HQ * 2);
+  }
+  return from_hip(osc::launch_attn(a, D, p.units, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -21,8 +21,10 @@
 //     four wavefronts take 32 keys each in turn and are merged at the end.  HBM-bound.
 //   large: 128 rows, four wavefronts of 32 rows each; 64 keys of K and V^T at a time in LDS, loaded
 //     by LDS-DMA while the previous 64 are worked on.  Bound by the matrix and vector units.
-// With few tiles the keys are cut into nsplit ranges whose unnormalised outputs go to the workspace
-// and are joined by a second launch in a fixed order.
+// With few tiles the keys are cut into ranges whose unnormalised outputs go to the workspace and are
+// joined by a second launch in a fixed order.  The lengths are on the device, so the cut is made there:
+// every workgroup adds up the step's work, from which follow the steps of 64 keys that one unit of
+// work takes, each request's number of ranges, and the unit that is the workgroup's own.
 #include "osc_device.h"
 #include "osc_internal.h"
 
@@ -34,6 +36,9 @@ typedef __bf16 v4bf __attribute__((ext_vector_type(4)));
 
 constexpr int kSmallRows = 32;
 constexpr int kLargeRows = 128;
+constexpr int kSlots = 512;     // workgroups that run at once: two on each of 256 CUs
+constexpr int kMaxSplit = 64;   // ranges of a request's keys (the join's lanes)
+constexpr int kMinSteps = 4;    // 64-key steps that a range has at least
 // the running maximum is left as it is while no score exceeds it by more than 2^kSlack (in the
 // exponent of 2): P is then at most 2^kSlack, which binary32 sums and bf16's exponent take as well
 constexpr float kSlack = 8.0f;
@@ -42,6 +47,7 @@ __device__ __forceinline__ float neg_inf() { return -__builtin_inff(); }
 
 struct Tile {
   int row0, rows;  // the tile's rows (token, head of the group): first and end, inside the request
+  int split, ns;   // which of the request's ranges of keys
   int tok0, n;     // the request's first token and token count
   int kv;          // keys of the request
   const int32_t* pages;
@@ -88,7 +94,7 @@ __device__ __forceinline__ float max_groups(float v) {
 
 // ------------------------------------------------------------------ small tiles
 template <int D>
-__device__ __forceinline__ void small_tile(const AttnArgs& a, const Tile& t, int h, int split, float* lds) {
+__device__ __forceinline__ void small_tile(const AttnArgs& a, const Tile& t, int h, float* lds) {
   constexpr int DK = D / 32, DB = D / 16;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int col = lane & 15, grp = lane >> 4;
@@ -110,7 +116,7 @@ __device__ __forceinline__ void small_tile(const AttnArgs& a, const Tile& t, int
   const int tok_end = ((t.row0 + 16 < t.rows ? t.row0 + 16 : t.rows) - 1) / g;
   const int kend = clampi(t.kv - t.n + tok_end + 1, 0, t.kv);
   const int steps = (kend + 31) >> 5;
-  const int lo = (int)((long)steps * split / a.nsplit), hi = (int)((long)steps * (split + 1) / a.nsplit);
+  const int lo = (int)((long)steps * t.split / t.ns), hi = (int)((long)steps * (t.split + 1) / t.ns);
 
   v4f o[DB];
 #pragma unroll
@@ -211,7 +217,8 @@ __device__ __forceinline__ void small_tile(const AttnArgs& a, const Tile& t, int
   if (r >= t.rows) return;
   const int tk = r / g;
   const long at = (long)(t.tok0 + tk) * a.HQ + h * g + (r - tk * g);
-  if (a.nsplit == 1) {
+  if (a.CNT && t.split == 0 && d0 == 0) a.CNT[at] = t.ns;
+  if (t.ns == 1) {
     const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;  // no key: zeros
 #pragma unroll
     for (int i = 0; i < PT; i += 4) {
@@ -224,8 +231,8 @@ __device__ __forceinline__ void small_tile(const AttnArgs& a, const Tile& t, int
     const long rows = (long)a.S * a.HQ;
 #pragma unroll
     for (int i = 0; i < PT; i += 4)
-      *reinterpret_cast<v4f*>(a.PO + ((long)split * rows + at) * D + d0 + i) = v4f{acc[i], acc[i + 1], acc[i + 2], acc[i + 3]};
-    if (d0 == 0) *reinterpret_cast<float2*>(a.PM + ((long)split * rows + at) * 2) = float2{ms * c, ll};
+      *reinterpret_cast<v4f*>(a.PO + (t.split * rows + at) * D + d0 + i) = v4f{acc[i], acc[i + 1], acc[i + 2], acc[i + 3]};
+    if (d0 == 0) *reinterpret_cast<float2*>(a.PM + (t.split * rows + at) * 2) = float2{ms * c, ll};
   }
 }
 
@@ -263,7 +270,7 @@ __device__ __forceinline__ void load_kv(const AttnArgs& a, const Tile& t, int h,
 }
 
 template <int D>
-__device__ __forceinline__ void large_tile(const AttnArgs& a, const Tile& t, int h, int split, uint8_t* lds) {
+__device__ __forceinline__ void large_tile(const AttnArgs& a, const Tile& t, int h, uint8_t* lds) {
   constexpr int DK = D / 16, DB = D / 32, CH = D / 8;
   constexpr int BUF = 64 * D * 4;
   const int lane = threadIdx.x & 63;
@@ -288,7 +295,7 @@ __device__ __forceinline__ void large_tile(const AttnArgs& a, const Tile& t, int
   // the first row of the wavefront sees the fewest keys: tiles up to it need no mask
   const int wfirst = base + (t.row0 + wave * 32) / g;
   const int steps = (kend + 63) >> 6;
-  const int lo = (int)((long)steps * split / a.nsplit), hi = (int)((long)steps * (split + 1) / a.nsplit);
+  const int lo = (int)((long)steps * t.split / t.ns), hi = (int)((long)steps * (t.split + 1) / t.ns);
 
   v16f o[DB];
 #pragma unroll
@@ -385,7 +392,8 @@ __device__ __forceinline__ void large_tile(const AttnArgs& a, const Tile& t, int
   }
   l += __shfl_xor(l, 32);
   if (!live) return;
-  if (a.nsplit == 1) {
+  if (a.CNT && t.split == 0 && half == 0) a.CNT[out_row] = t.ns;
+  if (t.ns == 1) {
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // no key: zeros
     __bf16* out = static_cast<__bf16*>(a.O) + out_row * D;
 #pragma unroll
@@ -398,7 +406,7 @@ __device__ __forceinline__ void large_tile(const AttnArgs& a, const Tile& t, int
         *reinterpret_cast<v4bf*>(out + d * 32 + 8 * i + 4 * half) = b;
       }
   } else {
-    const long at = (long)split * a.S * a.HQ + out_row;
+    const long at = (long)t.split * a.S * a.HQ + out_row;
     float* out = a.PO + at * D;
 #pragma unroll
     for (int d = 0; d < DB; ++d)
@@ -410,132 +418,182 @@ __device__ __forceinline__ void large_tile(const AttnArgs& a, const Tile& t, int
   }
 }
 
-// Workgroups: first the large tiles (the later rows of a request first, they see the most keys), then
-// two small tiles a request; key heads fastest (an XCD takes every eighth workgroup, so with eight key
-// heads each XCD's L2 holds one head's cache), then the splits.
+// A request's tiles, and the 64-key steps that each takes (a step's cost is about the same for both
+// shapes: the small one waits for memory, the large one works).
+__device__ __forceinline__ void shape(const AttnArgs& a, int r, int& tiles, int& steps) {
+  const int c0 = clampi(a.CU[r], 0, a.S), c1 = clampi(a.CU[r + 1], 0, a.S);
+  const int rows = (c1 > c0 ? c1 - c0 : 0) * a.g;
+  tiles = rows > kSmallRows ? (rows + kLargeRows - 1) / kLargeRows : (rows + 15) >> 4;
+  steps = (clampi(a.KV[r], 0, (int)((long)a.MB << a.sh)) + 63) >> 6;
+}
+
+// Workgroups: key heads fastest (an XCD takes every eighth workgroup, so with eight key heads each XCD's
+// L2 holds one head's cache), then units of work: requests in order, a request's later tiles first (they
+// see the most keys), a tile's ranges of keys in order.  Every wavefront finds the unit by itself, its
+// lanes a share of the requests each.
 template <int D>
 __global__ __launch_bounds__(256, 2) void k_attn(AttnArgs a) {
   __shared__ __align__(16) uint8_t lds[64 * D * 8 > 128 * 4 + 4 * 16 * (D + 4) * 4 ? 64 * D * 8 : 128 * 4 + 4 * 16 * (D + 4) * 4];
-  const int b = blockIdx.x;
-  const int h = b % a.HKV;
-  const int x = b / a.HKV;
-  const int split = x % a.nsplit;
-  int tile = x / a.nsplit;
-  Tile t;
-  if (tile >= a.large_tiles) {
-    tile -= a.large_tiles;
-    request(a, tile >> 1, t);
-    t.row0 = (tile & 1) * 16;
-    t.rows = t.n * a.g;
-    if (t.row0 >= t.rows || t.rows > kSmallRows) return;
-    small_tile<D>(a, t, h, split, reinterpret_cast<float*>(lds));
-    return;
-  }
-  // the large tile's request: tiles of the requests before it, 256 requests at a time
-  tile = a.large_tiles - 1 - tile;
-  int* found = reinterpret_cast<int*>(lds);  // [0..3] wavefront totals, [4] request, [5] tile in it
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  int hit = -1, in = 0;
-  for (int r0 = 0; r0 < a.R; r0 += 256) {
-    const int r = r0 + threadIdx.x;
-    int tiles = 0;
-    if (r < a.R) {
-      const int c0 = clampi(a.CU[r], 0, a.S), c1 = clampi(a.CU[r + 1], 0, a.S);
-      const int rows = (c1 > c0 ? c1 - c0 : 0) * a.g;
-      tiles = rows > kSmallRows ? (rows + kLargeRows - 1) / kLargeRows : 0;
+  const int h = blockIdx.x % a.HKV;
+  const int unit = blockIdx.x / a.HKV;
+  const int lane = threadIdx.x & 63;
+  const int per = (a.R + 63) >> 6;
+  const int r0 = lane * per, r1 = r0 + per < a.R ? r0 + per : a.R;
+  int tiles, steps;
+  int chunk = 0x7FFFFFFF;  // steps of a unit
+  if (a.cap > 1) {
+    long sum = 0;
+    for (int r = r0; r < r1; ++r) {
+      shape(a, r, tiles, steps);
+      sum += (long)tiles * steps;
     }
-    int sum = tiles;
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int up = __shfl_up(sum, d);
-      if (lane >= d) sum += up;
-    }
-    if (lane == 63) found[wave] = sum;
-    if (threadIdx.x == 0) found[4] = -1;
-    __syncthreads();
-    int before = sum - tiles;
-    for (int w = 0; w < wave; ++w) before += found[w];
-    if (tile >= before && tile < before + tiles) found[4] = r, found[5] = tile - before;
-    __syncthreads();
-    hit = found[4], in = found[5];
-    const int total = found[0] + found[1] + found[2] + found[3];
-    __syncthreads();
-    if (hit >= 0) break;
-    tile -= total;
+    for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
+    const long want = (sum + a.target - 1) / a.target;
+    chunk = want < kMinSteps ? kMinSteps : want < chunk ? (int)want : chunk;
   }
-  if (hit < 0) return;
-  request(a, __builtin_amdgcn_readfirstlane(hit), t);
-  t.row0 = __builtin_amdgcn_readfirstlane(in) * kLargeRows;
+  auto ranges = [&](int st) {  // of a request of st steps
+    const int n = a.cap > 1 ? (int)(((long)st + chunk - 1) / chunk) : 1;
+    return n < 1 ? 1 : n < a.cap ? n : a.cap;
+  };
+  int units = 0;
+  for (int r = r0; r < r1; ++r) {
+    shape(a, r, tiles, steps);
+    units += tiles * ranges(steps);
+  }
+  int upto = units;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int up = __shfl_up(upto, d);
+    if (lane >= d) upto += up;
+  }
+  const unsigned long long mine = __ballot(unit >= upto - units && unit < upto);
+  if (mine == 0) return;  // no such unit: the grid is an upper bound
+  int in = unit - (upto - units), hit = r0, ns = 1, nt = 0;
+  for (int r = r0; r < r1; ++r) {
+    shape(a, r, tiles, steps);
+    const int n = ranges(steps);
+    hit = r, ns = n, nt = tiles;
+    if (in < tiles * n) break;
+    in -= tiles * n;
+  }
+  const int src = __ffsll(mine) - 1;
+  hit = __builtin_amdgcn_readlane(hit, src);
+  in = __builtin_amdgcn_readlane(in, src);
+  ns = __builtin_amdgcn_readlane(ns, src);
+  nt = __builtin_amdgcn_readlane(nt, src);
+  Tile t;
+  request(a, hit, t);
   t.rows = t.n * a.g;
-  large_tile<D>(a, t, h, split, lds);
+  t.ns = ns;
+  t.split = in % ns;
+  const int tile = nt - 1 - in / ns;
+  if (t.rows <= kSmallRows) {
+    t.row0 = tile * 16;
+    small_tile<D>(a, t, h, reinterpret_cast<float*>(lds));
+  } else {
+    t.row0 = tile * kLargeRows;
+    large_tile<D>(a, t, h, lds);
+  }
 }
 
-// Joins the splits of each row of a request's tokens: D / 4 lanes a row, four values each, the splits
-// in order.  HBM-bound on the partial outputs.
-template <int D>
+// Joins the ranges of each row that was cut: WPR wavefronts a row, D / 64 values a lane, lane s holding
+// range s's maximum and sum; the ranges are added in an order that their number alone fixes.
+// HBM-bound on the partial outputs; with few rows four wavefronts share one, to have its loads in flight at once.
+template <int D, int WPR>
 __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
-  constexpr int LR = D / 4;
-  const long row = (long)blockIdx.x * (256 / LR) + threadIdx.x / LR;
-  const int d = (threadIdx.x % LR) * 4;
+  constexpr int E = D / 64;
+  typedef float vE __attribute__((ext_vector_type(E)));
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const long row = (long)blockIdx.x * (4 / WPR) + wave / WPR;
+  const int part = wave % WPR;
   const long first = (long)clampi(a.CU[0], 0, a.S) * a.HQ, end = (long)clampi(a.CU[a.R], 0, a.S) * a.HQ;
   if (row < first || row >= end) return;
+  const int ns = __builtin_amdgcn_readfirstlane(clampi(a.CNT[row], 1, a.cap));
+  if (ns == 1) return;  // written by its tile
   const long rows = (long)a.S * a.HQ;
-  float m = neg_inf();
-  for (int s = 0; s < a.nsplit; ++s) {
-    const float2 ml = *reinterpret_cast<const float2*>(a.PM + (s * rows + row) * 2);
-    if (ml.y != 0.0f) m = fmaxf(m, ml.x);
-  }
-  float l = 0.0f;
-  v4f acc = {0, 0, 0, 0};
-  for (int s = 0; s < a.nsplit; ++s) {
-    const float2 ml = *reinterpret_cast<const float2*>(a.PM + (s * rows + row) * 2);
-    if (ml.y != 0.0f) {
-      const float f = __builtin_amdgcn_exp2f(ml.x - m);
-      l += f * ml.y;
-      acc += *reinterpret_cast<const v4f*>(a.PO + (s * rows + row) * D + d) * f;
+  float2 ml = {0.0f, 0.0f};
+  if (lane < ns) ml = *reinterpret_cast<const float2*>(a.PM + (lane * rows + row) * 2);
+  const bool any = ml.y != 0.0f;  // a range of no keys has a sum of 0 and no output
+  float m = any ? ml.x : neg_inf();
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
+  const float f = any ? __builtin_amdgcn_exp2f(ml.x - m) : 0.0f;
+  float l = f * ml.y;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) l += __shfl_xor(l, d);
+  const int s0 = ns * part / WPR, s1 = ns * (part + 1) / WPR;
+  const float* src = a.PO + row * D + lane * E;
+  vE acc = {};
+  for (int s = s0; s < s1; s += 8) {
+    vE v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int x = s + i < s1 ? s + i : s1 - 1;
+      v[i] = *reinterpret_cast<const vE*>(src + x * rows * D);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float w = s + i < s1 ? __shfl(f, s + i) : 0.0f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] += w != 0.0f ? v[i][e] * w : 0.0f;
     }
   }
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  v4bf o;
+  if constexpr (WPR > 1) {
+    __shared__ vE half[WPR][64];
+    half[part][lane] = acc;
+    __syncthreads();  // the wavefronts of a workgroup share the row: all are here or none
+    if (part != 0) return;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) o[j] = (__bf16)(acc[j] * inv);
-  *reinterpret_cast<v4bf*>(static_cast<__bf16*>(a.O) + row * D + d) = o;
+    for (int p = 1; p < WPR; ++p) acc += half[p][lane];
+  }
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  __bf16* out = static_cast<__bf16*>(a.O) + row * D + lane * E;
+#pragma unroll
+  for (int e = 0; e < E; ++e) out[e] = (__bf16)(acc[e] * inv);
 }
 
 }  // namespace
 
-// Tiles and splits of a call.  Large tiles: a request has n g / 128 of them rounded up, and only
-// requests of more than kSmallRows rows have any, so S g / 128 and S g / 33 more are enough.
+// Units and ranges of a call.  A request of more than kSmallRows rows has rows / 128 large tiles rounded
+// up, any other two small ones at most; the units are at most one more for each tile than the work
+// divided by a unit's (osc_attn.hip's kernel takes at least work / target steps for a unit).
 AttnPlan attn_plan(int S, int R, int HQ, int HKV, int D, int page, int MB) {
   const long rows = (long)S * (HQ / HKV);
   const long big = rows / (kSmallRows + 1);
+  const long large = big > 0 ? rows / kLargeRows + (big < R ? big : R) : 0;
+  const long few = rows / 16 + R < 2l * R ? rows / 16 + R : 2l * R;
+  const long tiles = large + few;
+  // tiles that are expected to work: all rows in 128-row tiles, or one small tile a request
+  const long busy = (rows / R > kSmallRows ? (rows + kLargeRows - 1) / kLargeRows : R) * HKV;
   AttnPlan p;
-  p.large_tiles = big > 0 ? (int)(rows / kLargeRows + (big < R ? big : R)) : 0;
-  // the workgroups that are expected to work: all rows in 128-row tiles, or one small tile a request
-  const long avg = rows / R;
-  const long wg = (avg > kSmallRows ? (rows + kLargeRows - 1) / kLargeRows : R) * HKV;
-  const long keys = (long)MB * page;
-  long n = (1024 + wg - 1) / wg;
-  const long most = (keys + 255) / 256;  // at least 256 keys a split, were a request's table full
-  if (n > most) n = most;
-  if (n > 64) n = 64;
-  if (n < 1) n = 1;
-  p.nsplit = (int)n;
-  p.ws_bytes = n > 1 ? n * S * HQ * (long)(D + 2) * 4 : 0;
+  const long steps = ((long)MB * page + 63) / 64;
+  long cap = steps / kMinSteps;  // were a request's table full
+  if (cap > kMaxSplit) cap = kMaxSplit;
+  if (busy >= 4 * kSlots || cap < 1) cap = 1;
+  p.cap = (int)cap;
+  p.target = (kSlots + HKV - 1) / HKV;
+  p.units = cap == 1 ? tiles : tiles * cap < p.target + tiles ? tiles * cap : p.target + tiles;
+  p.ws_bytes = cap > 1 ? cap * S * HQ * (long)(D + 2) * 4 + (long)S * HQ * 4 : 0;
   return p;
 }
 
-hipError_t launch_attn(const AttnArgs& a, int D, hipStream_t st) {
-  const long grid = ((long)a.large_tiles + 2l * a.R) * a.nsplit * a.HKV;
+hipError_t launch_attn(const AttnArgs& a, int D, long units, hipStream_t st) {
+  const long grid = units * a.HKV;
   if (grid > 0x7FFFFFFFL) return hipErrorInvalidValue;
   if (D == 128) hipLaunchKernelGGL(k_attn<128>, dim3((unsigned)grid), dim3(256), 0, st, a);
   else hipLaunchKernelGGL(k_attn<64>, dim3((unsigned)grid), dim3(256), 0, st, a);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess || a.nsplit == 1) return e;
-  const int rb = 256 / (D / 4);
-  const unsigned jg = (unsigned)(((long)a.S * a.HQ + rb - 1) / rb);
-  if (D == 128) hipLaunchKernelGGL(k_attn_join<128>, dim3(jg), dim3(256), 0, st, a);
-  else hipLaunchKernelGGL(k_attn_join<64>, dim3(jg), dim3(256), 0, st, a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.cap == 1) return e;
+  const long rows = (long)a.S * a.HQ;
+  if (rows <= 4096) {
+    if (D == 128) hipLaunchKernelGGL((k_attn_join<128, 4>), dim3((unsigned)rows), dim3(256), 0, st, a);
+    else hipLaunchKernelGGL((k_attn_join<64, 4>), dim3((unsigned)rows), dim3(256), 0, st, a);
+  } else {
+    const unsigned jg = (unsigned)((rows + 3) / 4);
+    if (D == 128) hipLaunchKernelGGL((k_attn_join<128, 1>), dim3(jg), dim3(256), 0, st, a);
+    else hipLaunchKernelGGL((k_attn_join<64, 1>), dim3(jg), dim3(256), 0, st, a);
+  }
   return hipGetLastError();
 }
 

@@ -129,8 +129,9 @@ hipError_t launch_qkv_append(const AppendArgs& a, hipStream_t st);
 
 // Attention over the paged cache (osc_attn_paged).
 struct AttnPlan {
-  int large_tiles;  // upper bound on the 128-row tiles of one key head
-  int nsplit;       // ranges the keys of a tile are cut into
+  int cap;     // most ranges that a request's keys are cut into
+  int target;  // units of work wanted for each key head
+  long units;  // upper bound on them
   long ws_bytes;
 };
 AttnPlan attn_plan(int S, int R, int HQ, int HKV, int D, int page, int MB);
@@ -141,9 +142,11 @@ struct AttnArgs {
   const int32_t *TABLE, *CU, *KV;
   float scale_log2;  // scale * log2(e)
   void* O;
-  float *PO, *PM;  // [nsplit][S*HQ][D] unnormalised outputs, [nsplit][S*HQ][2] scaled maximum and sum
-  int large_tiles, nsplit;
+  // with cap > 1: [cap][S*HQ][D] unnormalised outputs, [cap][S*HQ][2] scaled maximum and sum, [S*HQ] ranges of a row
+  float *PO, *PM;
+  int32_t* CNT;
+  int cap, target;
 };
-hipError_t launch_attn(const AttnArgs& a, int D, hipStream_t st);
+hipError_t launch_attn(const AttnArgs& a, int D, long units, hipStream_t st);
 
 }  // namespace osc
