@@ -105,7 +105,7 @@ def attn(Q=A, KC=A, VC=A, S=4, R=2, HQ=4, HKV=2, D=128, page=16, MB=4, NP=8, T=A
 def test_attn_refusals():
     for f in (lambda **k: ws(**k)[0], attn):
         assert f(page=20) == 2 and f(S=-1) == 2 and f(S=1 << 24) == 2 and f(R=-1) == 2 and f(R=4097) == 2 and f(MB=0) == 2
-        assert f(HQ=5) == 2 and f(HQ=0) == 2 and f(HKV=0) == 2 and f(D=32) == 2 and f(MB=1 << 27) == 2
+        assert f(HQ=5) == 2 and f(HQ=0) == 2 and f(HKV=0) == 2 and f(D=32) == 2 and f(MB=(1 << 26) + 1) == 2
         assert f(S=(1 << 24) - 1, HQ=16) == 2
     assert call("osc_attn_workspace", 4, 2, 4, 2, 128, 16, 4, None) == 1
     assert attn(NP=0) == 2 and attn(NP=1 << 27) == 2

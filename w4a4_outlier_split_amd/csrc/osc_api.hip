@@ -351,7 +351,7 @@ static osc_status check_attn(int S, int R, int HQ, int HKV, int D, int page, int
   const int sh = page_shift(page);
   if (sh < 0 || S < 0 || S >= (1 << 24) || R < 0 || R > OSC_MAX_REQUESTS || MB < 1) return OSC_E_SHAPE;
   if (!valid_heads(HQ, HKV, D) || HQ % HKV != 0) return OSC_E_SHAPE;
-  if ((long long)S * HQ * D >= (1LL << 34) || ((long long)MB << sh) > 0x7FFFFFFFLL) return OSC_E_SHAPE;
+  if ((long long)S * HQ * D >= (1LL << 34) || ((long long)MB << sh) > (1LL << 30)) return OSC_E_SHAPE;
   return OSC_OK;
 }
 

@@ -123,9 +123,12 @@ __device__ __forceinline__ void small_tile(const AttnArgs& a, const Tile& t, int
   for (int d = 0; d < DB; ++d) o[d] = v4f{0, 0, 0, 0};
   float m = neg_inf(), mc = 0.0f, l = 0.0f;
   const float c = a.scale_log2;
-  for (int st = lo + wave; st < hi; st += 4) {
+  // the pages of the wavefront's next 32 steps, a run of 16 keys a lane (a page holds at least one)
+  int ids = 0;
+  for (int st = lo + wave, n = 0; st < hi; st += 4, ++n) {
     const int k0 = st * 32;
-    const int id0 = page_of(a, t, k0), id1 = page_of(a, t, k0 + 16);  // a page holds at least 16 keys
+    if ((n & 31) == 0) ids = page_of(a, t, k0 + (lane >> 1) * 128 + (lane & 1) * 16);
+    const int id0 = __builtin_amdgcn_readlane(ids, 2 * (n & 31)), id1 = __builtin_amdgcn_readlane(ids, 2 * (n & 31) + 1);
     const bool whole = k0 + 32 <= t.kv && id0 >= 0 && id1 >= 0;
     const int idl = (grp & 2) ? id1 : id0;  // V's keys 8 * grp ..
     const int u = k0 + (grp & 2) * 8;
@@ -241,11 +244,10 @@ __device__ __forceinline__ void small_tile(const AttnArgs& a, const Tile& t, int
 // pieces at position piece ^ (row & (D/8 - 1)), V^T rows their two halves at half ^ (d >> 3 & 1): the
 // 16 lanes that LDS serves together then read 16 different 16-byte columns of its 256.
 template <int D>
-__device__ __forceinline__ void load_kv(const AttnArgs& a, const Tile& t, int h, int k0, lds_u8* buf) {
+__device__ __forceinline__ void load_kv(const AttnArgs& a, int id, int h, int k0, lds_u8* buf) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int key = k0 + wave * 16;  // this wavefront's run of keys: inside one page
-  const int id = page_of(a, t, key);
+  const int key = k0 + wave * 16;  // this wavefront's run of keys: inside page id
   const long base = block_at<D>(a, id < 0 ? 0 : id, h);
   const int at = key & a.mask;
   constexpr int CH = D / 8;                 // 16-byte pieces of a K row
@@ -308,22 +310,24 @@ __device__ __forceinline__ void large_tile(const AttnArgs& a, const Tile& t, int
   // row `col` of score block x holds key 32 x + 16 (a / 2) + 8 hh + 4 (a % 2) + j, col = 8 a + 4 hh + j
   const int perm = 16 * (col >> 4) + 8 * ((col >> 2) & 1) + 4 * ((col >> 3) & 1) + (col & 3);
 
-  if (lo < hi) load_kv<D>(a, t, h, lo * 64, lb);
+  // The pages of 16 steps, a run of 16 keys a lane.  They are fetched a block of steps ahead: a load
+  // waited for here would be waited for behind the DMA that the step has just begun.
+  int ids = page_of(a, t, (lo * 4 + lane) * 16), next_ids = page_of(a, t, (lo * 4 + 64 + lane) * 16);
+  if (lo < hi) load_kv<D>(a, __builtin_amdgcn_readlane(ids, wave), h, lo * 64, lb);
   for (int st = lo; st < hi; ++st) {
     const int k0 = st * 64;
+    const int n = (st - lo) & 15;
     uint8_t* buf = lds + ((st - lo) & 1) * BUF;
+    int bad = (int)(__ballot(ids < 0) >> (n * 4)) & 15;  // runs of 16 keys without a page
+    if (k0 + 64 > t.kv) bad |= 16;
     wait_vm<0>();
     lds_barrier();  // this buffer has landed, and the other one is no longer read
-    if (st + 1 < hi) load_kv<D>(a, t, h, k0 + 64, lb + ((st - lo + 1) & 1) * BUF);
-    int bad = 0;  // runs of 16 keys without a page
-    if (k0 + 64 <= t.kv) {
-#pragma unroll
-      for (int u = 0; u < 4; ++u) bad |= (page_of(a, t, k0 + 16 * u) < 0 ? 1 : 0) << u;
-    } else {
-#pragma unroll
-      for (int u = 0; u < 4; ++u) bad |= (page_of(a, t, k0 + 16 * u) < 0 ? 1 : 0) << u;
-      bad |= 16;
+    if (n == 15) {
+      ids = next_ids;
+      next_ids = page_of(a, t, ((st + 1) * 4 + 64 + lane) * 16);
     }
+    if (st + 1 < hi)
+      load_kv<D>(a, __builtin_amdgcn_readlane(ids, ((n + 1) & 15) * 4 + wave), h, k0 + 64, lb + ((st - lo + 1) & 1) * BUF);
     if (bad) {  // V of keys that do not exist may hold anything, and 0 * NaN is not 0
       uint16_t* v = reinterpret_cast<uint16_t*>(buf + 64 * D * 2);
       for (int i = threadIdx.x; i < 64 * D; i += 256) {
