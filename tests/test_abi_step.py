@@ -122,11 +122,11 @@ def test_attn_refusals():
 
 def test_attn_workspace():
     assert ws(S=0) == (0, 0) and ws(R=0) == (0, 0)
-    assert ws(S=8192, R=1, HQ=32, HKV=8, page=64, MB=128) == (0, 0)    # tiles enough: no split
-    st, need = ws(S=1, R=1, HQ=32, HKV=8, page=64, MB=128)             # one token over a long table: split
-    assert st == 0 and need >= 2 * 32 * 130 * 4
-    big = dict(S=1, R=1, HQ=32, HKV=8, page=64, MB=128)
-    assert attn(**big, WS=None) == 1 and attn(**big, n=need - 1) == 2 and attn(**big, n=-1) == 2
+    assert ws(S=8192, R=1, HQ=32, HKV=8, page=64, MB=128) == (0, 0)  # tiles enough: none is cut
+    for sizes in (dict(S=1, R=1, HQ=32, HKV=8, page=64, MB=128), dict(S=2048, R=1, HQ=32, HKV=8, page=64, MB=128), dict(S=9, R=3, D=64)):
+        st, need = ws(**sizes)
+        assert st == 0 and 0 < need < 1 << 28  # two tiles for each workgroup, whatever the lengths
+        assert attn(**sizes, WS=None) == 1 and attn(**sizes, n=need - 1) == 2 and attn(**sizes, n=-1) == 2
 
 
 def test_a_short_table_is_refused_by_the_binding():

@@ -287,13 +287,13 @@ def test_attn_one_request(kv, n, D, page):
     check_attn(build([(kv, n)], 8, 2, D, page, kv + n))
 
 
-@pytest.mark.parametrize("MB", [8, 200])
-def test_attn_split_keys(MB):
-    """A long table makes the call split the keys, whatever the requests really hold."""
-    for reqs in ([(500, 1)], [(3, 1), (512, 1), (0, 0)], [(512, 60), (1, 1)], [(128, 128), (400, 9)]):
-        p = build(reqs, 4, 1, 128, 64, MB + len(reqs), MB=MB)
-        assert (osc.osc_attn_workspace(p["S"], p["R"], 4, 1, 128, 64, MB) > 0) == (MB * 64 > 256)
-        check_attn(p)
+@pytest.mark.parametrize("reqs", [[(5000, 1)], [(3, 1), (5012, 1), (0, 0)], [(5012, 60), (1, 1)], [(128, 128), (4000, 9)], [(20000, 1)],
+                                  [(9000, 300), (64, 64), (1, 1), (700, 0)], [(1, 1)] * 70, [(300, 1), (0, 0)] * 40, [(2000, 2000)],
+                                  [(260, 2)] * 130])
+@pytest.mark.parametrize("HQ,HKV", [(4, 1), (6, 3)])
+def test_attn_cuts(reqs, HQ, HKV):
+    """Tiles cut into many parts, parts of many tiles, idle requests in between; more key heads than 1 and not 8."""
+    check_attn(build(reqs, HQ, HKV, 64, 64, len(reqs) + HQ, MB=330))
 
 
 def test_attn_rows_that_see_nothing_are_zero():
@@ -323,7 +323,7 @@ def test_attn_rows_outside_the_requests_stay_as_they_were():
     full = poisoned((p["S"] + 6, 4, 128), torch.bfloat16)
     Q = torch.cat([torch.full((2, 4, 128), float("nan"), dtype=torch.bfloat16, device=DEV), p["Q"],
                    torch.full((4, 4, 128), float("nan"), dtype=torch.bfloat16, device=DEV)])
-    for MB in (p["MB"], 300):  # one launch, and split
+    for MB in (p["MB"], 300):
         q = dict(p, Q=Q, cu=[c + 2 for c in p["cu"]], table=[r + [-1] * (MB - len(r)) for r in p["table"]], MB=MB)
         O = attend(q, S=p["S"] + 6, O=full)
         assert bool((O[:2].view(torch.int16) == -1).all()) and bool((O[-4:].view(torch.int16) == -1).all())

@@ -359,7 +359,7 @@ osc_status osc_attn_workspace(int S, int R, int HQ, int HKV, int D, int page, in
   const osc_status st = check_attn(S, R, HQ, HKV, D, page, MB);
   if (st != OSC_OK) return st;
   if (!bytes) return OSC_E_NULL;
-  *bytes = S == 0 || R == 0 ? 0 : osc::attn_plan(S, R, HQ, HKV, D, page, MB).ws_bytes;
+  *bytes = S == 0 || R == 0 ? 0 : osc::attn_plan(S, R, HQ, HKV, D).ws_bytes;
   return OSC_OK;
 }
 
@@ -372,20 +372,21 @@ osc_status osc_attn_paged(const void* Q, const void* KC, const void* VC, int S, 
   if (NP < 1 || ((long long)NP << sh) > 0x7FFFFFFFLL || !positive(scale)) return OSC_E_SHAPE;
   if (S == 0 || R == 0) return OSC_OK;
   if (!Q || !KC || !VC || !TABLE || !CU || !KV || !O) return OSC_E_NULL;
-  const osc::AttnPlan p = osc::attn_plan(S, R, HQ, HKV, D, page, MB);
+  const osc::AttnPlan p = osc::attn_plan(S, R, HQ, HKV, D);
   if (p.ws_bytes > 0 && !WS) return OSC_E_NULL;
   if (ws_bytes < p.ws_bytes) return OSC_E_SHAPE;
   if (!aligned16(Q) || !aligned16(KC) || !aligned16(VC) || !aligned16(O) || !aligned16(WS) || !aligned4(TABLE) ||
       !aligned4(CU) || !aligned4(KV))
     return OSC_E_ALIGN;
   osc::AttnArgs a{Q,  KC,   VC, S,  R,  HQ, HKV, HQ / HKV, sh, page - 1, MB, NP, TABLE, CU, KV, scale * 1.4426950408889634f,
-                  O,  nullptr, nullptr, nullptr, p.cap, p.target};
-  if (p.cap > 1) {
-    a.PO = static_cast<float*>(WS);
-    a.PM = a.PO + (long)p.cap * S * HQ * D;
-    a.CNT = reinterpret_cast<int32_t*>(a.PM + (long)p.cap * S * HQ * 2);
+                  O,  nullptr, nullptr, nullptr, p.target};
+  if (p.ws_bytes > 0) {  // notes, then 2 and D values a row
+    const long notes = (long)HKV * p.target;
+    a.NOTE = static_cast<int4*>(WS);
+    a.PM = reinterpret_cast<float*>(a.NOTE + notes);
+    a.PO = a.PM + (p.ws_bytes - notes * (long)sizeof(int4)) / 4 / (D + 2) * 2;
   }
-  return from_hip(osc::launch_attn(a, D, p.units, static_cast<hipStream_t>(stream)));
+  return from_hip(osc::launch_attn(a, D, p, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

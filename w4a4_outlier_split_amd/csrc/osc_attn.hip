@@ -16,15 +16,17 @@
 // of the second product, with no exchange between lanes.  V^T's rows are contiguous keys in the
 // cache's V layout [page][head][D][slot].
 //
-// Two tile shapes, one launch, chosen per request by its row count n * HQ/HKV:
-//   small (at most kSmallRows): 16 rows, the cache read from memory straight into registers; the
+// Two kernels, by the call's tokens and requests:
+//   small (single tokens): tiles of 16 rows, the cache read from memory straight into registers; the
 //     four wavefronts take 32 keys each in turn and are merged at the end.  HBM-bound.
-//   large: 128 rows, four wavefronts of 32 rows each; 64 keys of K and V^T at a time in LDS, loaded
-//     by LDS-DMA while the previous 64 are worked on.  Bound by the matrix and vector units.
-// With few tiles the keys are cut into ranges whose unnormalised outputs go to the workspace and are
-// joined by a second launch in a fixed order.  The lengths are on the device, so the cut is made there:
-// every workgroup adds up the step's work, from which follow the steps of 64 keys that one unit of
-// work takes, each request's number of ranges, and the unit that is the workgroup's own.
+//   large: tiles of 256 rows, eight wavefronts of 32 rows each, one workgroup a CU; 64 keys of K and V^T at a
+//     time in a ring in LDS, loaded by LDS-DMA three tiles ahead.  Bound by what the matrix unit and the rest
+//     draw together: the card lowers its clock under this load, so what counts is work per product.
+// The work is cut evenly, whatever the lengths: all tiles of a key head stand in a row, each as long as the keys
+// that it sees, and the row is cut into as many equal parts as workgroups run at once.  A workgroup takes
+// its part, tile by tile.  A tile that a cut goes through has its unnormalised outputs left in the workspace, at
+// most two tiles for a workgroup, and a second launch joins them in a fixed order.  The lengths are on the
+// device, so each wavefront works the cuts out for itself.
 #include "osc_device.h"
 #include "osc_internal.h"
 
@@ -34,38 +36,36 @@ namespace {
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef __bf16 v4bf __attribute__((ext_vector_type(4)));
 
-constexpr int kSmallRows = 32;
-constexpr int kLargeRows = 128;
-constexpr int kSlots = 512;     // workgroups that run at once: two on each of 256 CUs
-constexpr int kMaxSplit = 64;   // ranges of a request's keys (the join's lanes)
-constexpr int kMinSteps = 4;    // 64-key steps that a range has at least
-// the running maximum is left as it is while no score exceeds it by more than 2^kSlack (in the
-// exponent of 2): P is then at most 2^kSlack, which binary32 sums and bf16's exponent take as well
-constexpr float kSlack = 8.0f;
+constexpr int kSmallRows = 16;
+constexpr int kLargeRows = 256;
+constexpr int kRing = 4;        // tiles of 64 keys in LDS
+constexpr int kCUs = 256;
+constexpr int kMaxCuts = 61;    // of one tile: its parts, two more at most, are the lanes of the join
+constexpr int kMinKeys = 256;   // that a workgroup's part has at least
+// The running maximum is left as it is while no score exceeds it by more than kSlack (in the exponent
+// of 2): P is then at most 2^kSlack, and binary32 holds sums of 2^31 of them times a bf16 value of up to
+// 2^50; neither format loses precision by the factor.
+constexpr float kSlack = 40.0f;
+
+// branches that the loops seldom take: the registers are laid out for the other side
+__device__ __forceinline__ bool rare(bool c) { return __builtin_expect(c, 0); }
 
 __device__ __forceinline__ float neg_inf() { return -__builtin_inff(); }
 
 struct Tile {
   int row0, rows;  // the tile's rows (token, head of the group): first and end, inside the request
-  int split, ns;   // which of the request's ranges of keys
   int tok0, n;     // the request's first token and token count
   int kv;          // keys of the request
   const int32_t* pages;
+  int lo, hi;      // the steps of keys to take (64 keys each)
+  long part;       // first row of the workspace for a part of a tile, -1: the whole tile
 };
 
 __device__ __forceinline__ int clampi(int v, int lo, int hi) { return v < lo ? lo : v > hi ? hi : v; }
 
-__device__ __forceinline__ void request(const AttnArgs& a, int r, Tile& t) {
-  const int c0 = clampi(a.CU[r], 0, a.S), c1 = clampi(a.CU[r + 1], 0, a.S);
-  t.tok0 = c0;
-  t.n = c1 > c0 ? c1 - c0 : 0;
-  t.kv = clampi(a.KV[r], 0, (int)((long)a.MB << a.sh));
-  t.pages = a.TABLE + (long)r * a.MB;
-}
-
 // the page of key `key`, -1 behind the request's keys or off the pool
 __device__ __forceinline__ int page_of(const AttnArgs& a, const Tile& t, int key) {
-  const int id = key < t.kv ? t.pages[key >> a.sh] : -1;
+  const int id = (unsigned)key < (unsigned)t.kv ? t.pages[key >> a.sh] : -1;
   return id >= 0 && id < a.NP ? id : -1;
 }
 
@@ -115,8 +115,7 @@ __device__ __forceinline__ void small_tile(const AttnArgs& a, const Tile& t, int
   const int last = live ? t.kv - t.n + tok : -1;  // the last key of the lane's row
   const int tok_end = ((t.row0 + 16 < t.rows ? t.row0 + 16 : t.rows) - 1) / g;
   const int kend = clampi(t.kv - t.n + tok_end + 1, 0, t.kv);
-  const int steps = (kend + 31) >> 5;
-  const int lo = (int)((long)steps * t.split / t.ns), hi = (int)((long)steps * (t.split + 1) / t.ns);
+  const int lo = 2 * t.lo, hi = clampi((kend + 31) >> 5, lo, 2 * t.hi);  // steps of 32 keys
 
   v4f o[DB];
 #pragma unroll
@@ -196,6 +195,7 @@ __device__ __forceinline__ void small_tile(const AttnArgs& a, const Tile& t, int
   // merge the wavefronts: m, l and O^T of each through LDS
   float* ml = lds;                   // [4][2][16]
   float* ob = lds + 128;             // [4][16][D + 4]
+  __syncthreads();  // the tile before is merged
   if (grp == 0) ml[wave * 32 + col] = m, ml[wave * 32 + 16 + col] = l;
 #pragma unroll
   for (int d = 0; d < DB; ++d) *reinterpret_cast<v4f*>(ob + (wave * 16 + col) * (D + 4) + 16 * d + 4 * grp) = o[d];
@@ -218,10 +218,9 @@ __device__ __forceinline__ void small_tile(const AttnArgs& a, const Tile& t, int
   }
   const int r = t.row0 + orow;
   if (r >= t.rows) return;
-  const int tk = r / g;
-  const long at = (long)(t.tok0 + tk) * a.HQ + h * g + (r - tk * g);
-  if (a.CNT && t.split == 0 && d0 == 0) a.CNT[at] = t.ns;
-  if (t.ns == 1) {
+  if (t.part < 0) {
+    const int tk = r / g;
+    const long at = (long)(t.tok0 + tk) * a.HQ + h * g + (r - tk * g);
     const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;  // no key: zeros
 #pragma unroll
     for (int i = 0; i < PT; i += 4) {
@@ -231,55 +230,57 @@ __device__ __forceinline__ void small_tile(const AttnArgs& a, const Tile& t, int
       *reinterpret_cast<v4bf*>(static_cast<__bf16*>(a.O) + at * D + d0 + i) = b;
     }
   } else {
-    const long rows = (long)a.S * a.HQ;
+    const long at = t.part + orow;
 #pragma unroll
     for (int i = 0; i < PT; i += 4)
-      *reinterpret_cast<v4f*>(a.PO + (t.split * rows + at) * D + d0 + i) = v4f{acc[i], acc[i + 1], acc[i + 2], acc[i + 3]};
-    if (d0 == 0) *reinterpret_cast<float2*>(a.PM + (t.split * rows + at) * 2) = float2{ms * c, ll};
+      *reinterpret_cast<v4f*>(a.PO + at * D + d0 + i) = v4f{acc[i], acc[i + 1], acc[i + 2], acc[i + 3]};
+    if (d0 == 0) *reinterpret_cast<float2*>(a.PM + at * 2) = float2{ms * c, ll};
   }
 }
 
 // ------------------------------------------------------------------ large tiles
-// LDS: two buffers of K [64 keys][D] and V^T [4 runs of 16 keys][D][16].  K rows hold their 16-byte
-// pieces at position piece ^ (row & (D/8 - 1)), V^T rows their two halves at half ^ (d >> 3 & 1): the
-// 16 lanes that LDS serves together then read 16 different 16-byte columns of its 256.
+// LDS: two buffers of K [64 keys][D] and two of V^T [4 runs of 16 keys][D][16].  K rows hold their
+// 16-byte pieces at position piece ^ (row & (D/8 - 1)), V^T rows their two halves at half ^ (d >> 3 & 1):
+// the 16 lanes that LDS serves together then read 16 different 16-byte columns of its 256.
+// LDS-DMA of half of one run of 16 keys, which lie in one page (block: its byte offset for the key head, K's and
+// V's alike; from slot `at`): the keys 8 part .. of K, the rows D/2 part .. of V^T.  off: the lane's place in the
+// first 1024 bytes.
 template <int D>
-__device__ __forceinline__ void load_kv(const AttnArgs& a, int id, int h, int k0, lds_u8* buf) {
+__device__ __forceinline__ int k_place() {
+  constexpr int CH = D / 8;  // 16-byte pieces of a K row
   const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int key = k0 + wave * 16;  // this wavefront's run of keys: inside page id
-  const long base = block_at<D>(a, id < 0 ? 0 : id, h);
-  const int at = key & a.mask;
-  constexpr int CH = D / 8;                 // 16-byte pieces of a K row
-  const __bf16* kb = static_cast<const __bf16*>(a.KC) + base + (long)at * D;
-  const __bf16* vb = static_cast<const __bf16*>(a.VC) + base + at;
-  lds_u8* kl = buf + wave * 16 * D * 2;
-  lds_u8* vl = buf + 64 * D * 2 + wave * D * 32;
+  return lane / CH * D * 2 + (((lane % CH) ^ (lane / CH)) << 4);
+}
+template <int D>
+__device__ __forceinline__ void load_k(const AttnArgs& a, long block, int at, int part, int off, lds_u8* buf) {
+  const auto r = panel_rsrc(static_cast<const uint8_t*>(a.KC) + block, (2l * D) << a.sh);
+  // D = 128: the row's number is 8 part + 4 i + lane / 16, and its pieces stand at position piece ^ row number
 #pragma unroll
-  for (int i = 0; i < 16 * CH / 64; ++i) {
-    const int row = i * (64 / CH) + lane / CH;
-    const int piece = (lane % CH) ^ (row & (CH - 1));
-    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(kb + row * D + piece * 8),
-                                     (__attribute__((address_space(3))) void*)(kl + i * 1024), 16, 0, 0);
-  }
+  for (int i = 0; i < D / 64; ++i)
+    dma16s(r, off ^ (D == 128 ? part * 128 + i * 64 : 0), (at + 8 * part) * D * 2 + i * 1024, buf + i * 1024);
+}
+__device__ __forceinline__ int v_place(int sh) {  // row d = lane / 2, its halves in turn
+  const int lane = threadIdx.x & 63;
+  return ((lane >> 1) << (sh + 1)) + (((lane & 1) ^ ((lane >> 4) & 1)) << 4);
+}
+template <int D>
+__device__ __forceinline__ void load_v(const AttnArgs& a, long block, int at, int part, int off, lds_u8* buf) {
+  const auto r = panel_rsrc(static_cast<const uint8_t*>(a.VC) + block, (2l * D) << a.sh);
 #pragma unroll
-  for (int i = 0; i < D / 32; ++i) {
-    const int d = i * 32 + lane / 2;
-    const int half = (lane & 1) ^ ((d >> 3) & 1);
-    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(vb + ((long)d << a.sh) + half * 8),
-                                     (__attribute__((address_space(3))) void*)(vl + i * 1024), 16, 0, 0);
-  }
+  for (int i = 0; i < D / 64; ++i)
+    dma16s(r, off, at * 2 + ((part * (D / 64) + i) << (a.sh + 6)), buf + i * 1024);
 }
 
+// Eight wavefronts, a ring of kRing tiles of 64 keys in LDS filled three tiles ahead; one barrier a tile, behind
+// which the tile before is free.
 template <int D>
 __device__ __forceinline__ void large_tile(const AttnArgs& a, const Tile& t, int h, uint8_t* lds) {
-  constexpr int DK = D / 16, DB = D / 32, CH = D / 8;
-  constexpr int BUF = 64 * D * 4;
+  constexpr int DK = D / 16, DB = D / 32, CH = D / 8, HALF = 64 * D * 2, TILE = 2 * HALF;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 31, half = lane >> 5;
   const int g = a.g;
-  const int row = t.row0 + wave * 32 + col;
+  const int row0 = t.row0 + wave * 32, row = row0 + col;
   const bool live = row < t.rows;
   const int tok = row / g;
   const long out_row = (long)(t.tok0 + tok) * a.HQ + h * g + (row - tok * g);
@@ -291,113 +292,141 @@ __device__ __forceinline__ void large_tile(const AttnArgs& a, const Tile& t, int
     if (live) q[s] = *reinterpret_cast<const v8bf*>(static_cast<const __bf16*>(a.Q) + out_row * D + s * 16 + half * 8);
   }
   const int base = t.kv - t.n;
-  const int last = live ? base + tok : -1;
-  const int tile_end = t.row0 + kLargeRows < t.rows ? t.row0 + kLargeRows : t.rows;
-  const int kend = clampi(base + (tile_end - 1) / g + 1, 0, t.kv);
+  const int last = live ? base + tok - 8 * half : -1;  // the last key the row sees, from the lane's first
   // the first row of the wavefront sees the fewest keys: tiles up to it need no mask
-  const int wfirst = base + (t.row0 + wave * 32) / g;
-  const int steps = (kend + 63) >> 6;
-  const int lo = (int)((long)steps * t.split / t.ns), hi = (int)((long)steps * (t.split + 1) / t.ns);
-
+  const int wfirst = base + row0 / g;
+  const int lo = t.lo, hi = t.hi;
   v16f o[DB];
 #pragma unroll
-  for (int d = 0; d < DB; ++d)
-#pragma unroll
-    for (int i = 0; i < 16; ++i) o[d][i] = 0.0f;
-  float m = neg_inf(), mc = 0.0f, l = 0.0f;
+  for (int d = 0; d < DB; ++d) o[d] = v16f{};
+  float m = neg_inf(), l = 0.0f;  // the running maximum (times c; -inf: no key yet) and sum of the lane's row
   const float c = a.scale_log2;
-  lds_u8* lb = (lds_u8*)lds;
-  // row `col` of score block x holds key 32 x + 16 (a / 2) + 8 hh + 4 (a % 2) + j, col = 8 a + 4 hh + j
-  const int perm = 16 * (col >> 4) + 8 * ((col >> 2) & 1) + 4 * ((col >> 3) & 1) + (col & 3);
 
-  // The pages of 16 steps, a run of 16 keys a lane.  They are fetched a block of steps ahead: a load
-  // waited for here would be waited for behind the DMA that the step has just begun.
-  int ids = page_of(a, t, (lo * 4 + lane) * 16), next_ids = page_of(a, t, (lo * 4 + 64 + lane) * 16);
-  if (lo < hi) load_kv<D>(a, __builtin_amdgcn_readlane(ids, wave), h, lo * 64, lb);
-  for (int st = lo; st < hi; ++st) {
-    const int k0 = st * 64;
-    const int n = (st - lo) & 15;
-    uint8_t* buf = lds + ((st - lo) & 1) * BUF;
-    int bad = (int)(__ballot(ids < 0) >> (n * 4)) & 15;  // runs of 16 keys without a page
-    if (k0 + 64 > t.kv) bad |= 16;
-    wait_vm<0>();
-    lds_barrier();  // this buffer has landed, and the other one is no longer read
-    if (n == 15) {
-      ids = next_ids;
-      next_ids = page_of(a, t, ((st + 1) * 4 + 64 + lane) * 16);
+  if (lo < hi) {
+    // The pages of 16 tiles, a run of 16 keys a lane, and those of the next 16: a page that is looked up
+    // when it is needed would be waited for behind the DMA that is under way.
+    int ids = page_of(a, t, (lo * 4 + lane) * 16), next_ids = page_of(a, t, (lo * 4 + 64 + lane) * 16);
+    auto bad_of = [&](int n, int k0) {  // runs of 16 keys without a page; 16: the request ends in this tile
+      return ((int)(__ballot(ids < 0) >> ((n & 15) * 4)) & 15) | (k0 + 64 > t.kv ? 16 : 0);
+    };
+    // A wavefront loads half a run: 8 keys of K, half the rows of V^T.
+    const int run = wave >> 1, part = wave & 1;
+    const int koff = k_place<D>(), voff = v_place(a.sh);
+    lds_u8* const lk = (lds_u8*)lds + (run * 16 + part * 8) * D * 2;
+    lds_u8* const lv = (lds_u8*)lds + HALF + run * D * 32 + part * D * 16;
+    auto load = [&](int n) {
+      const int id = __builtin_amdgcn_readlane(ids, (n & 15) * 4 + run);
+      const long block = 2 * block_at<D>(a, id < 0 ? 0 : id, h);
+      const int at = ((lo + n) * 64 + run * 16) & a.mask, slot = (n & (kRing - 1)) * TILE;
+      load_k<D>(a, block, at, part, koff, lk + slot);
+      load_v<D>(a, block, at, part, voff, lv + slot);
+    };
+    constexpr int LOADS = D / 32;  // of a wavefront for a tile
+    lds_barrier();  // the tile before is done with the ring
+    int bads = 0;  // eight bits a tile: st, st + 1, st + 2 (the lowest first)
+#pragma unroll
+    for (int i = 0; i < kRing - 1; ++i) {
+      if (lo + i < hi) load(i);
+      bads |= bad_of(i, (lo + i) * 64) << (8 * i);
     }
-    if (st + 1 < hi)
-      load_kv<D>(a, __builtin_amdgcn_readlane(ids, ((n + 1) & 15) * 4 + wave), h, k0 + 64, lb + ((st - lo + 1) & 1) * BUF);
-    if (bad) {  // V of keys that do not exist may hold anything, and 0 * NaN is not 0
-      uint16_t* v = reinterpret_cast<uint16_t*>(buf + 64 * D * 2);
-      for (int i = threadIdx.x; i < 64 * D; i += 256) {
-        const int u = i / (16 * D), d = (i / 16) % D, e = i & 15;
-        const int key = u * 16 + ((((e >> 3) ^ (d >> 3)) & 1) << 3) + (e & 7);
-        if (k0 + key >= t.kv || ((bad >> u) & 1)) v[i] = 0;
+    // row `col` of a score block holds its key 16 (b / 2) + 8 hh + 4 (b % 2) + j, col = 8 b + 4 hh + j; piece
+    // 2 k + half of a row stands at position (2 k + half) ^ row number, where 2 k changes the higher bits only
+    const int kr = 16 * (col >> 4) + 8 * ((col >> 2) & 1) + 4 * ((col >> 3) & 1) + (col & 3);
+    const int ka = kr * D * 2 + ((half ^ (kr & (CH - 1))) << 4), va = HALF + col * 32 + ((half ^ ((col >> 3) & 1)) << 4);
+    int slot = 0;  // of tile st
+    for (int st = lo; st < hi; ++st) {
+      const int k0 = st * 64, n = st - lo;
+      if (st + 2 < hi) wait_vm<2 * LOADS>();
+      else wait_vm<0>();
+      lds_barrier();  // tile st has landed, tile st - 1 is no longer read
+      if (rare(((n + 3) & 15) == 0)) {
+        ids = next_ids;
+        next_ids = page_of(a, t, (st * 4 + 76 + lane) * 16);
       }
-      lds_barrier();
-    }
-    v16f s[2];
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) s[x][i] = 0.0f;
-      const int kr = 32 * x + perm;
-#pragma unroll
-      for (int k = 0; k < DK; ++k) {
-        const v8bf kf = *reinterpret_cast<const v8bf*>(buf + kr * D * 2 + (((2 * k + half) ^ (kr & (CH - 1))) << 4));
-        s[x] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, q[k], s[x], 0, 0, 0);
+      if (st + 3 < hi) load(n + 3);
+      bads |= bad_of(n + 3, k0 + 192) << 24;
+      const int bad = bads & 31;
+      bads = (int)((unsigned)bads >> 8);
+      if (rare(bad != 0)) {  // V of keys that do not exist may hold anything, and 0 * NaN is not 0
+        uint16_t* v = reinterpret_cast<uint16_t*>(lds + slot + HALF);
+        int first = threadIdx.x;
+        asm volatile("" : "+v"(first));  // rarely run: nothing of it is kept in registers over the loop
+        for (int i = first; i < 64 * D; i += 512) {
+          const int u = i / (16 * D), d = (i / 16) % D, e = i & 15;
+          const int key = u * 16 + ((((e >> 3) ^ (d >> 3)) & 1) << 3) + (e & 7);
+          if (k0 + key >= t.kv || ((bad >> u) & 1)) v[i] = 0;
+        }
+        lds_barrier();
       }
-    }
-    if (k0 + 63 > wfirst || bad) {
-      // element i of block x is key 32 x + 16 (i / 8) + 8 half + i % 8
+      // Scores: element i of block x is key 32 x + 16 (i / 8) + 8 half + i % 8.  All operands are read ahead of the
+      // first product (left to itself the compiler reads each when it is due, and every product waits for LDS),
+      // and the two blocks take turns, so that no product waits for the one before.
+      v16f s[2];
+      v8bf kf[2][DK];
+#pragma unroll
+      for (int k = 0; k < DK; ++k)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) kf[x][k] = *reinterpret_cast<const v8bf*>(lds + x * (HALF / 2) + ((slot + ka) ^ (k * 32)));
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int k = 0; k < DK; ++k)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) s[x] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[x][k], q[k], k == 0 ? v16f{} : s[x], 0, 0, 0);
+      auto value = [&](int y, int d) { return *reinterpret_cast<const v8bf*>(lds + slot + va + (y * DB + d) * 1024); };
+      v8bf vf[2][DB];
+#pragma unroll
+      for (int y = 0; y < 2; ++y)
+#pragma unroll
+        for (int d = 0; d < DB; ++d) vf[y][d] = value(y, d);
+      __builtin_amdgcn_sched_barrier(0);
+      if (k0 + 63 > wfirst || bad) {
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const int end = (bad >> y) & 1 ? -1 : last - k0;
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (16 * y + i > end) s[y >> 1][8 * (y & 1) + i] = neg_inf();
+        }
+      }
+      float mx = neg_inf();
 #pragma unroll
       for (int x = 0; x < 2; ++x)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int key = 32 * x + 16 * (i >> 3) + 8 * half + (i & 7);
-          if (k0 + key > last || ((bad >> (2 * x + (i >> 3))) & 1)) s[x][i] = neg_inf();
-        }
-    }
-    float mx = neg_inf();
+        for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[x][i]);
+      mx *= c;
+      if (__any(mx > m + kSlack)) {
+        const float mn = fmaxf(m, max_halves(mx));
+        const float f = __builtin_amdgcn_exp2f(m - (mn == neg_inf() ? 0.0f : mn));
+        l *= f;
 #pragma unroll
-    for (int x = 0; x < 2; ++x)
+        for (int d = 0; d < DB; ++d) o[d] *= f;
+        m = mn;
+      }
+      const float mc = m == neg_inf() ? 0.0f : m;
+      const v2bf one = {(__bf16)1.0f, (__bf16)1.0f};
 #pragma unroll
-      for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[x][i]);
-    if (__any(mx * c > mc + kSlack || (m == neg_inf() && mx > neg_inf()))) {
-      const float mn = fmaxf(m, max_halves(mx));
-      const float ms = mn == neg_inf() ? 0.0f : mn;
-      const float f = __builtin_amdgcn_exp2f(m * c - ms * c);
-      l *= f;
-#pragma unroll
-      for (int d = 0; d < DB; ++d) o[d] *= f;
-      m = mn;
-      mc = ms * c;
-    }
-#pragma unroll
-    for (int x = 0; x < 2; ++x)
-#pragma unroll
-      for (int y = 0; y < 2; ++y) {
+      for (int y = 0; y < 4; ++y) {
         v8bf p;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[x][8 * y + i], c, -mc));
-          l += e;
-          p[i] = (__bf16)e;
+        for (int i = 0; i < 8; i += 2) {
+          const v2bf e = {(__bf16)__builtin_amdgcn_exp2f(__builtin_fmaf(s[y >> 1][8 * (y & 1) + i], c, -mc)),
+                          (__bf16)__builtin_amdgcn_exp2f(__builtin_fmaf(s[y >> 1][8 * (y & 1) + i + 1], c, -mc))};
+          p[i] = e[0], p[i + 1] = e[1];
+          l = __builtin_amdgcn_fdot2_f32_bf16(e, one, l, false);
         }
-        const uint8_t* vt = buf + 64 * D * 2 + (2 * x + y) * D * 32;
 #pragma unroll
-        for (int d = 0; d < DB; ++d) {
-          const int dr = d * 32 + col;
-          const v8bf vf = *reinterpret_cast<const v8bf*>(vt + dr * 32 + ((half ^ ((dr >> 3) & 1)) << 4));
-          o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, p, o[d], 0, 0, 0);
+        for (int d = 0; d < DB; ++d) o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[y & 1][d], p, o[d], 0, 0, 0);
+        if (y < 2) {
+#pragma unroll
+          for (int d = 0; d < DB; ++d) vf[y][d] = value(y + 2, d);
         }
       }
+      slot = (slot + TILE) & (kRing * TILE - 1);
+    }
   }
   l += __shfl_xor(l, 32);
   if (!live) return;
-  if (a.CNT && t.split == 0 && half == 0) a.CNT[out_row] = t.ns;
-  if (t.ns == 1) {
+  if (t.part < 0) {
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // no key: zeros
     __bf16* out = static_cast<__bf16*>(a.O) + out_row * D;
 #pragma unroll
@@ -410,7 +439,7 @@ __device__ __forceinline__ void large_tile(const AttnArgs& a, const Tile& t, int
         *reinterpret_cast<v4bf*>(out + d * 32 + 8 * i + 4 * half) = b;
       }
   } else {
-    const long at = (long)t.split * a.S * a.HQ + out_row;
+    const long at = t.part + wave * 32 + col;
     float* out = a.PO + at * D;
 #pragma unroll
     for (int d = 0; d < DB; ++d)
@@ -418,187 +447,282 @@ __device__ __forceinline__ void large_tile(const AttnArgs& a, const Tile& t, int
       for (int i = 0; i < 4; ++i)
         *reinterpret_cast<v4f*>(out + d * 32 + 8 * i + 4 * half) =
             v4f{o[d][4 * i], o[d][4 * i + 1], o[d][4 * i + 2], o[d][4 * i + 3]};
-    if (half == 0) *reinterpret_cast<float2*>(a.PM + at * 2) = float2{mc, l};
+    if (half == 0) *reinterpret_cast<float2*>(a.PM + at * 2) = float2{m, l};
   }
 }
 
-// A request's tiles, and the 64-key steps that each takes (a step's cost is about the same for both
-// shapes: the small one waits for memory, the large one works).
-__device__ __forceinline__ void shape(const AttnArgs& a, int r, int& tiles, int& steps) {
-  const int c0 = clampi(a.CU[r], 0, a.S), c1 = clampi(a.CU[r + 1], 0, a.S);
-  const int rows = (c1 > c0 ? c1 - c0 : 0) * a.g;
-  tiles = rows > kSmallRows ? (rows + kLargeRows - 1) / kLargeRows : (rows + 15) >> 4;
-  steps = (clampi(a.KV[r], 0, (int)((long)a.MB << a.sh)) + 63) >> 6;
+// ------------------------------------------------------------------ the cuts
+// The tiles of ROWS rows of a request and their lengths: tile i sees the keys up to its last token, base + (i +
+// 1) tau with tau tokens a tile, and the i tiles ahead of it together (exactly, in whole numbers) before(i).
+// WHOLE: every tile has the length 1.
+template <int ROWS, bool WHOLE>
+struct Request {
+  int c0, n, kv, tiles;
+  long base, tau;
+  __device__ __forceinline__ Request(const AttnArgs& a, int r) {
+    c0 = clampi(a.CU[r], 0, a.S);
+    const int c1 = clampi(a.CU[r + 1], 0, a.S);
+    n = c1 > c0 ? c1 - c0 : 0;
+    kv = clampi(a.KV[r], 0, (int)((long)a.MB << a.sh));
+    tiles = (n * a.g + ROWS - 1) / ROWS;
+    base = WHOLE ? 1 : kv > n ? kv - n : 0;
+    tau = WHOLE ? 0 : (ROWS + a.g - 1) / a.g;
+  }
+  __device__ __forceinline__ long before(long i) const { return i * base + tau * (i * (i + 1) / 2); }
+  __device__ __forceinline__ long all() const { return before(tiles); }
+};
+
+__device__ __forceinline__ long lane_of(long v, int src) {
+  const unsigned lo = __builtin_amdgcn_readlane((int)v, src), hi = __builtin_amdgcn_readlane((int)(v >> 32), src);
+  return (long)((unsigned long)hi << 32 | lo);
 }
 
-// Workgroups: key heads fastest (an XCD takes every eighth workgroup, so with eight key heads each XCD's
-// L2 holds one head's cache), then units of work: requests in order, a request's later tiles first (they
-// see the most keys), a tile's ranges of keys in order.  Every wavefront finds the unit by itself, its
-// lanes a share of the requests each.
-template <int D>
-__global__ __launch_bounds__(256, 2) void k_attn(AttnArgs a) {
-  __shared__ __align__(16) uint8_t lds[64 * D * 8 > 128 * 4 + 4 * 16 * (D + 4) * 4 ? 64 * D * 8 : 128 * 4 + 4 * 16 * (D + 4) * 4];
-  const int h = blockIdx.x % a.HKV;
-  const int unit = blockIdx.x / a.HKV;
-  const int lane = threadIdx.x & 63;
-  const int per = (a.R + 63) >> 6;
-  const int r0 = lane * per, r1 = r0 + per < a.R ? r0 + per : a.R;
-  int tiles, steps;
-  int chunk = 0x7FFFFFFF;  // steps of a unit
-  if (a.cap > 1) {
-    long sum = 0;
+// All tiles of a key head in a row, cut into `parts` equal parts (WHOLE: a tile each).  A wavefront's lanes hold
+// a share of the requests each.
+template <int ROWS, bool WHOLE>
+struct Cuts {
+  typedef Request<ROWS, WHOLE> Req;
+  long all, upto;  // the row's length; the lane's requests end there
+  long mine;       // length of the lane's requests
+  long each;       // all / parts
+  int over;        // all % parts
+  int r0, r1, parts;
+
+  __device__ __forceinline__ Cuts(const AttnArgs& a) {
+    const int lane = threadIdx.x & 63;
+    const int per = (a.R + 63) >> 6;
+    r0 = lane * per < a.R ? lane * per : a.R;
+    r1 = r0 + per < a.R ? r0 + per : a.R;
+    long most = 0;  // the longest tile
+    mine = 0;
+#pragma unroll 4
     for (int r = r0; r < r1; ++r) {
-      shape(a, r, tiles, steps);
-      sum += (long)tiles * steps;
+      const Req q(a, r);
+      mine += q.all();
+      const long last = q.tiles > 0 ? q.base + q.tiles * q.tau : 0;
+      most = last > most ? last : most;
     }
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
-    const long want = (sum + a.target - 1) / a.target;
-    chunk = want < kMinSteps ? kMinSteps : want < chunk ? (int)want : chunk;
+    upto = mine;
+    const int lanes = (a.R + per - 1) / per;
+    for (int d = 1; d < lanes; d <<= 1) {  // up to each lane
+      const long up = __shfl_up(upto, d), other = __shfl_up(most, d);
+      if (lane >= d) {
+        upto += up;
+        most = other > most ? other : most;
+      }
+    }
+    all = lane_of(upto, lanes - 1);
+    most = lane_of(most, lanes - 1);
+    if (WHOLE) {
+      parts = (int)all;
+      each = 1, over = 0;
+    } else {
+      long p = a.target;
+      if (p > all / kMinKeys) p = all / kMinKeys;
+      if (most > 0 && p > kMaxCuts * (all / most)) p = kMaxCuts * (all / most);
+      parts = p < 1 ? 1 : (int)p;
+      each = all / parts;
+      over = (int)(all - each * parts);
+    }
   }
-  auto ranges = [&](int st) {  // of a request of st steps
-    const int n = a.cap > 1 ? (int)(((long)st + chunk - 1) / chunk) : 1;
-    return n < 1 ? 1 : n < a.cap ? n : a.cap;
-  };
-  int units = 0;
-  for (int r = r0; r < r1; ++r) {
-    shape(a, r, tiles, steps);
-    units += tiles * ranges(steps);
+  // where part w begins
+  __device__ __forceinline__ long cut(int w) const { return each * w + over * w / parts; }
+
+  // The tile at `at` of the row (0 <= at < all): its request, its number there, and where it begins.
+  __device__ __forceinline__ void find(const AttnArgs& a, long at, int& r, int& tile, long& begin) const {
+    const int src = __ffsll(__ballot(at < upto)) - 1;
+    long from = upto - mine;
+    int hit = r0, i = 0;
+    for (int x = r0; x < r1; ++x) {
+      const Req q(a, x);
+      const long len = q.all();
+      if (at - from < len) {
+        if (WHOLE) {
+          i = (int)(at - from);
+        } else if (q.tiles > 1) {
+          // the largest i with before(i) <= at - from: the root of the parabola, put right by whole numbers
+          const double b = (double)q.base + 0.5 * (double)q.tau, y = (double)(at - from);
+          i = (int)((sqrt(b * b + 2.0 * (double)q.tau * y) - b) / (double)q.tau);
+          i = i < 0 ? 0 : i < q.tiles ? i : q.tiles - 1;
+          while (i + 1 < q.tiles && q.before(i + 1) <= at - from) ++i;
+          while (i > 0 && q.before(i) > at - from) --i;
+        }
+        from += q.before(i);
+        hit = x;
+        break;
+      }
+      from += len;
+    }
+    r = __builtin_amdgcn_readlane(hit, src);
+    tile = __builtin_amdgcn_readlane(i, src);
+    begin = lane_of(from, src);
   }
-  int upto = units;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int up = __shfl_up(upto, d);
-    if (lane >= d) upto += up;
+};
+
+// Workgroup: key head h = blockIdx % HKV (an XCD takes every eighth workgroup, so with eight key heads each XCD's
+// L2 holds one head's cache), part w = blockIdx / HKV of the head's row; body(t, h) for each tile of the part in
+// turn.  WHOLE takes a request's later tiles first, which see the most keys, and all from their first key, so that
+// the tiles that run together stream the same keys.  Otherwise the workgroup notes a tile that begins in its part
+// and goes on behind it, for the join.
+template <int ROWS, bool WHOLE, typename Body>
+__device__ __forceinline__ void each_tile(const AttnArgs& a, Body body) {
+  const Cuts<ROWS, WHOLE> cuts(a);
+  const int h = blockIdx.x % a.HKV, w = blockIdx.x / a.HKV;
+  int4 note = {0, 0, 0, 0};
+  if (w < cuts.parts && cuts.all > 0) {
+    const long first = cuts.cut(w), end = cuts.cut(w + 1);
+    int r, i;
+    long begin;
+    cuts.find(a, first, r, i, begin);
+    for (;;) {
+      const Request<ROWS, WHOLE> q(a, r);
+      const long len = WHOLE ? 1 : q.before(i + 1) - q.before(i);
+      Tile t;
+      t.tok0 = __builtin_amdgcn_readfirstlane(q.c0);
+      t.n = __builtin_amdgcn_readfirstlane(q.n);
+      t.kv = __builtin_amdgcn_readfirstlane(q.kv);
+      t.pages = a.TABLE + (long)r * a.MB;
+      t.rows = t.n * a.g;
+      t.row0 = (WHOLE ? q.tiles - 1 - i : i) * ROWS;
+      const int tile_end = t.row0 + ROWS < t.rows ? t.row0 + ROWS : t.rows;
+      const int steps = (clampi(t.kv - t.n + (tile_end - 1) / a.g + 1, 0, t.kv) + 63) >> 6;
+      t.lo = 0, t.hi = steps, t.part = -1;
+      if (!WHOLE) {
+        if (begin < first) t.lo = (int)((first - begin) * steps / len);
+        if (begin + len > end) t.hi = (int)((end - begin) * steps / len);
+        // a tile of several parts: in the workgroup's second place where it begins there, in the first behind a cut
+        if (begin < first || begin + len > end)
+          t.part = (((long)h * a.target + w) * 2 + (begin < first ? 0 : 1)) * ROWS;
+        if (begin >= first && begin + len > end) {
+          int ns = 2;
+          while (w + ns < cuts.parts && cuts.cut(w + ns) < begin + len) ++ns;
+          note = int4{ns, t.row0, t.rows, t.tok0};
+        }
+      }
+      body(t, h);
+      begin += len;
+      if (WHOLE || begin >= end) break;
+      if (++i == q.tiles) {  // the next request; behind idle ones it is looked up
+        i = 0, ++r;
+        if (Request<ROWS, WHOLE>(a, r).tiles == 0) cuts.find(a, begin, r, i, begin);
+      }
+    }
   }
-  const unsigned long long mine = __ballot(unit >= upto - units && unit < upto);
-  if (mine == 0) return;  // no such unit: the grid is an upper bound
-  int in = unit - (upto - units), hit = r0, ns = 1, nt = 0;
-  for (int r = r0; r < r1; ++r) {
-    shape(a, r, tiles, steps);
-    const int n = ranges(steps);
-    hit = r, ns = n, nt = tiles;
-    if (in < tiles * n) break;
-    in -= tiles * n;
-  }
-  const int src = __ffsll(mine) - 1;
-  hit = __builtin_amdgcn_readlane(hit, src);
-  in = __builtin_amdgcn_readlane(in, src);
-  ns = __builtin_amdgcn_readlane(ns, src);
-  nt = __builtin_amdgcn_readlane(nt, src);
-  Tile t;
-  request(a, hit, t);
-  t.rows = t.n * a.g;
-  t.ns = ns;
-  t.split = in % ns;
-  const int tile = nt - 1 - in / ns;
-  if (t.rows <= kSmallRows) {
-    t.row0 = tile * 16;
-    small_tile<D>(a, t, h, reinterpret_cast<float*>(lds));
-  } else {
-    t.row0 = tile * kLargeRows;
-    large_tile<D>(a, t, h, lds);
-  }
+  if (!WHOLE && threadIdx.x == 0) a.NOTE[h * a.target + w] = note;
 }
 
-// Joins the ranges of each row that was cut: WPR wavefronts a row, D / 64 values a lane, lane s holding
-// range s's maximum and sum; the ranges are added in an order that their number alone fixes.
-// HBM-bound on the partial outputs; with few rows four wavefronts share one, to have its loads in flight at once.
-template <int D, int WPR>
+template <int D>
+__global__ __launch_bounds__(256, 2) void k_attn_small(AttnArgs a) {
+  __shared__ __align__(16) float lds[128 + 4 * 16 * (D + 4)];
+  each_tile<kSmallRows, false>(a, [&](const Tile& t, int h) { small_tile<D>(a, t, h, lds); });
+}
+
+template <int D, bool WHOLE>
+__global__ __launch_bounds__(512, 2) void k_attn_large(AttnArgs a) {
+  extern __shared__ __align__(16) uint8_t dlds[];
+  each_tile<kLargeRows, WHOLE>(a, [&](const Tile& t, int h) { large_tile<D>(a, t, h, dlds); });
+}
+
+// Joins the parts of the tile that part w noted, 16 rows a workgroup, four a wavefront: lane k holds the maximum
+// and sum of part w + k of a row, and the lanes D / 64 values of it each; the parts are added in their order.
+template <int D, int ROWS>
 __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
-  constexpr int E = D / 64;
+  constexpr int E = D / 64, RW = 4;
   typedef float vE __attribute__((ext_vector_type(E)));
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const long row = (long)blockIdx.x * (4 / WPR) + wave / WPR;
-  const int part = wave % WPR;
-  const long first = (long)clampi(a.CU[0], 0, a.S) * a.HQ, end = (long)clampi(a.CU[a.R], 0, a.S) * a.HQ;
-  if (row < first || row >= end) return;
-  const int ns = __builtin_amdgcn_readfirstlane(clampi(a.CNT[row], 1, a.cap));
-  if (ns == 1) return;  // written by its tile
-  const long rows = (long)a.S * a.HQ;
-  float2 ml = {0.0f, 0.0f};
-  if (lane < ns) ml = *reinterpret_cast<const float2*>(a.PM + (lane * rows + row) * 2);
-  const bool any = ml.y != 0.0f;  // a range of no keys has a sum of 0 and no output
-  float m = any ? ml.x : neg_inf();
+  const int h = blockIdx.x % a.HKV, w = blockIdx.x / a.HKV;
+  const int4 note = a.NOTE[h * a.target + w];
+  const int ns = __builtin_amdgcn_readfirstlane(note.x);
+  const int x0 = blockIdx.y * 16 + wave;  // the wavefront's rows of the tile: x0, x0 + 4, ..
+  if (ns == 0 || note.y + x0 >= note.z) return;
+  // row x of the tile in part w + k: in that workgroup's second place for k = 0, in its first for the others
+  auto place = [&](int k, int x) { return (((long)h * a.target + w + k) * 2 + (k == 0 ? 1 : 0)) * ROWS + x; };
+  float2 ml[RW];
 #pragma unroll
-  for (int d = 1; d < 64; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
-  const float f = any ? __builtin_amdgcn_exp2f(ml.x - m) : 0.0f;
-  float l = f * ml.y;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) l += __shfl_xor(l, d);
-  const int s0 = ns * part / WPR, s1 = ns * (part + 1) / WPR;
-  const float* src = a.PO + row * D + lane * E;
-  vE acc = {};
-  for (int s = s0; s < s1; s += 8) {
-    vE v[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int x = s + i < s1 ? s + i : s1 - 1;
-      v[i] = *reinterpret_cast<const vE*>(src + x * rows * D);
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float w = s + i < s1 ? __shfl(f, s + i) : 0.0f;
-#pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] += w != 0.0f ? v[i][e] * w : 0.0f;
-    }
+  for (int j = 0; j < RW; ++j) {
+    ml[j] = float2{0.0f, 0.0f};
+    if (lane < ns) ml[j] = *reinterpret_cast<const float2*>(a.PM + place(lane, x0 + 4 * j) * 2);
   }
-  if constexpr (WPR > 1) {
-    __shared__ vE half[WPR][64];
-    half[part][lane] = acc;
-    __syncthreads();  // the wavefronts of a workgroup share the row: all are here or none
-    if (part != 0) return;
+  float f[RW], l[RW];
 #pragma unroll
-    for (int p = 1; p < WPR; ++p) acc += half[p][lane];
+  for (int j = 0; j < RW; ++j) {
+    const bool any = ml[j].y != 0.0f;  // a part of no keys has a sum of 0, and its output does not count
+    float m = any ? ml[j].x : neg_inf();
+    for (int d = 1; d < ns; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
+    f[j] = any ? __builtin_amdgcn_exp2f(ml[j].x - __shfl(m, 0)) : 0.0f;
+    l[j] = f[j] * ml[j].y;
+    for (int d = 1; d < ns; d <<= 1) l[j] += __shfl_xor(l[j], d);
+    l[j] = __shfl(l[j], 0);
   }
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  __bf16* out = static_cast<__bf16*>(a.O) + row * D + lane * E;
+  vE acc[RW] = {};
+  for (int k = 0; k < ns; k += 4) {
+    vE v[4][RW];
 #pragma unroll
-  for (int e = 0; e < E; ++e) out[e] = (__bf16)(acc[e] * inv);
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < RW; ++j)
+        v[i][j] = *reinterpret_cast<const vE*>(a.PO + place(k + i < ns ? k + i : ns - 1, x0 + 4 * j) * D + lane * E);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < RW; ++j) {
+        const float wt = k + i < ns ? __shfl(f[j], k + i) : 0.0f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[j][e] += wt != 0.0f ? v[i][j][e] * wt : 0.0f;
+      }
+  }
+#pragma unroll
+  for (int j = 0; j < RW; ++j) {
+    const int row = note.y + x0 + 4 * j;
+    if (row >= note.z) return;
+    const float inv = l[j] == 0.0f ? 0.0f : 1.0f / l[j];
+    const int tok = row / a.g;
+    __bf16* out = static_cast<__bf16*>(a.O) + ((long)(note.w + tok) * a.HQ + h * a.g + (row - tok * a.g)) * D + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; ++e) out[e] = (__bf16)(acc[j][e] * inv);
+  }
 }
 
 }  // namespace
 
-// Units and ranges of a call.  A request of more than kSmallRows rows has rows / 128 large tiles rounded
-// up, any other two small ones at most; the units are at most one more for each tile than the work
-// divided by a unit's (osc_attn.hip's kernel takes at least work / target steps for a unit).
-AttnPlan attn_plan(int S, int R, int HQ, int HKV, int D, int page, int MB) {
-  const long rows = (long)S * (HQ / HKV);
-  const long big = rows / (kSmallRows + 1);
-  const long large = big > 0 ? rows / kLargeRows + (big < R ? big : R) : 0;
-  const long few = rows / 16 + R < 2l * R ? rows / 16 + R : 2l * R;
-  const long tiles = large + few;
-  // tiles that are expected to work: all rows in 128-row tiles, or one small tile a request
-  const long busy = (rows / R > kSmallRows ? (rows + kLargeRows - 1) / kLargeRows : R) * HKV;
+// Small tiles where there are at most as many tokens as requests: single tokens, in all likelihood.  A chunk
+// among as many idle requests would be slow there but right; with more tokens than requests a large tile
+// of a few rows still takes no longer than its keys take from memory.  With three tiles and more for every
+// workgroup that runs at once the large tiles are left whole: there is little to even out then.
+AttnPlan attn_plan(int S, int R, int HQ, int HKV, int D) {
   AttnPlan p;
-  const long steps = ((long)MB * page + 63) / 64;
-  long cap = steps / kMinSteps;  // were a request's table full
-  if (cap > kMaxSplit) cap = kMaxSplit;
-  if (busy >= 4 * kSlots || cap < 1) cap = 1;
-  p.cap = (int)cap;
-  p.target = (kSlots + HKV - 1) / HKV;
-  p.units = cap == 1 ? tiles : tiles * cap < p.target + tiles ? tiles * cap : p.target + tiles;
-  p.ws_bytes = cap > 1 ? cap * S * HQ * (long)(D + 2) * 4 + (long)S * HQ * 4 : 0;
+  p.small = S <= R;
+  const long tiles = (long)S * (HQ / HKV) / kLargeRows;  // at least, were all of the tokens one request's
+  const int slots = p.small ? 2 * kCUs : kCUs;           // workgroups that run at once
+  p.whole = !p.small && tiles * HKV >= 3 * slots;
+  p.target = p.whole ? (int)(tiles + (R < S ? R : S)) : (slots + HKV - 1) / HKV;
+  const long rows = p.whole ? 0 : (long)HKV * p.target * 2 * (p.small ? kSmallRows : kLargeRows);
+  p.ws_bytes = rows * (D + 2) * 4 + (p.whole ? 0 : (long)HKV * p.target * (long)sizeof(int4));
   return p;
 }
 
-hipError_t launch_attn(const AttnArgs& a, int D, long units, hipStream_t st) {
-  const long grid = units * a.HKV;
-  if (grid > 0x7FFFFFFFL) return hipErrorInvalidValue;
-  if (D == 128) hipLaunchKernelGGL(k_attn<128>, dim3((unsigned)grid), dim3(256), 0, st, a);
-  else hipLaunchKernelGGL(k_attn<64>, dim3((unsigned)grid), dim3(256), 0, st, a);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || a.cap == 1) return e;
-  const long rows = (long)a.S * a.HQ;
-  if (rows <= 4096) {
-    if (D == 128) hipLaunchKernelGGL((k_attn_join<128, 4>), dim3((unsigned)rows), dim3(256), 0, st, a);
-    else hipLaunchKernelGGL((k_attn_join<64, 4>), dim3((unsigned)rows), dim3(256), 0, st, a);
-  } else {
-    const unsigned jg = (unsigned)((rows + 3) / 4);
-    if (D == 128) hipLaunchKernelGGL((k_attn_join<128, 1>), dim3(jg), dim3(256), 0, st, a);
-    else hipLaunchKernelGGL((k_attn_join<64, 1>), dim3(jg), dim3(256), 0, st, a);
+template <int D>
+static hipError_t launch_d(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
+  const long blocks = (long)p.target * a.HKV;
+  if (blocks > 0x7FFFFFFFL) return hipErrorInvalidValue;
+  const unsigned grid = (unsigned)blocks;
+  if (p.small) {
+    hipLaunchKernelGGL(k_attn_small<D>, dim3(grid), dim3(256), 0, st, a);
+    hipLaunchKernelGGL((k_attn_join<D, kSmallRows>), dim3(grid), dim3(256), 0, st, a);
+    return hipGetLastError();
   }
+  constexpr int bytes = kRing * 64 * D * 4;
+  auto kern = p.whole ? k_attn_large<D, true> : k_attn_large<D, false>;
+  const hipError_t e =
+      hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(kern, dim3(grid), dim3(512), bytes, st, a);
+  if (!p.whole) hipLaunchKernelGGL((k_attn_join<D, kLargeRows>), dim3(grid, kLargeRows / 16), dim3(256), 0, st, a);
   return hipGetLastError();
+}
+
+hipError_t launch_attn(const AttnArgs& a, int D, const AttnPlan& p, hipStream_t st) {
+  return D == 128 ? launch_d<128>(a, p, st) : launch_d<64>(a, p, st);
 }
 
 }  // namespace osc

@@ -129,12 +129,12 @@ hipError_t launch_qkv_append(const AppendArgs& a, hipStream_t st);
 
 // Attention over the paged cache (osc_attn_paged).
 struct AttnPlan {
-  int cap;     // most ranges that a request's keys are cut into
-  int target;  // units of work wanted for each key head
-  long units;  // upper bound on them
+  bool small;  // 16-row tiles
+  bool whole;  // no tile is cut
+  int target;  // workgroups for each key head
   long ws_bytes;
 };
-AttnPlan attn_plan(int S, int R, int HQ, int HKV, int D, int page, int MB);
+AttnPlan attn_plan(int S, int R, int HQ, int HKV, int D);
 struct AttnArgs {
   const void *Q, *KC, *VC;
   int S, R, HQ, HKV, g;  // g = HQ / HKV
@@ -142,11 +142,13 @@ struct AttnArgs {
   const int32_t *TABLE, *CU, *KV;
   float scale_log2;  // scale * log2(e)
   void* O;
-  // with cap > 1: [cap][S*HQ][D] unnormalised outputs, [cap][S*HQ][2] scaled maximum and sum, [S*HQ] ranges of a row
-  float *PO, *PM;
-  int32_t* CNT;
-  int cap, target;
+  // Workspace, where tiles are cut: [HKV][target] notes of the workgroups; [HKV][target][2 places][rows of a tile]
+  // scaled maximum and sum, and D unnormalised outputs.
+  float* PO;
+  float* PM;
+  int4* NOTE;
+  int target;
 };
-hipError_t launch_attn(const AttnArgs& a, int D, long units, hipStream_t st);
+hipError_t launch_attn(const AttnArgs& a, int D, const AttnPlan& p, hipStream_t st);
 
 }  // namespace osc
