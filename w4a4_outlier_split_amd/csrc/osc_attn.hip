@@ -41,7 +41,7 @@ constexpr int kLargeRows = 256;
 constexpr int kRing = 4;        // tiles of 64 keys in LDS
 constexpr int kCUs = 256;
 constexpr int kMaxCuts = 61;    // of one tile: its parts, two more at most, are the lanes of the join
-constexpr int kMinKeys = 256;   // that a workgroup's part has at least
+constexpr int kMinKeysSmall = 128, kMinKeysLarge = 256;  // that a workgroup's part has at least
 // The running maximum is left as it is while no score exceeds it by more than kSlack (in the exponent
 // of 2): P is then at most 2^kSlack, and binary32 holds sums of 2^31 of them times a bf16 value of up to
 // 2^50; neither format loses precision by the factor.
@@ -90,6 +90,32 @@ __device__ __forceinline__ float max_groups(float v) {
   const auto x = __builtin_amdgcn_permlane16_swap(a, a, false, false);
   const unsigned x0 = x[0], x1 = x[1];
   return max_halves(fmaxf(__builtin_bit_cast(float, x0), __builtin_bit_cast(float, x1)));
+}
+
+// The same and the sum over all lanes.  A row of 16 lanes first: neighbours, pairs, then the two mirrors.
+template <int CTRL>
+__device__ __forceinline__ float lane_swap(float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xF, 0xF, false));
+}
+__device__ __forceinline__ float max_wave(float v) {
+  v = fmaxf(v, lane_swap<0xB1>(v));
+  v = fmaxf(v, lane_swap<0x4E>(v));
+  v = fmaxf(v, lane_swap<0x141>(v));
+  v = fmaxf(v, lane_swap<0x140>(v));
+  return max_groups(v);
+}
+__device__ __forceinline__ float sum_wave(float v) {
+  v += lane_swap<0xB1>(v);
+  v += lane_swap<0x4E>(v);
+  v += lane_swap<0x141>(v);
+  v += lane_swap<0x140>(v);
+  const unsigned a = __builtin_bit_cast(unsigned, v);
+  const auto x = __builtin_amdgcn_permlane16_swap(a, a, false, false);
+  const unsigned x0 = x[0], x1 = x[1];
+  const unsigned b = __builtin_bit_cast(unsigned, __builtin_bit_cast(float, x0) + __builtin_bit_cast(float, x1));
+  const auto y = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+  const unsigned y0 = y[0], y1 = y[1];
+  return __builtin_bit_cast(float, y0) + __builtin_bit_cast(float, y1);
 }
 
 // ------------------------------------------------------------------ small tiles
@@ -334,7 +360,8 @@ __device__ __forceinline__ void large_tile(const AttnArgs& a, const Tile& t, int
     const int kr = 16 * (col >> 4) + 8 * ((col >> 2) & 1) + 4 * ((col >> 3) & 1) + (col & 3);
     const int ka = kr * D * 2 + ((half ^ (kr & (CH - 1))) << 4), va = HALF + col * 32 + ((half ^ ((col >> 3) & 1)) << 4);
     int slot = 0;  // of tile st
-    for (int st = lo; st < hi; ++st) {
+    // The part of a step that loads and waits; the runs of keys missing in the tile, and 16 where the request ends.
+    auto begin = [&](int st) {
       const int k0 = st * 64, n = st - lo;
       if (st + 2 < hi) wait_vm<2 * LOADS>();
       else wait_vm<0>();
@@ -358,6 +385,17 @@ __device__ __forceinline__ void large_tile(const AttnArgs& a, const Tile& t, int
         }
         lds_barrier();
       }
+      return bad;
+    };
+    if (row0 >= t.rows) {  // a wavefront without a row loads its share, and leaves the rest to the others
+      for (int st = lo; st < hi; ++st) {
+        begin(st);
+        slot = (slot + TILE) & (kRing * TILE - 1);
+      }
+      return;
+    }
+    for (int st = lo; st < hi; ++st) {
+      const int k0 = st * 64, bad = begin(st);
       // Scores: element i of block x is key 32 x + 16 (i / 8) + 8 half + i % 8.  All operands are read ahead of the
       // first product (left to itself the compiler reads each when it is due, and every product waits for LDS),
       // and the two blocks take turns, so that no product waits for the one before.
@@ -477,6 +515,14 @@ __device__ __forceinline__ long lane_of(long v, int src) {
   return (long)((unsigned long)hi << 32 | lo);
 }
 
+// a / b for 0 <= a, 0 < b, a / b < 2^50, by way of 64-bit floating point (a division of integers takes five times as long)
+__device__ __forceinline__ long divide(long a, long b) {
+  long q = (long)((double)a / (double)b);
+  while (q * b > a) --q;
+  while ((q + 1) * b <= a) ++q;
+  return q;
+}
+
 // All tiles of a key head in a row, cut into `parts` equal parts (WHOLE: a tile each).  A wavefront's lanes hold
 // a share of the requests each.
 template <int ROWS, bool WHOLE>
@@ -518,10 +564,11 @@ struct Cuts {
       each = 1, over = 0;
     } else {
       long p = a.target;
-      if (p > all / kMinKeys) p = all / kMinKeys;
-      if (most > 0 && p > kMaxCuts * (all / most)) p = kMaxCuts * (all / most);
+      constexpr int least = ROWS == kSmallRows ? kMinKeysSmall : kMinKeysLarge;
+      if (p > all / least) p = all / least;
+      if (most > 0 && p > kMaxCuts && p > kMaxCuts * divide(all, most)) p = kMaxCuts * divide(all, most);
       parts = p < 1 ? 1 : (int)p;
-      each = all / parts;
+      each = divide(all, parts);
       over = (int)(all - each * parts);
     }
   }
@@ -588,8 +635,8 @@ __device__ __forceinline__ void each_tile(const AttnArgs& a, Body body) {
       const int steps = (clampi(t.kv - t.n + (tile_end - 1) / a.g + 1, 0, t.kv) + 63) >> 6;
       t.lo = 0, t.hi = steps, t.part = -1;
       if (!WHOLE) {
-        if (begin < first) t.lo = (int)((first - begin) * steps / len);
-        if (begin + len > end) t.hi = (int)((end - begin) * steps / len);
+        if (begin < first) t.lo = (int)divide((first - begin) * steps, len);
+        if (begin + len > end) t.hi = (int)divide((end - begin) * steps, len);
         // a tile of several parts: in the workgroup's second place where it begins there, in the first behind a cut
         if (begin < first || begin + len > end)
           t.part = (((long)h * a.target + w) * 2 + (begin < first ? 0 : 1)) * ROWS;
@@ -623,64 +670,53 @@ __global__ __launch_bounds__(512, 2) void k_attn_large(AttnArgs a) {
   each_tile<kLargeRows, WHOLE>(a, [&](const Tile& t, int h) { large_tile<D>(a, t, h, dlds); });
 }
 
-// Joins the parts of the tile that part w noted, 16 rows a workgroup, four a wavefront: lane k holds the maximum
-// and sum of part w + k of a row, and the lanes D / 64 values of it each; the parts are added in their order.
+// The weighted sum of a row's parts 0 .. ns - 1 in their order, FLY of them in flight: part k at src + place(k) * D,
+// its weight in lane k (0 in lane 63).
+template <int FLY, int D, typename vE, typename Place>
+__device__ __forceinline__ vE weigh(const float* src, Place place, int ns, float f) {
+  vE acc = {};
+  for (int k = 0; k < ns; k += FLY) {
+    vE v[FLY];
+#pragma unroll
+    for (int i = 0; i < FLY; ++i) v[i] = *reinterpret_cast<const vE*>(src + place(k + i < ns ? k + i : ns - 1) * D);
+#pragma unroll
+    for (int i = 0; i < FLY; ++i) {
+      const int bits = __builtin_amdgcn_readlane(__builtin_bit_cast(int, f), k + i < ns ? k + i : 63);
+      const float wt = __builtin_bit_cast(float, bits);
+#pragma unroll
+      for (int e = 0; e < D / 64; ++e) acc[e] += wt != 0.0f ? v[i][e] * wt : 0.0f;
+    }
+  }
+  return acc;
+}
+
+// Joins the parts of the tile that part w noted, a row a wavefront: lane k holds the maximum and sum of part w + k,
+// and the lanes D / 64 values of the row each.
 template <int D, int ROWS>
 __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
-  constexpr int E = D / 64, RW = 4;
+  constexpr int E = D / 64;
   typedef float vE __attribute__((ext_vector_type(E)));
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int h = blockIdx.x % a.HKV, w = blockIdx.x / a.HKV;
   const int4 note = a.NOTE[h * a.target + w];
   const int ns = __builtin_amdgcn_readfirstlane(note.x);
-  const int x0 = blockIdx.y * 16 + wave;  // the wavefront's rows of the tile: x0, x0 + 4, ..
-  if (ns == 0 || note.y + x0 >= note.z) return;
+  const int x = blockIdx.y * 4 + wave, row = note.y + x;
+  if (ns == 0 || row >= note.z) return;
   // row x of the tile in part w + k: in that workgroup's second place for k = 0, in its first for the others
-  auto place = [&](int k, int x) { return (((long)h * a.target + w + k) * 2 + (k == 0 ? 1 : 0)) * ROWS + x; };
-  float2 ml[RW];
+  auto place = [&](int k) { return (((long)h * a.target + w + k) * 2 + (k == 0 ? 1 : 0)) * ROWS + x; };
+  float2 ml = {0.0f, 0.0f};
+  if (lane < ns) ml = *reinterpret_cast<const float2*>(a.PM + place(lane) * 2);
+  const bool any = ml.y != 0.0f;  // a part of no keys has a sum of 0, and its output does not count
+  const float m = max_wave(any ? ml.x : neg_inf());
+  const float f = any ? __builtin_amdgcn_exp2f(ml.x - m) : 0.0f;
+  const float l = sum_wave(f * ml.y);
+  const float* src = a.PO + lane * E;
+  const vE acc = ns <= 4 ? weigh<4, D, vE>(src, place, ns, f) : weigh<16, D, vE>(src, place, ns, f);
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  const int tok = row / a.g;
+  __bf16* out = static_cast<__bf16*>(a.O) + ((long)(note.w + tok) * a.HQ + h * a.g + (row - tok * a.g)) * D + lane * E;
 #pragma unroll
-  for (int j = 0; j < RW; ++j) {
-    ml[j] = float2{0.0f, 0.0f};
-    if (lane < ns) ml[j] = *reinterpret_cast<const float2*>(a.PM + place(lane, x0 + 4 * j) * 2);
-  }
-  float f[RW], l[RW];
-#pragma unroll
-  for (int j = 0; j < RW; ++j) {
-    const bool any = ml[j].y != 0.0f;  // a part of no keys has a sum of 0, and its output does not count
-    float m = any ? ml[j].x : neg_inf();
-    for (int d = 1; d < ns; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
-    f[j] = any ? __builtin_amdgcn_exp2f(ml[j].x - __shfl(m, 0)) : 0.0f;
-    l[j] = f[j] * ml[j].y;
-    for (int d = 1; d < ns; d <<= 1) l[j] += __shfl_xor(l[j], d);
-    l[j] = __shfl(l[j], 0);
-  }
-  vE acc[RW] = {};
-  for (int k = 0; k < ns; k += 4) {
-    vE v[4][RW];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < RW; ++j)
-        v[i][j] = *reinterpret_cast<const vE*>(a.PO + place(k + i < ns ? k + i : ns - 1, x0 + 4 * j) * D + lane * E);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < RW; ++j) {
-        const float wt = k + i < ns ? __shfl(f[j], k + i) : 0.0f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[j][e] += wt != 0.0f ? v[i][j][e] * wt : 0.0f;
-      }
-  }
-#pragma unroll
-  for (int j = 0; j < RW; ++j) {
-    const int row = note.y + x0 + 4 * j;
-    if (row >= note.z) return;
-    const float inv = l[j] == 0.0f ? 0.0f : 1.0f / l[j];
-    const int tok = row / a.g;
-    __bf16* out = static_cast<__bf16*>(a.O) + ((long)(note.w + tok) * a.HQ + h * a.g + (row - tok * a.g)) * D + lane * E;
-#pragma unroll
-    for (int e = 0; e < E; ++e) out[e] = (__bf16)(acc[j][e] * inv);
-  }
+  for (int e = 0; e < E; ++e) out[e] = (__bf16)(acc[e] * inv);
 }
 
 }  // namespace
@@ -706,9 +742,11 @@ static hipError_t launch_d(const AttnArgs& a, const AttnPlan& p, hipStream_t st)
   const long blocks = (long)p.target * a.HKV;
   if (blocks > 0x7FFFFFFFL) return hipErrorInvalidValue;
   const unsigned grid = (unsigned)blocks;
+  const long rows = (long)a.S * a.g;  // of a tile at most, too
   if (p.small) {
     hipLaunchKernelGGL(k_attn_small<D>, dim3(grid), dim3(256), 0, st, a);
-    hipLaunchKernelGGL((k_attn_join<D, kSmallRows>), dim3(grid), dim3(256), 0, st, a);
+    const unsigned jy = (unsigned)(((rows < kSmallRows ? rows : kSmallRows) + 3) / 4);
+    hipLaunchKernelGGL((k_attn_join<D, kSmallRows>), dim3(grid, jy), dim3(256), 0, st, a);
     return hipGetLastError();
   }
   constexpr int bytes = kRing * 64 * D * 4;
@@ -717,7 +755,10 @@ static hipError_t launch_d(const AttnArgs& a, const AttnPlan& p, hipStream_t st)
       hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(kern, dim3(grid), dim3(512), bytes, st, a);
-  if (!p.whole) hipLaunchKernelGGL((k_attn_join<D, kLargeRows>), dim3(grid, kLargeRows / 16), dim3(256), 0, st, a);
+  if (!p.whole) {
+    const unsigned jy = (unsigned)(((rows < kLargeRows ? rows : kLargeRows) + 3) / 4);
+    hipLaunchKernelGGL((k_attn_join<D, kLargeRows>), dim3(grid, jy), dim3(256), 0, st, a);
+  }
   return hipGetLastError();
 }
 
