@@ -349,6 +349,7 @@ osc_status osc_rmsnorm(const void* X, const void* RES, const void* W, int S, int
  * What does not fit: a page behind FREE's end or outside [0, NP) is entered as -1, and
  * tokens in it, or at positions >= MB * page, get slot -1 (osc_qkv_append skips them; USED
  * > F - *HEAD tells).  Tokens >= T are counted in CU but not mapped.  Sums saturate at 2^31 - 1.
+ * No input overlaps an output (KV is not CTX or NEW, USED is not HEAD: OSC_E_SHAPE).
  * The call reads no entry that it writes: repeated on the same inputs (a replayed graph) it
  * gives the same tables.  One launch.
  * Constraints: 0 <= R <= OSC_MAX_REQUESTS, F, T >= 0, NP, MB >= 1, NP * page < 2^31,
@@ -369,7 +370,7 @@ osc_status osc_page_plan(const int32_t* CTX, const int32_t* NEW, int R, int page
  *   POS, SLOT  int32 [S]: position (read only with CS) and cache slot of each token.
  *   Q    [S][HQ][D] bf16, written (rounded once); KC, VC: the slots of the S tokens written.
  * A token whose slot is outside [0, NP * page), or whose position is outside [0, P), writes
- * nothing: its row of Q stays as it was.  Slots must be distinct: of two tokens with one slot
+ * nothing: its row of Q stays as it was.  No input overlaps an output.  Slots must be distinct: of two tokens with one slot
  * the cache holds channels of either.
  * Constraints: S >= 0, S < 2^24, 1 <= HQ, HKV <= 1024, D in {64, 128}, S (HQ + 2 HKV) D <
  * 2^34, NP >= 1, NP * page < 2^31, eps positive and finite with WQ, P >= 1 with CS.
@@ -386,10 +387,12 @@ osc_status osc_qkv_append(const void* QKV, int S, int HQ, int HKV, int D, const 
  * with scores, softmax and sums in binary32 and the weights rounded to bf16 for the second
  * product.  n = 1 is a decode step, KV = n a whole prompt, anything between a chunk; the
  * requests of one call may differ.
- *   Q, O [S][HQ][D] bf16; CU int32 [R + 1] ascending (values are taken into [0, S]),
- *   KV int32 [R] (taken into [0, MB * page]).
+ *   Q, O [S][HQ][D] bf16 (O overlaps no other operand); CU int32 [R + 1], 0 <= CU[r] <=
+ *   CU[r + 1]; KV int32 [R] (negative counts as 0).
  * A token that sees no key (KV < n, or no page of its keys exists) gets zeros; keys whose
- * page does not exist are left out.  Rows of O outside [CU[0], CU[R]) stay as they were.
+ * page does not exist, and those at positions >= MB * page, are left out, and tokens >= S
+ * are passed over: what osc_page_plan does not map changes nothing for the others.  Rows of
+ * O outside [CU[0], CU[R]) stay as they were.
  * What the cache holds behind a request's KV keys is never used, whatever it is; NaN in a
  * key reaches the rows that see it, NaN in a value may reach every row of its request.
  *   WS, ws_bytes: device workspace of at least osc_attn_workspace's bytes for the same
@@ -398,7 +401,8 @@ osc_status osc_qkv_append(const void* QKV, int S, int HQ, int HKV, int D, const 
  * The result does not depend on what else runs (sums are joined in a fixed order).
  * Constraints: S >= 0, S < 2^24, 0 <= R <= OSC_MAX_REQUESTS, HQ a multiple of HKV, both in
  * 1..1024, D in {64, 128}, S * HQ * D < 2^34, NP, MB >= 1, NP * page < 2^31, MB * page <=
- * 2^30, scale positive and finite; too small a workspace is OSC_E_SHAPE.
+ * 2^30, scale positive and scale * log2 e finite; too small a workspace is OSC_E_SHAPE.
+ * Scores must stay finite in binary32, times scale * log2 e too.
  */
 osc_status osc_attn_workspace(int S, int R, int HQ, int HKV, int D, int page, int MB, int64_t* bytes);
 osc_status osc_attn_paged(const void* Q, const void* KC, const void* VC, int S, int R, int HQ, int HKV, int D, int page,

@@ -71,6 +71,9 @@ def test_page_plan_refusals():
         assert plan(**{k: V}) == 4, k
     assert plan(HEAD=V) == 4
     assert plan(R=0, T=0, F=0, CU=None) == 1 and plan(R=0, USED=None) == 1
+    # written while other workgroups read: lengths and the list's head are not updated in place
+    B, C = 0x20000, 0x30000
+    assert plan(CTX=B, KV=B) == 2 and plan(NEW=B, KV=B) == 2 and plan(KV=B, HEAD=C, USED=C) == 2
 
 
 def append(QKV=A, S=4, HQ=4, HKV=2, D=128, WQ=A, WK=A, eps=1e-6, CS=A, P=8, POS=A, SLOT=A, Q=A, KC=A, VC=A, NP=8, page=16):
@@ -109,7 +112,7 @@ def test_attn_refusals():
         assert f(S=(1 << 24) - 1, HQ=16) == 2
     assert call("osc_attn_workspace", 4, 2, 4, 2, 128, 16, 4, None) == 1
     assert attn(NP=0) == 2 and attn(NP=1 << 27) == 2
-    for s in (0.0, -1.0, float("inf"), float("nan")):
+    for s in (0.0, -1.0, float("inf"), float("nan"), 3e38):            # the last: over the range times log2 e
         assert attn(scale=s) == 2, s
     for k in ("Q", "KC", "VC", "T", "CU", "KV", "O"):
         assert attn(**{k: None}) == 1, k

@@ -170,6 +170,9 @@ def test_refusals():
         pages.release([0, 0])
     with pytest.raises(ValueError):
         pages.release([R])
+    x = torch.zeros((1, H), dtype=torch.bfloat16, device=DEV)
+    with pytest.raises(ValueError):
+        b.forward(x, None, 1, pages, None, None, x)
     with pytest.raises(ValueError):
         blk.Attention(b.attention.qkv, b.attention.out, HQ, HKV + 1, D)
     with pytest.raises(ValueError):

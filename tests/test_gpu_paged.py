@@ -236,12 +236,14 @@ def attn_reference(p):
     out = torch.zeros(S, HQ, D, dtype=torch.float64, device=DEV)
     tol = torch.zeros_like(out)
     for r in range(p["R"]):
-        kv, a, n = p["kv"][r], p["cu"][r], p["cu"][r + 1] - p["cu"][r]
+        a, b = (min(max(c, 0), S) for c in p["cu"][r:r + 2])
+        n, first = b - a, max(p["kv"][r], 0) - (b - a) - max(p["cu"][r + 1] - S, 0)  # token i sees keys up to first + i
+        kv = min(max(first + n, 0), p["MB"] * page)
         ids = torch.tensor(p["table"][r], device=DEV)[torch.arange(kv, device=DEV) // page]
         ok = (ids >= 0) & (ids < p["NP"])
         ids = ids.clamp(0, p["NP"] - 1)
         off = torch.arange(kv, device=DEV) % page
-        hidden = torch.arange(kv, device=DEV)[None] > (kv - n + torch.arange(n, device=DEV))[:, None]
+        hidden = torch.arange(kv, device=DEV)[None] > (first + torch.arange(n, device=DEV))[:, None]
         hidden = hidden | ~ok[None]
         for h in range(HKV):
             k = p["KC"][ids, h, off].double()
@@ -331,12 +333,36 @@ def test_attn_rows_outside_the_requests_stay_as_they_were():
 
 
 def test_attn_lengths_off_their_ranges_stay_inside():
-    """Counts past S and lengths past the table are taken into range."""
+    """Counts past S and lengths past the table: the other tokens' keys are as if all had been there."""
     p = build([(64, 8), (64, 8)], 4, 2, 128, 16, 2, MB=4)
-    q = dict(p, cu=[-3, 8, 10 ** 9], kv=[10 ** 9, -7])
-    O = attend(q)
-    r = dict(p, kv=[64, 0])
-    check_attn(r, O)
+    for cu, kv in (([-3, 8, 10 ** 9], [10 ** 9, -7]), ([0, 8, 2 ** 31 - 1], [2 ** 31 - 1, 2 ** 31 - 1]), ([-2 ** 31, 8, 16], [-2 ** 31, 64])):
+        check_attn(dict(p, cu=cu, kv=kv))
+
+
+@pytest.mark.parametrize("idle", [0, 40])
+def test_attn_tokens_that_the_plan_does_not_map_change_nothing_for_the_others(idle):
+    """5 tokens too many for the table's pages, and 5 for the call's rows: what is left is the request without them."""
+    p = build([(70, 1), (512, 30), *[(0, 0)] * idle], 4, 2, 64, 64, 21, MB=8)
+    ref, tol = attn_reference(p)
+    ok = lambda O, n: bool(((O[:n].double() - ref[:n]).abs() <= tol[:n]).all())
+    long = dict(p, Q=torch.cat([p["Q"], p["Q"][:5]]), S=36, cu=[0, 1] + [36] * (idle + 1), kv=[70, 517] + [0] * idle)
+    O = attend(long)
+    assert ok(O, 31) and bool(torch.isfinite(O.float()).all())
+    O = attend(dict(p, S=26), S=26)
+    assert ok(O, 26)
+
+
+def test_attn_chunk_and_tokens_among_idle_requests():
+    """As many requests as a call may have, most of them idle, and fewer tokens than requests: a chunk on single-token tiles."""
+    reqs = [(0, 0)] * 4096
+    reqs[5], reqs[70], reqs[71], reqs[4095] = (900, 1), (300, 200), (17, 0), (65, 65)
+    check_attn(build(reqs, 8, 2, 64, 64, 22, MB=16))
+
+
+def test_attn_chunks_of_the_most_requests():
+    """More tokens than the 4096 requests: large tiles of one or two tokens, found among many."""
+    rng = np.random.RandomState(23)
+    check_attn(build([(int(k), min(int(k), 2)) for k in rng.randint(0, 40, 4096)], 2, 1, 64, 16, 23, MB=3))
 
 
 def test_attn_large_scores_and_growing_maximum():

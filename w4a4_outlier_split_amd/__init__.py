@@ -225,58 +225,64 @@ def osc_build_table_multi(Xcal, R: int, H: int, G: int, alpha: float, rho: float
 
 # ---- between the projections: norm, paged cache, attention
 
-def _fits(call: str, *pairs) -> None:
-    """The tensors of ``pairs`` (tensor or None or address, bytes the call reads or writes) lie
-    contiguously on the current device and hold that many bytes."""
-    dev = torch.cuda.current_device()
-    for t, need in pairs:
-        if t is None or isinstance(t, int):
-            continue
-        if t.get_device() != dev:
-            raise OscError(2, call, f"a tensor on {t.device}, the current device is cuda:{dev}")
-        if not t.is_contiguous() or t.nbytes < need:
-            raise OscError(2, call, f"a tensor of {t.nbytes} bytes, strides {tuple(t.stride())}, where {need} contiguous "
-                                    "bytes are needed")
+def _at(call: str, dev: int, t, need: int) -> Optional[int]:
+    """Address of a tensor (or an address, or None) of which the call reads or writes ``need`` contiguous
+    bytes on the current device ``dev``."""
+    if t is None or type(t) is int:
+        return t
+    if t.get_device() != dev:
+        raise OscError(2, call, f"a tensor on {t.device}, the current device is cuda:{dev}")
+    if not t.is_contiguous() or t.nbytes < need:
+        raise OscError(2, call, f"a tensor of {t.nbytes} bytes, strides {tuple(t.stride())}, where {need} contiguous "
+                                "bytes are needed")
+    return t.data_ptr()
 
 
 def osc_rmsnorm_quant(X, RES, W, S: int, H: int, eps: float, G: int, L, m: int, afmt: int, RES_OUT, QX, SX, B,
                       stream=None) -> None:
     """r = X + RES to RES_OUT (both None: r = X); the RMS norm of r, quantized as osc_quant_act_multi."""
+    c = "osc_rmsnorm_quant"
     keep, lp = _table(L)
     n = 2 * S * H
     g = max(G, 1)  # the library refuses a group size it does not have
     if keep is not None and keep.size < H // g * m:
-        raise OscError(3, "osc_rmsnorm_quant", f"{keep.size} table entries for {H // g} groups of {m}")
-    _fits("osc_rmsnorm_quant", (X, n), (RES, n), (W, 2 * H), (RES_OUT, n), (QX, code_bytes(S, H, afmt)),
-          (SX, scale_bytes(S, H, g, afmt)), (B, 2 * side_elems(S, H, g, m)))
-    _check(_lib.osc_rmsnorm_quant(_ptr(X), _ptr(RES), _ptr(W), S, H, eps, G, lp, m, afmt, _ptr(RES_OUT), _ptr(QX), _ptr(SX),
-                                  _ptr(B), _stream(stream)), "osc_rmsnorm_quant")
+        raise OscError(3, c, f"{keep.size} table entries for {H // g} groups of {m}")
+    d = torch.cuda.current_device()
+    _check(_lib.osc_rmsnorm_quant(_at(c, d, X, n), _at(c, d, RES, n), _at(c, d, W, 2 * H), S, H, eps, G, lp, m, afmt,
+                                  _at(c, d, RES_OUT, n), _at(c, d, QX, code_bytes(S, H, afmt)),
+                                  _at(c, d, SX, scale_bytes(S, H, g, afmt)), _at(c, d, B, 2 * side_elems(S, H, g, m)),
+                                  _stream(stream)), c)
 
 
 def osc_rmsnorm(X, RES, W, S: int, H: int, eps: float, RES_OUT, Y, stream=None) -> None:
     """The same norm written out: Y [S, H] bf16."""
+    c = "osc_rmsnorm"
     n = 2 * S * H
-    _fits("osc_rmsnorm", (X, n), (RES, n), (W, 2 * H), (RES_OUT, n), (Y, n))
-    _check(_lib.osc_rmsnorm(_ptr(X), _ptr(RES), _ptr(W), S, H, eps, _ptr(RES_OUT), _ptr(Y), _stream(stream)), "osc_rmsnorm")
+    d = torch.cuda.current_device()
+    _check(_lib.osc_rmsnorm(_at(c, d, X, n), _at(c, d, RES, n), _at(c, d, W, 2 * H), S, H, eps, _at(c, d, RES_OUT, n),
+                            _at(c, d, Y, n), _stream(stream)), c)
 
 
 def osc_page_plan(CTX, NEW, R: int, page: int, NP: int, FREE, F: int, HEAD, T: int, TABLE, MB: int, CU, KV, SLOT, POS, USED,
                   stream=None) -> None:
     """Page tables and slot maps of one step from request lengths (all int32 device tensors)."""
-    _fits("osc_page_plan", (CTX, 4 * R), (NEW, 4 * R), (FREE, 4 * F), (HEAD, 4), (TABLE, 4 * R * MB), (CU, 4 * R + 4), (KV, 4 * R),
-          (SLOT, 4 * T), (POS, 4 * T), (USED, 4))
-    _check(_lib.osc_page_plan(_ptr(CTX), _ptr(NEW), R, page, NP, _ptr(FREE), F, _ptr(HEAD), T, _ptr(TABLE), MB, _ptr(CU), _ptr(KV),
-                              _ptr(SLOT), _ptr(POS), _ptr(USED), _stream(stream)), "osc_page_plan")
+    c = "osc_page_plan"
+    d = torch.cuda.current_device()
+    _check(_lib.osc_page_plan(_at(c, d, CTX, 4 * R), _at(c, d, NEW, 4 * R), R, page, NP, _at(c, d, FREE, 4 * F), F,
+                              _at(c, d, HEAD, 4), T, _at(c, d, TABLE, 4 * R * MB), MB, _at(c, d, CU, 4 * R + 4),
+                              _at(c, d, KV, 4 * R), _at(c, d, SLOT, 4 * T), _at(c, d, POS, 4 * T), _at(c, d, USED, 4),
+                              _stream(stream)), c)
 
 
 def osc_qkv_append(QKV, S: int, HQ: int, HKV: int, D: int, WQ, WK, eps: float, CS, P: int, POS, SLOT, Q, KC, VC, NP: int,
                    page: int, stream=None) -> None:
     """QKV rows [S, (HQ + 2 HKV) D]: normed and rotated queries to Q, keys and values to their slots."""
-    c = 2 * NP * HKV * page * D
-    _fits("osc_qkv_append", (QKV, 2 * S * (HQ + 2 * HKV) * D), (WQ, 2 * D), (WK, 2 * D), (CS, 4 * P * D), (POS, 4 * S), (SLOT, 4 * S),
-          (Q, 2 * S * HQ * D), (KC, c), (VC, c))
-    _check(_lib.osc_qkv_append(_ptr(QKV), S, HQ, HKV, D, _ptr(WQ), _ptr(WK), eps, _ptr(CS), P, _ptr(POS), _ptr(SLOT), _ptr(Q),
-                               _ptr(KC), _ptr(VC), NP, page, _stream(stream)), "osc_qkv_append")
+    c = "osc_qkv_append"
+    d = torch.cuda.current_device()
+    n = 2 * NP * HKV * page * D
+    _check(_lib.osc_qkv_append(_at(c, d, QKV, 2 * S * (HQ + 2 * HKV) * D), S, HQ, HKV, D, _at(c, d, WQ, 2 * D), _at(c, d, WK, 2 * D),
+                               eps, _at(c, d, CS, 4 * P * D), P, _at(c, d, POS, 4 * S), _at(c, d, SLOT, 4 * S),
+                               _at(c, d, Q, 2 * S * HQ * D), _at(c, d, KC, n), _at(c, d, VC, n), NP, page, _stream(stream)), c)
 
 
 def osc_attn_workspace(S: int, R: int, HQ: int, HKV: int, D: int, page: int, MB: int) -> int:
@@ -290,7 +296,9 @@ def osc_attn_paged(Q, KC, VC, S: int, R: int, HQ: int, HKV: int, D: int, page: i
                    scale: float, O, WS, stream=None) -> None:
     """Causal attention of the new tokens of R requests over the paged cache; WS: a tensor of at least
     osc_attn_workspace bytes, or None where that is 0."""
-    c, n = 2 * NP * HKV * page * D, 2 * S * HQ * D
-    _fits("osc_attn_paged", (Q, n), (KC, c), (VC, c), (TABLE, 4 * R * MB), (CU, 4 * R + 4), (KV, 4 * R), (O, n), (WS, 0))
-    _check(_lib.osc_attn_paged(_ptr(Q), _ptr(KC), _ptr(VC), S, R, HQ, HKV, D, page, MB, NP, _ptr(TABLE), _ptr(CU), _ptr(KV), scale,
-                               _ptr(O), _ptr(WS), 0 if WS is None else WS.nbytes, _stream(stream)), "osc_attn_paged")
+    c = "osc_attn_paged"
+    d = torch.cuda.current_device()
+    n, q = 2 * NP * HKV * page * D, 2 * S * HQ * D
+    _check(_lib.osc_attn_paged(_at(c, d, Q, q), _at(c, d, KC, n), _at(c, d, VC, n), S, R, HQ, HKV, D, page, MB, NP,
+                               _at(c, d, TABLE, 4 * R * MB), _at(c, d, CU, 4 * R + 4), _at(c, d, KV, 4 * R), scale, _at(c, d, O, q),
+                               _at(c, d, WS, 0), 0 if WS is None else WS.nbytes, _stream(stream)), c)

@@ -315,7 +315,9 @@ class Block:
     def forward(self, X, res, S: int, pages: Pages, cache: LayerCache, bufs, Y, stream=None):
         """X: [S, H] bf16, the block before's Y; res: the residual stream, updated in place.  The first
         block takes res = None: X is the stream then, and is updated in place.  Writes the MLP's
-        output to Y (not X) and returns the stream."""
+        output to Y (neither X nor res) and returns the stream."""
+        if Y is X or Y is res:
+            raise ValueError("Y is written while X and the residual stream are in use")
         self.attention.qkv.norm_quantize(X, res, self.w_attn, self.eps, S, bufs["attn"]["x"], stream)
         stream_rows = X if res is None else res
         self.attention.forward_quantized(S, pages, cache, bufs["attn"], bufs["y"], stream)

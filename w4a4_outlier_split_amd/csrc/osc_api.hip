@@ -326,6 +326,8 @@ osc_status osc_page_plan(const int32_t* CTX, const int32_t* NEW, int R, int page
   if (!aligned4(CTX) || !aligned4(NEW) || !aligned4(FREE) || !aligned4(HEAD) || !aligned4(TABLE) || !aligned4(CU) ||
       !aligned4(KV) || !aligned4(SLOT) || !aligned4(POS) || !aligned4(USED))
     return OSC_E_ALIGN;
+  // every workgroup reads the inputs, one of them writes these outputs
+  if ((R > 0 && (KV == CTX || KV == NEW)) || USED == HEAD) return OSC_E_SHAPE;
   osc::PlanArgs a{CTX, NEW, R, sh, NP, FREE, F, HEAD, T, TABLE, MB, CU, KV, SLOT, POS, USED};
   return from_hip(osc::launch_page_plan(a, static_cast<hipStream_t>(stream)));
 }
@@ -370,6 +372,8 @@ osc_status osc_attn_paged(const void* Q, const void* KC, const void* VC, int S, 
   if (st != OSC_OK) return st;
   const int sh = page_shift(page);
   if (NP < 1 || ((long long)NP << sh) > 0x7FFFFFFFLL || !positive(scale)) return OSC_E_SHAPE;
+  const float scale_log2 = scale * 1.4426950408889634f;
+  if (!isfinite(scale_log2)) return OSC_E_SHAPE;
   if (S == 0 || R == 0) return OSC_OK;
   if (!Q || !KC || !VC || !TABLE || !CU || !KV || !O) return OSC_E_NULL;
   const osc::AttnPlan p = osc::attn_plan(S, R, HQ, HKV, D);
@@ -378,7 +382,7 @@ osc_status osc_attn_paged(const void* Q, const void* KC, const void* VC, int S, 
   if (!aligned16(Q) || !aligned16(KC) || !aligned16(VC) || !aligned16(O) || !aligned16(WS) || !aligned4(TABLE) ||
       !aligned4(CU) || !aligned4(KV))
     return OSC_E_ALIGN;
-  osc::AttnArgs a{Q,  KC,   VC, S,  R,  HQ, HKV, HQ / HKV, sh, page - 1, MB, NP, TABLE, CU, KV, scale * 1.4426950408889634f,
+  osc::AttnArgs a{Q,  KC,   VC, S,  R,  HQ, HKV, HQ / HKV, sh, page - 1, MB, NP, TABLE, CU, KV, scale_log2,
                   O,  nullptr, nullptr, nullptr, p.target};
   if (p.ws_bytes > 0) {  // notes, then 2 and D values a row
     const long notes = (long)HKV * p.target;

@@ -54,8 +54,9 @@ __device__ __forceinline__ float neg_inf() { return -__builtin_inff(); }
 
 struct Tile {
   int row0, rows;  // the tile's rows (token, head of the group): first and end, inside the request
-  int tok0, n;     // the request's first token and token count
-  int kv;          // keys of the request
+  int tok0;        // the request's first token
+  int first;       // position of that token: token i sees the keys up to first + i
+  int kv;          // keys of the request that may be read
   const int32_t* pages;
   int lo, hi;      // the steps of keys to take (64 keys each)
   long part;       // first row of the workspace for a part of a tile, -1: the whole tile
@@ -138,9 +139,9 @@ __device__ __forceinline__ void small_tile(const AttnArgs& a, const Tile& t, int
     for (int i = 0; i < 8; ++i) q[s][i] = (__bf16)0.0f;
     if (live) q[s] = *reinterpret_cast<const v8bf*>(static_cast<const __bf16*>(a.Q) + out_row * D + s * 32 + grp * 8);
   }
-  const int last = live ? t.kv - t.n + tok : -1;  // the last key of the lane's row
+  const int last = live ? t.first + tok : -1;  // the last key of the lane's row
   const int tok_end = ((t.row0 + 16 < t.rows ? t.row0 + 16 : t.rows) - 1) / g;
-  const int kend = clampi(t.kv - t.n + tok_end + 1, 0, t.kv);
+  const int kend = clampi(t.first + tok_end + 1, 0, t.kv);
   const int lo = 2 * t.lo, hi = clampi((kend + 31) >> 5, lo, 2 * t.hi);  // steps of 32 keys
 
   v4f o[DB];
@@ -317,7 +318,7 @@ __device__ __forceinline__ void large_tile(const AttnArgs& a, const Tile& t, int
     for (int i = 0; i < 8; ++i) q[s][i] = (__bf16)0.0f;
     if (live) q[s] = *reinterpret_cast<const v8bf*>(static_cast<const __bf16*>(a.Q) + out_row * D + s * 16 + half * 8);
   }
-  const int base = t.kv - t.n;
+  const int base = t.first;
   const int last = live ? base + tok - 8 * half : -1;  // the last key the row sees, from the lane's first
   // the first row of the wavefront sees the fewest keys: tiles up to it need no mask
   const int wfirst = base + row0 / g;
@@ -492,16 +493,21 @@ __device__ __forceinline__ void large_tile(const AttnArgs& a, const Tile& t, int
 // ------------------------------------------------------------------ the cuts
 // The tiles of ROWS rows of a request and their lengths: tile i sees the keys up to its last token, base + (i +
 // 1) tau with tau tokens a tile, and the i tiles ahead of it together (exactly, in whole numbers) before(i).
-// WHOLE: every tile has the length 1.
+// WHOLE: every tile has the length 1.  Tokens behind the call's S rows count for the others' positions, and keys
+// behind the table's pages for the tokens', but neither is looked at.
 template <int ROWS, bool WHOLE>
 struct Request {
-  int c0, n, kv, tiles;
+  int c0, n, first, kv, tiles;
   long base, tau;
   __device__ __forceinline__ Request(const AttnArgs& a, int r) {
     c0 = clampi(a.CU[r], 0, a.S);
     const int c1 = clampi(a.CU[r + 1], 0, a.S);
     n = c1 > c0 ? c1 - c0 : 0;
-    kv = clampi(a.KV[r], 0, (int)((long)a.MB << a.sh));
+    const int held = a.KV[r] > 0 ? a.KV[r] : 0, beyond = a.CU[r + 1] > a.S ? a.CU[r + 1] - a.S : 0;
+    const long at = (long)held - n - beyond;
+    constexpr long most = 1l << 30;  // as many positions as a table can hold: 32 bits do from here on
+    first = (int)(at < -most ? -most : at < most ? at : most);
+    kv = clampi(first + n, 0, (int)((long)a.MB << a.sh));
     tiles = (n * a.g + ROWS - 1) / ROWS;
     base = WHOLE ? 1 : kv > n ? kv - n : 0;
     tau = WHOLE ? 0 : (ROWS + a.g - 1) / a.g;
@@ -626,13 +632,13 @@ __device__ __forceinline__ void each_tile(const AttnArgs& a, Body body) {
       const long len = WHOLE ? 1 : q.before(i + 1) - q.before(i);
       Tile t;
       t.tok0 = __builtin_amdgcn_readfirstlane(q.c0);
-      t.n = __builtin_amdgcn_readfirstlane(q.n);
+      t.first = __builtin_amdgcn_readfirstlane(q.first);
       t.kv = __builtin_amdgcn_readfirstlane(q.kv);
       t.pages = a.TABLE + (long)r * a.MB;
-      t.rows = t.n * a.g;
+      t.rows = __builtin_amdgcn_readfirstlane(q.n) * a.g;
       t.row0 = (WHOLE ? q.tiles - 1 - i : i) * ROWS;
       const int tile_end = t.row0 + ROWS < t.rows ? t.row0 + ROWS : t.rows;
-      const int steps = (clampi(t.kv - t.n + (tile_end - 1) / a.g + 1, 0, t.kv) + 63) >> 6;
+      const int steps = (clampi(t.first + (tile_end - 1) / a.g + 1, 0, t.kv) + 63) >> 6;
       t.lo = 0, t.hi = steps, t.part = -1;
       if (!WHOLE) {
         if (begin < first) t.lo = (int)divide((first - begin) * steps, len);
