@@ -298,6 +298,17 @@ def test_attn_cuts(reqs, HQ, HKV):
     check_attn(build(reqs, HQ, HKV, 64, 64, len(reqs) + HQ, MB=330))
 
 
+@pytest.mark.parametrize("reqs,D,page", [([(3300, 3300)], 64, 16), ([(2100, 1700)], 128, 64), ([(1500, 1500), (0, 0), (900, 700), (601, 600), (1, 1), (520, 520)], 64, 64),
+                                         ([(30, 30)] * 112, 64, 32), ([(900, 1), (1700, 1700)], 128, 256), ([(1700, 1700), (30000, 1), (70, 60)], 128, 64),
+                                         ([(20000, 20), (3300, 3300)], 64, 128)])
+def test_attn_many_tiles(reqs, D, page):
+    """Tiles enough to leave them whole: one request, several, and such with a context so long that they are cut all the same."""
+    p = build(reqs, 64 if D == 64 else 128, 8, D, page, len(reqs) + D)
+    if len(reqs) > 3:
+        p["table"][0][3 if len(reqs) < 20 else 0] = -1
+    check_attn(p)
+
+
 def test_attn_rows_that_see_nothing_are_zero():
     p = build([(5, 5), (40, 40), (70, 2)], 4, 2, 128, 16, 7)
     p["kv"] = [3, 0, 70]  # fewer keys than tokens: the first ones see none

@@ -361,7 +361,7 @@ osc_status osc_attn_workspace(int S, int R, int HQ, int HKV, int D, int page, in
   const osc_status st = check_attn(S, R, HQ, HKV, D, page, MB);
   if (st != OSC_OK) return st;
   if (!bytes) return OSC_E_NULL;
-  *bytes = S == 0 || R == 0 ? 0 : osc::attn_plan(S, R, HQ, HKV, D).ws_bytes;
+  *bytes = S == 0 || R == 0 ? 0 : osc::attn_plan(S, R, HQ, HKV, D, (long)MB * page).ws_bytes;
   return OSC_OK;
 }
 
@@ -376,7 +376,7 @@ osc_status osc_attn_paged(const void* Q, const void* KC, const void* VC, int S, 
   if (!isfinite(scale_log2)) return OSC_E_SHAPE;
   if (S == 0 || R == 0) return OSC_OK;
   if (!Q || !KC || !VC || !TABLE || !CU || !KV || !O) return OSC_E_NULL;
-  const osc::AttnPlan p = osc::attn_plan(S, R, HQ, HKV, D);
+  const osc::AttnPlan p = osc::attn_plan(S, R, HQ, HKV, D, (long)MB * page);
   if (p.ws_bytes > 0 && !WS) return OSC_E_NULL;
   if (ws_bytes < p.ws_bytes) return OSC_E_SHAPE;
   if (!aligned16(Q) || !aligned16(KC) || !aligned16(VC) || !aligned16(O) || !aligned16(WS) || !aligned4(TABLE) ||

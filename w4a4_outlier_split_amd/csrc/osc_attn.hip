@@ -493,13 +493,13 @@ __device__ __forceinline__ void large_tile(const AttnArgs& a, const Tile& t, int
 // ------------------------------------------------------------------ the cuts
 // The tiles of ROWS rows of a request and their lengths: tile i sees the keys up to its last token, base + (i +
 // 1) tau with tau tokens a tile, and the i tiles ahead of it together (exactly, in whole numbers) before(i).
-// WHOLE: every tile has the length 1.  Tokens behind the call's S rows count for the others' positions, and keys
+// whole: every tile has the length 1.  Tokens behind the call's S rows count for the others' positions, and keys
 // behind the table's pages for the tokens', but neither is looked at.
-template <int ROWS, bool WHOLE>
+template <int ROWS>
 struct Request {
   int c0, n, first, kv, tiles;
   long base, tau;
-  __device__ __forceinline__ Request(const AttnArgs& a, int r) {
+  __device__ __forceinline__ Request(const AttnArgs& a, int r, bool whole) {
     c0 = clampi(a.CU[r], 0, a.S);
     const int c1 = clampi(a.CU[r + 1], 0, a.S);
     n = c1 > c0 ? c1 - c0 : 0;
@@ -509,8 +509,8 @@ struct Request {
     first = (int)(at < -most ? -most : at < most ? at : most);
     kv = clampi(first + n, 0, (int)((long)a.MB << a.sh));
     tiles = (n * a.g + ROWS - 1) / ROWS;
-    base = WHOLE ? 1 : kv > n ? kv - n : 0;
-    tau = WHOLE ? 0 : (ROWS + a.g - 1) / a.g;
+    base = whole ? 1 : kv > n ? kv - n : 0;
+    tau = whole ? 0 : (ROWS + a.g - 1) / a.g;
   }
   __device__ __forceinline__ long before(long i) const { return i * base + tau * (i * (i + 1) / 2); }
   __device__ __forceinline__ long all() const { return before(tiles); }
@@ -519,6 +519,21 @@ struct Request {
 __device__ __forceinline__ long lane_of(long v, int src) {
   const unsigned lo = __builtin_amdgcn_readlane((int)v, src), hi = __builtin_amdgcn_readlane((int)(v >> 32), src);
   return (long)((unsigned long)hi << 32 | lo);
+}
+
+__device__ __forceinline__ long uniform(long v) {  // a value that all lanes share, into scalar registers
+  const unsigned lo = __builtin_amdgcn_readfirstlane((int)v), hi = __builtin_amdgcn_readfirstlane((int)(v >> 32));
+  return (long)((unsigned long)hi << 32 | lo);
+}
+
+// the next request with tokens behind r, of which the caller knows
+__device__ __forceinline__ int next_request(const AttnArgs& a, int r) {
+  for (int from = r + 1; from < a.R; from += 64) {
+    const int x = from + (int)(threadIdx.x & 63);
+    const unsigned long long has = __ballot(x < a.R && clampi(a.CU[x + 1], 0, a.S) > clampi(a.CU[x], 0, a.S));
+    if (has) return from + __ffsll(has) - 1;
+  }
+  return r;
 }
 
 // a / b for 0 <= a, 0 < b, a / b < 2^50, by way of 64-bit floating point (a division of integers takes five times as long)
@@ -530,10 +545,11 @@ __device__ __forceinline__ long divide(long a, long b) {
 }
 
 // All tiles of a key head in a row, cut into `parts` equal parts (WHOLE: a tile each).  A wavefront's lanes hold
-// a share of the requests each.
-template <int ROWS, bool WHOLE>
+// a share of the requests each.  IF: no parts unless the lengths call for this way of the two: tiles are left whole
+// where none is longer than a CU's share of all.
+template <int ROWS, bool WHOLE, bool IF>
 struct Cuts {
-  typedef Request<ROWS, WHOLE> Req;
+  typedef Request<ROWS> Req;
   long all, upto;  // the row's length; the lane's requests end there
   long mine;       // length of the lane's requests
   long each;       // all / parts
@@ -546,25 +562,33 @@ struct Cuts {
     r0 = lane * per < a.R ? lane * per : a.R;
     r1 = r0 + per < a.R ? r0 + per : a.R;
     long most = 0;  // the longest tile
+    long count = 0, counted;  // tiles of the lane's requests, and up to their end
     mine = 0;
 #pragma unroll 4
     for (int r = r0; r < r1; ++r) {
-      const Req q(a, r);
+      const Req q(a, r, WHOLE && !IF);
       mine += q.all();
       const long last = q.tiles > 0 ? q.base + q.tiles * q.tau : 0;
       most = last > most ? last : most;
+      count += q.tiles;
     }
-    upto = mine;
+    upto = mine, counted = count;
     const int lanes = (a.R + per - 1) / per;
     for (int d = 1; d < lanes; d <<= 1) {  // up to each lane
       const long up = __shfl_up(upto, d), other = __shfl_up(most, d);
+      const long tiles = IF && WHOLE ? __shfl_up(counted, d) : 0;
       if (lane >= d) {
-        upto += up;
+        upto += up, counted += tiles;
         most = other > most ? other : most;
       }
     }
     all = lane_of(upto, lanes - 1);
     most = lane_of(most, lanes - 1);
+    const bool even = most * kCUs <= all * a.HKV;
+    if (IF && WHOLE) {
+      mine = count, upto = counted;
+      all = lane_of(upto, lanes - 1);
+    }
     if (WHOLE) {
       parts = (int)all;
       each = 1, over = 0;
@@ -577,6 +601,7 @@ struct Cuts {
       each = divide(all, parts);
       over = (int)(all - each * parts);
     }
+    if (IF && even != WHOLE) parts = 0;
   }
   // where part w begins
   __device__ __forceinline__ long cut(int w) const { return each * w + over * w / parts; }
@@ -587,7 +612,7 @@ struct Cuts {
     long from = upto - mine;
     int hit = r0, i = 0;
     for (int x = r0; x < r1; ++x) {
-      const Req q(a, x);
+      const Req q(a, x, WHOLE);
       const long len = q.all();
       if (at - from < len) {
         if (WHOLE) {
@@ -614,66 +639,79 @@ struct Cuts {
 
 // Workgroup: key head h = blockIdx % HKV (an XCD takes every eighth workgroup, so with eight key heads each XCD's
 // L2 holds one head's cache), part w = blockIdx / HKV of the head's row; body(t, h) for each tile of the part in
-// turn.  WHOLE takes a request's later tiles first, which see the most keys, and all from their first key, so that
+// turn.  Whole tiles take a request's later tiles first, which see the most keys, and all from their first key, so that
 // the tiles that run together stream the same keys.  Otherwise the workgroup notes a tile that begins in its part
 // and goes on behind it, for the join.
-template <int ROWS, bool WHOLE, typename Body>
+// What outlives a tile is held in scalar registers and no more than needed: the body needs all vector registers
+// that there are.
+template <int ROWS, bool WHOLE, bool IF, typename Body>
 __device__ __forceinline__ void each_tile(const AttnArgs& a, Body body) {
-  const Cuts<ROWS, WHOLE> cuts(a);
   const int h = blockIdx.x % a.HKV, w = blockIdx.x / a.HKV;
-  int4 note = {0, 0, 0, 0};
-  if (w < cuts.parts && cuts.all > 0) {
-    const long first = cuts.cut(w), end = cuts.cut(w + 1);
-    int r, i;
-    long begin;
-    cuts.find(a, first, r, i, begin);
-    for (;;) {
-      const Request<ROWS, WHOLE> q(a, r);
-      const long len = WHOLE ? 1 : q.before(i + 1) - q.before(i);
-      Tile t;
-      t.tok0 = __builtin_amdgcn_readfirstlane(q.c0);
-      t.first = __builtin_amdgcn_readfirstlane(q.first);
-      t.kv = __builtin_amdgcn_readfirstlane(q.kv);
-      t.pages = a.TABLE + (long)r * a.MB;
-      t.rows = __builtin_amdgcn_readfirstlane(q.n) * a.g;
-      t.row0 = (WHOLE ? q.tiles - 1 - i : i) * ROWS;
-      const int tile_end = t.row0 + ROWS < t.rows ? t.row0 + ROWS : t.rows;
-      const int steps = (clampi(t.first + (tile_end - 1) / a.g + 1, 0, t.kv) + 63) >> 6;
-      t.lo = 0, t.hi = steps, t.part = -1;
-      if (!WHOLE) {
-        if (begin < first) t.lo = (int)divide((first - begin) * steps, len);
-        if (begin + len > end) t.hi = (int)divide((end - begin) * steps, len);
-        // a tile of several parts: in the workgroup's second place where it begins there, in the first behind a cut
-        if (begin < first || begin + len > end)
-          t.part = (((long)h * a.target + w) * 2 + (begin < first ? 0 : 1)) * ROWS;
-        if (begin >= first && begin + len > end) {
-          int ns = 2;
-          while (w + ns < cuts.parts && cuts.cut(w + ns) < begin + len) ++ns;
-          note = int4{ns, t.row0, t.rows, t.tok0};
+  auto noted = [&](const int4& note) {
+    if (!WHOLE && threadIdx.x == 0) a.NOTE[h * a.target + w] = note;
+  };
+  bool any;
+  int r = 0, i = 0, parts, over;
+  long begin = 0, first = 0, end = 0, each;
+  {
+    const Cuts<ROWS, WHOLE, IF> cuts(a);
+    any = w < cuts.parts && cuts.all > 0;
+    if (any) {
+      first = uniform(cuts.cut(w)), end = uniform(cuts.cut(w + 1));
+      cuts.find(a, first, r, i, begin);
+    }
+    parts = __builtin_amdgcn_readfirstlane(cuts.parts), over = __builtin_amdgcn_readfirstlane(cuts.over);
+    each = uniform(cuts.each);
+  }
+  if (!any) return noted(int4{0, 0, 0, 0});
+  for (;;) {
+    const Request<ROWS> q(a, r, WHOLE);
+    const long len = uniform(WHOLE ? 1 : q.before(i + 1) - q.before(i));
+    const int tiles = __builtin_amdgcn_readfirstlane(q.tiles);
+    Tile t;
+    t.tok0 = __builtin_amdgcn_readfirstlane(q.c0);
+    t.first = __builtin_amdgcn_readfirstlane(q.first);
+    t.kv = __builtin_amdgcn_readfirstlane(q.kv);
+    t.pages = a.TABLE + (long)r * a.MB;
+    t.rows = __builtin_amdgcn_readfirstlane(q.n) * a.g;
+    t.row0 = (WHOLE ? tiles - 1 - i : i) * ROWS;
+    const int tile_end = t.row0 + ROWS < t.rows ? t.row0 + ROWS : t.rows;
+    const int steps = (clampi(t.first + (tile_end - 1) / a.g + 1, 0, t.kv) + 63) >> 6;
+    t.lo = 0, t.hi = __builtin_amdgcn_readfirstlane(steps), t.part = -1;
+    const bool last = WHOLE || begin + len >= end;
+    if (!WHOLE) {
+      if (begin < first) t.lo = (int)uniform(divide((first - begin) * steps, len));
+      if (begin + len > end) t.hi = (int)uniform(divide((end - begin) * steps, len));
+      // a tile of several parts: in the workgroup's second place where it begins there, in the first behind a cut
+      if (begin < first || begin + len > end)
+        t.part = (((long)h * a.target + w) * 2 + (begin < first ? 0 : 1)) * ROWS;
+      if (last) {
+        int ns = 0;
+        if (begin >= first && begin + len > end) {  // the parts that begin in the tile: kMaxCuts and two at most
+          const int p = w + 1 + (int)(threadIdx.x & 63);
+          ns = 1 + __popcll(__ballot(p < parts && each * p + over * p / parts < begin + len));
         }
-      }
-      body(t, h);
-      begin += len;
-      if (WHOLE || begin >= end) break;
-      if (++i == q.tiles) {  // the next request; behind idle ones it is looked up
-        i = 0, ++r;
-        if (Request<ROWS, WHOLE>(a, r).tiles == 0) cuts.find(a, begin, r, i, begin);
+        noted(int4{ns, t.row0, t.rows, t.tok0});
+      } else {
+        begin += len;
+        if (++i == tiles) i = 0, r = next_request(a, r);
       }
     }
+    body(t, h);
+    if (last) return;
   }
-  if (!WHOLE && threadIdx.x == 0) a.NOTE[h * a.target + w] = note;
 }
 
 template <int D>
 __global__ __launch_bounds__(256, 2) void k_attn_small(AttnArgs a) {
   __shared__ __align__(16) float lds[128 + 4 * 16 * (D + 4)];
-  each_tile<kSmallRows, false>(a, [&](const Tile& t, int h) { small_tile<D>(a, t, h, lds); });
+  each_tile<kSmallRows, false, false>(a, [&](const Tile& t, int h) { small_tile<D>(a, t, h, lds); });
 }
 
-template <int D, bool WHOLE>
+template <int D, bool WHOLE, bool IF>
 __global__ __launch_bounds__(512, 2) void k_attn_large(AttnArgs a) {
   extern __shared__ __align__(16) uint8_t dlds[];
-  each_tile<kLargeRows, WHOLE>(a, [&](const Tile& t, int h) { large_tile<D>(a, t, h, dlds); });
+  each_tile<kLargeRows, WHOLE, IF>(a, [&](const Tile& t, int h) { large_tile<D>(a, t, h, dlds); });
 }
 
 // The weighted sum of a row's parts 0 .. ns - 1 in their order, FLY of them in flight: part k at src + place(k) * D,
@@ -730,41 +768,55 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
 // Small tiles where there are at most as many tokens as requests: single tokens, in all likelihood.  A chunk
 // among as many idle requests would be slow there but right; with more tokens than requests a large tile
 // of a few rows still takes no longer than its keys take from memory.  With three tiles and more for every
-// workgroup that runs at once the large tiles are left whole: there is little to even out then.
-AttnPlan attn_plan(int S, int R, int HQ, int HKV, int D) {
+// workgroup that runs at once the large tiles are left whole, and nothing is joined (a prompt of 8192: 520 us,
+// 645 cut; two of 4096: 265 and 360), unless one tile is longer than a CU's share of all (a prompt of 8192 beside a
+// token with 100 thousand keys: 1970 us, 740 cut).  One request cannot be so; nor can many where a table's row holds
+// no more keys than that share is when the S tokens have no keys but their own.  Else the device finds out: both kernels
+// run, and one of them, and the join, has nothing to do.
+AttnPlan attn_plan(int S, int R, int HQ, int HKV, int D, long keys) {
   AttnPlan p;
   p.small = S <= R;
-  const long tiles = (long)S * (HQ / HKV) / kLargeRows;  // at least, were all of the tokens one request's
-  const int slots = p.small ? 2 * kCUs : kCUs;           // workgroups that run at once
-  p.whole = !p.small && tiles * HKV >= 3 * slots;
-  p.target = p.whole ? (int)(tiles + (R < S ? R : S)) : (slots + HKV - 1) / HKV;
-  const long rows = p.whole ? 0 : (long)HKV * p.target * 2 * (p.small ? kSmallRows : kLargeRows);
-  p.ws_bytes = rows * (D + 2) * 4 + (p.whole ? 0 : (long)HKV * p.target * (long)sizeof(int4));
+  const int g = HQ / HKV;
+  const long tiles = (long)S * g / kLargeRows;  // at least, were all of the tokens one request's
+  const int slots = p.small ? 2 * kCUs : kCUs;  // workgroups that run at once
+  const double share = (double)S * S * g / (2.0 * kLargeRows * R) * HKV / kCUs;
+  p.split = p.small || tiles * HKV < 3 * slots ? kCut : R == 1 || (double)keys <= share ? kWhole : kEither;
+  p.grid = p.split == kCut ? 0 : (int)(tiles + (R < S ? R : S));  // whole tiles of a key head, at most
+  p.target = p.split == kWhole ? 0 : (slots + HKV - 1) / HKV;
+  const long rows = (long)HKV * p.target * 2 * (p.small ? kSmallRows : kLargeRows);
+  p.ws_bytes = rows * (D + 2) * 4 + (long)HKV * p.target * (long)sizeof(int4);
   return p;
+}
+
+// At most S HQ / 256 + R HKV < 2^20 + 2^22 workgroups of 512 threads: under a launch's 2^32.
+template <int D, bool WHOLE, bool IF>
+static hipError_t launch_large(const AttnArgs& a, int grid, hipStream_t st) {
+  constexpr int bytes = kRing * 64 * D * 4;
+  const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k_attn_large<D, WHOLE, IF>),
+                                           hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((k_attn_large<D, WHOLE, IF>), dim3((unsigned)grid * (unsigned)a.HKV), dim3(512), bytes, st, a);
+  return hipGetLastError();
 }
 
 template <int D>
 static hipError_t launch_d(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
-  const long blocks = (long)p.target * a.HKV;
-  if (blocks > 0x7FFFFFFFL) return hipErrorInvalidValue;
-  const unsigned grid = (unsigned)blocks;
+  const unsigned joins = (unsigned)(p.target * a.HKV);
   const long rows = (long)a.S * a.g;  // of a tile at most, too
   if (p.small) {
-    hipLaunchKernelGGL(k_attn_small<D>, dim3(grid), dim3(256), 0, st, a);
+    hipLaunchKernelGGL(k_attn_small<D>, dim3(joins), dim3(256), 0, st, a);
     const unsigned jy = (unsigned)(((rows < kSmallRows ? rows : kSmallRows) + 3) / 4);
-    hipLaunchKernelGGL((k_attn_join<D, kSmallRows>), dim3(grid, jy), dim3(256), 0, st, a);
+    hipLaunchKernelGGL((k_attn_join<D, kSmallRows>), dim3(joins, jy), dim3(256), 0, st, a);
     return hipGetLastError();
   }
-  constexpr int bytes = kRing * 64 * D * 4;
-  auto kern = p.whole ? k_attn_large<D, true> : k_attn_large<D, false>;
-  const hipError_t e =
-      hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(kern, dim3(grid), dim3(512), bytes, st, a);
-  if (!p.whole) {
-    const unsigned jy = (unsigned)(((rows < kLargeRows ? rows : kLargeRows) + 3) / 4);
-    hipLaunchKernelGGL((k_attn_join<D, kLargeRows>), dim3(grid, jy), dim3(256), 0, st, a);
+  if (p.split != kCut) {
+    const hipError_t e = p.split == kWhole ? launch_large<D, true, false>(a, p.grid, st) : launch_large<D, true, true>(a, p.grid, st);
+    if (e != hipSuccess || p.split == kWhole) return e;
   }
+  const hipError_t e = p.split == kCut ? launch_large<D, false, false>(a, p.target, st) : launch_large<D, false, true>(a, p.target, st);
+  if (e != hipSuccess) return e;
+  const unsigned jy = (unsigned)(((rows < kLargeRows ? rows : kLargeRows) + 3) / 4);
+  hipLaunchKernelGGL((k_attn_join<D, kLargeRows>), dim3(joins, jy), dim3(256), 0, st, a);
   return hipGetLastError();
 }
 

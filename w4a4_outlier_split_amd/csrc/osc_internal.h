@@ -128,13 +128,15 @@ struct AppendArgs {
 hipError_t launch_qkv_append(const AppendArgs& a, hipStream_t st);
 
 // Attention over the paged cache (osc_attn_paged).
+enum AttnSplit { kCut, kWhole, kEither };  // tiles cut for even work, left whole, or as the device finds the lengths
 struct AttnPlan {
-  bool small;  // 16-row tiles
-  bool whole;  // no tile is cut
-  int target;  // workgroups for each key head
+  bool small;       // 16-row tiles
+  AttnSplit split;
+  int target;       // workgroups for each key head that cut tiles are dealt to (0: none is cut)
+  int grid;         // workgroups for each key head where tiles are whole
   long ws_bytes;
 };
-AttnPlan attn_plan(int S, int R, int HQ, int HKV, int D);
+AttnPlan attn_plan(int S, int R, int HQ, int HKV, int D, long keys);  // keys: of a table's row
 struct AttnArgs {
   const void *Q, *KC, *VC;
   int S, R, HQ, HKV, g;  // g = HQ / HKV
