@@ -402,7 +402,7 @@ osc_status osc_qkv_append(const void* QKV, int S, int HQ, int HKV, int D, const 
  * Constraints: S >= 0, S < 2^24, 0 <= R <= OSC_MAX_REQUESTS, HQ a multiple of HKV, both in
  * 1..1024, D in {64, 128}, S * HQ * D < 2^34, NP, MB >= 1, NP * page < 2^31, MB * page <=
  * 2^30, scale positive and scale * log2 e finite; too small a workspace is OSC_E_SHAPE.
- * Scores must stay finite in binary32, times scale * log2 e too.
+ * Scores must stay finite in binary32, times scale * log2 e too; values below 2^80 in size.
  */
 osc_status osc_attn_workspace(int S, int R, int HQ, int HKV, int D, int page, int MB, int64_t* bytes);
 osc_status osc_attn_paged(const void* Q, const void* KC, const void* VC, int S, int R, int HQ, int HKV, int D, int page,

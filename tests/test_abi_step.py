@@ -125,8 +125,10 @@ def test_attn_refusals():
 
 def test_attn_workspace():
     assert ws(S=0) == (0, 0) and ws(R=0) == (0, 0)
-    assert ws(S=8192, R=1, HQ=32, HKV=8, page=64, MB=128) == (0, 0)  # tiles enough: none is cut
-    for sizes in (dict(S=1, R=1, HQ=32, HKV=8, page=64, MB=128), dict(S=2048, R=1, HQ=32, HKV=8, page=64, MB=128), dict(S=9, R=3, D=64)):
+    # none is cut: many tiles, a prompt that fills its table, short requests
+    assert ws(S=8192, R=1, HQ=32, HKV=8, page=64, MB=128) == (0, 0) and ws(S=2000, R=1, HQ=32, HKV=8, page=64, MB=32) == (0, 0)
+    assert ws(S=9, R=3, D=64) == (0, 0)
+    for sizes in (dict(S=1, R=1, HQ=32, HKV=8, page=64, MB=128), dict(S=1024, R=1, HQ=32, HKV=8, page=64, MB=640), dict(S=9, R=3, D=64, MB=640)):
         st, need = ws(**sizes)
         assert st == 0 and 0 < need < 1 << 28  # two tiles for each workgroup, whatever the lengths
         assert attn(**sizes, WS=None) == 1 and attn(**sizes, n=need - 1) == 2 and attn(**sizes, n=-1) == 2

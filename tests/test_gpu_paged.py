@@ -278,15 +278,25 @@ def test_attn_decode(HQ, HKV, D, page):
 
 
 @pytest.mark.parametrize("HQ,HKV,D", HEADS)
-@pytest.mark.parametrize("page", [16, 32, 128])
-def test_attn_chunks_of_uneven_lengths(HQ, HKV, D, page):
-    check_attn(build([(40, 40), (300, 7), (65, 64), (1, 1), (200, 0), (0, 0), (333, 129), (64, 3)], HQ, HKV, D, page, HQ * page))
+@pytest.mark.parametrize("page,MB", [(16, None), (32, None), (128, None), (16, 300), (64, 100)])
+def test_attn_chunks_of_uneven_lengths(HQ, HKV, D, page, MB):
+    check_attn(build([(40, 40), (300, 7), (65, 64), (1, 1), (200, 0), (0, 0), (333, 129), (64, 3)], HQ, HKV, D, page, HQ * page, MB=MB))
 
 
 @pytest.mark.parametrize("kv,n", [(1, 1), (2, 2), (17, 9), (63, 63), (64, 64), (129, 33), (700, 1), (700, 32), (1500, 300), (4100, 40)])
 @pytest.mark.parametrize("D,page", [(128, 64), (64, 16)])
-def test_attn_one_request(kv, n, D, page):
-    check_attn(build([(kv, n)], 8, 2, D, page, kv + n))
+@pytest.mark.parametrize("room", [0, 40000])
+def test_attn_one_request(kv, n, D, page, room):
+    check_attn(build([(kv, n)], 8, 2, D, page, kv + n, MB=-(-(kv + room) // page)))
+
+
+@pytest.mark.parametrize("reqs", [[(2000, 2000)], [(6000, 600)], [(2200, 1100)], [(9000, 700), (300, 300)], [(700, 700)] * 3, [(700, 700), (0, 0), (1, 1), (15000, 90)]])
+def test_attn_whole_or_cut_as_the_lengths_are(reqs):
+    """A table with room for 60 thousand keys: only the lengths on the device tell."""
+    p = build(reqs, 8, 2, 128, 64, 25, MB=940)
+    a = attend(p)
+    check_attn(p, a)
+    assert torch.equal(attend(p), a)
 
 
 @pytest.mark.parametrize("reqs", [[(5000, 1)], [(3, 1), (5012, 1), (0, 0)], [(5012, 60), (1, 1)], [(128, 128), (4000, 9)], [(20000, 1)],
@@ -322,7 +332,7 @@ def test_attn_rows_that_see_nothing_are_zero():
 
 @pytest.mark.parametrize("n", [2, 90])
 def test_attn_leaves_out_pages_that_do_not_exist(n):
-    p = build([(300, n), (100, 1)], 4, 1, 128, 16, n)
+    p = build([(300, n), (100, 1)], 4, 1, 128, 16, n, MB=300 if n == 90 else None)
     p["table"][0][2] = -1
     p["table"][0][7] = p["NP"]
     p["KC"][0], p["VC"][0] = float("nan"), float("inf")  # what stands in for them is never used
@@ -379,7 +389,7 @@ def test_attn_chunks_of_the_most_requests():
 def test_attn_large_scores_and_growing_maximum():
     """Scores whose maximum grows from tile to tile, by little and by much, and scores far below."""
     for step in (0.002, 0.05, 1.0):
-        p = build([(600, 70), (333, 1)], 4, 1, 128, 64, 3, spread=1.0)
+        p = build([(600, 70), (333, 1)], 4, 1, 128, 64, 3, spread=1.0, MB=64)
         for r in range(2):
             for i in range(p["kv"][r]):
                 id, off = p["table"][r][i // 64], i % 64
@@ -388,6 +398,18 @@ def test_attn_large_scores_and_growing_maximum():
         ref, tol = attn_reference(p)
         O = attend(p)
         assert bool(((O.double() - ref).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("n", [1, 40])
+def test_attn_large_values_under_a_growing_maximum(n):
+    """Values close to 2^80, and scores that grow by less than what the running maximum may lag behind."""
+    p = build([(600, n), (601, 1)], 4, 1, 64, 64, 24, spread=0.0)
+    p["Q"][..., 0] = 4.0
+    for r in range(2):
+        for i in range(p["kv"][r]):
+            p["KC"][p["table"][r][i // 64], :, i % 64, 0] = i * 0.04  # scores up to 12, 17 in the exponent of 2
+    p["VC"] *= 2.0 ** 76
+    check_attn(p)
 
 
 def test_attn_infinite_and_nan_inputs_stay_in_their_rows():

@@ -6,8 +6,9 @@
 // one pass over the keys: with m the running maximum of a row's scores and l the running sum of
 // exp(s - m), a tile of keys adds P = exp(S - m) to l and P V to the unnormalised output, and where
 // m grows both are scaled by exp(m_old - m_new).  Scores, m, l and the output are binary32; P is
-// rounded to bf16 for the matrix instruction (each weight off by at most 2^-9 of itself, as V's own
-// rounding is), l sums the unrounded P.
+// rounded to bf16 for the matrix instruction, which takes no wider operand beside bf16 values (each weight off
+// by at most 2^-8 of itself, in either direction).  l sums P as it is in the small kernel, and as rounded
+// in the large one, where two weights a dot product halve the additions.
 //
 // The HQ / HKV query heads that read one key head are rows of one tile, token by token, so a tile's
 // keys serve all of them.  Both products run transposed, S^T = K Q^T and O^T = V^T P^T: a lane then
@@ -17,16 +18,23 @@
 // cache's V layout [page][head][D][slot].
 //
 // Two kernels, by the call's tokens and requests:
-//   small (single tokens): tiles of 16 rows, the cache read from memory straight into registers; the
-//     four wavefronts take 32 keys each in turn and are merged at the end.  HBM-bound.
+//   small (single tokens): tiles of 16 rows, the cache read from memory straight into registers, every byte once;
+//     the four wavefronts take 32 keys each in turn and are merged at the end.  HBM-bound: 64 decodes over 136
+//     thousand keys (1.07 GB of cache) take 189 us, 5.7 TB/s.  A single decode over 4000 keys takes 9 us and 4 for the
+//     join, bound by the chain of page table, keys, scores and two launches (its 16 MB are worth 3.5 us).
 //   large: tiles of 256 rows, eight wavefronts of 32 rows each, one workgroup a CU; 64 keys of K and V^T at a
-//     time in a ring in LDS, loaded by LDS-DMA three tiles ahead.  Bound by what the matrix unit and the rest
-//     draw together: the card lowers its clock under this load, so what counts is work per product.
+//     time in a ring in LDS, loaded by LDS-DMA three tiles ahead, so that a key is fetched once for 256 rows.  Bound
+//     by what the matrix unit and the rest draw together: the card lowers its clock under this load, so
+//     what counts is work per product.  A prompt of 8192 (32 query and 8 key heads of 128): 495 to 535 us with the
+//     clock of the card, 1.03 to 1.11 PFLOP/s of the 1.35 to 1.55 that large matrix products reach; without loads,
+//     barriers and exponentials it would be 458 us.  33 tokens over 32700 keys take 43 us and 9 for the join: a
+//     tile of 132 rows on eight wavefronts, whose rate the chain through a step's two products sets.
 // The work is cut evenly, whatever the lengths: all tiles of a key head stand in a row, each as long as the keys
 // that it sees, and the row is cut into as many equal parts as workgroups run at once.  A workgroup takes
 // its part, tile by tile.  A tile that a cut goes through has its unnormalised outputs left in the workspace, at
 // most two tiles for a workgroup, and a second launch joins them in a fixed order.  The lengths are on the
-// device, so each wavefront works the cuts out for itself.
+// device, so each wavefront works the cuts out for itself.  (Four chunks of up to 1024 tokens behind up to 8192, 135 GFLOP:
+// 154 us and 20 for the join of 67 MB.)  Where there are many tiles they are left whole instead, see attn_plan.
 #include "osc_device.h"
 #include "osc_internal.h"
 
@@ -41,11 +49,13 @@ constexpr int kLargeRows = 256;
 constexpr int kRing = 4;        // tiles of 64 keys in LDS
 constexpr int kCUs = 256;
 constexpr int kMaxCuts = 61;    // of one tile: its parts, two more at most, are the lanes of the join
-constexpr int kMinKeysSmall = 128, kMinKeysLarge = 256;  // that a workgroup's part has at least
+// Keys that a workgroup's part has at least.  (A prompt of 300 cut at 64, 128, 256: 24, 30, 38 us; 200 tokens on one key
+// head behind 800: 35, 31, 34.)
+constexpr int kMinKeys = 128;
 // The running maximum is left as it is while no score exceeds it by more than kSlack (in the exponent
-// of 2): P is then at most 2^kSlack, and binary32 holds sums of 2^31 of them times a bf16 value of up to
-// 2^50; neither format loses precision by the factor.
-constexpr float kSlack = 40.0f;
+// of 2): P is then at most 2^kSlack, and binary32 holds sums over 2^30 keys of them times values below 2^80;
+// neither format loses precision by the factor.
+constexpr float kSlack = 16.0f;
 
 // branches that the loops seldom take: the registers are laid out for the other side
 __device__ __forceinline__ bool rare(bool c) { return __builtin_expect(c, 0); }
@@ -266,7 +276,7 @@ __device__ __forceinline__ void small_tile(const AttnArgs& a, const Tile& t, int
 }
 
 // ------------------------------------------------------------------ large tiles
-// LDS: two buffers of K [64 keys][D] and two of V^T [4 runs of 16 keys][D][16].  K rows hold their
+// LDS: a ring of tiles of K [64 keys][D] and V^T [4 runs of 16 keys][D][16].  K rows hold their
 // 16-byte pieces at position piece ^ (row & (D/8 - 1)), V^T rows their two halves at half ^ (d >> 3 & 1):
 // the 16 lanes that LDS serves together then read 16 different 16-byte columns of its 256.
 // LDS-DMA of half of one run of 16 keys, which lie in one page (block: its byte offset for the key head, K's and
@@ -544,9 +554,25 @@ __device__ __forceinline__ long divide(long a, long b) {
   return q;
 }
 
+// Whole tiles or cut ones?  A key head has s CUs to itself.  Whole, its tiles take as long as the CU that has most of
+// them; cut, a CU's even share, a quarter more for partial outputs and keys that are no longer read in step,
+// and what 1500 keys take for the second launch.  With three tiles a CU and more, the share is what counts as long as
+// no tile is longer; with fewer, a CU has the longest tile beside its share at worst.
+__host__ __device__ inline long slots_of(int HKV) { return HKV < kCUs ? kCUs / HKV : 1; }
+__host__ __device__ inline bool whole_pays(long s, long tiles, long most, long all) {
+  return 4 * most * s <= all + 6000 * s || (tiles >= 3 * s && most * s <= all);
+}
+// One request with tiles of base + tau, base + 2 tau, ... keys, the longest first: a CU has one, or two of which the
+// longest pair is the s-th and the next.
+__host__ __device__ inline bool whole_pays_alone(long s, long tiles, long base, long tau) {
+  if (tiles > 2 * s) return true;
+  const long one = base + tau * tiles, two = tiles > s ? 2 * base + tau * (2 * tiles + 1 - 2 * s) : 0;
+  const long all = tiles * base + tau * (tiles * (tiles + 1) / 2);
+  return 4 * (one > two ? one : two) * s <= 5 * all + 6000 * s;
+}
+
 // All tiles of a key head in a row, cut into `parts` equal parts (WHOLE: a tile each).  A wavefront's lanes hold
-// a share of the requests each.  IF: no parts unless the lengths call for this way of the two: tiles are left whole
-// where none is longer than a CU's share of all.
+// a share of the requests each.  IF: no parts unless the lengths call for this way of the two.
 template <int ROWS, bool WHOLE, bool IF>
 struct Cuts {
   typedef Request<ROWS> Req;
@@ -576,7 +602,7 @@ struct Cuts {
     const int lanes = (a.R + per - 1) / per;
     for (int d = 1; d < lanes; d <<= 1) {  // up to each lane
       const long up = __shfl_up(upto, d), other = __shfl_up(most, d);
-      const long tiles = IF && WHOLE ? __shfl_up(counted, d) : 0;
+      const long tiles = IF ? __shfl_up(counted, d) : 0;
       if (lane >= d) {
         upto += up, counted += tiles;
         most = other > most ? other : most;
@@ -584,7 +610,15 @@ struct Cuts {
     }
     all = lane_of(upto, lanes - 1);
     most = lane_of(most, lanes - 1);
-    const bool even = most * kCUs <= all * a.HKV;
+    bool even = false;
+    if (IF) {
+      const long s = slots_of(a.HKV);
+      even = whole_pays(s, lane_of(counted, lanes - 1), most, all);
+      if (a.R == 1) {
+        const Req q(a, 0, false);
+        even = even || whole_pays_alone(s, q.tiles, q.base, q.tau);
+      }
+    }
     if (IF && WHOLE) {
       mine = count, upto = counted;
       all = lane_of(upto, lanes - 1);
@@ -594,8 +628,7 @@ struct Cuts {
       each = 1, over = 0;
     } else {
       long p = a.target;
-      constexpr int least = ROWS == kSmallRows ? kMinKeysSmall : kMinKeysLarge;
-      if (p > all / least) p = all / least;
+      if (p > all / kMinKeys) p = all / kMinKeys;
       if (most > 0 && p > kMaxCuts && p > kMaxCuts * divide(all, most)) p = kMaxCuts * divide(all, most);
       parts = p < 1 ? 1 : (int)p;
       each = divide(all, parts);
@@ -734,8 +767,11 @@ __device__ __forceinline__ vE weigh(const float* src, Place place, int ns, float
   return acc;
 }
 
-// Joins the parts of the tile that part w noted, a row a wavefront: lane k holds the maximum and sum of part w + k,
-// and the lanes D / 64 values of the row each.
+// Joins the parts of the tile that part w noted: o = sum_k 2^(m_k - m) o_k / sum_k 2^(m_k - m) l_k with m the largest
+// m_k, in the order of the parts.  A row a wavefront: lane k holds the maximum and sum of part w + k, and the lanes
+// D / 64 values of the row each.  HBM-bound where the parts are many (67 MB in 20 us, launch and all); a few rows
+// (4 us) are bound by the launch and two loads one after the other, so the values' loads all start at once.
+// (A workgroup a tile took 9 us for one decode and 24 for 33 tokens over 32700 keys, whose 132 rows have 31 parts each: 9 now.)
 template <int D, int ROWS>
 __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
   constexpr int E = D / 64;
@@ -767,24 +803,29 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
 
 // Small tiles where there are at most as many tokens as requests: single tokens, in all likelihood.  A chunk
 // among as many idle requests would be slow there but right; with more tokens than requests a large tile
-// of a few rows still takes no longer than its keys take from memory.  With three tiles and more for every
-// workgroup that runs at once the large tiles are left whole, and nothing is joined (a prompt of 8192: 520 us,
-// 645 cut; two of 4096: 265 and 360), unless one tile is longer than a CU's share of all (a prompt of 8192 beside a
-// token with 100 thousand keys: 1970 us, 740 cut).  One request cannot be so; nor can many where a table's row holds
-// no more keys than that share is when the S tokens have no keys but their own.  Else the device finds out: both kernels
-// run, and one of them, and the join, has nothing to do.
+// of a few rows still takes no longer than its keys take from memory.
+// Large tiles are left whole where that is quicker whatever the lengths are, as far as the table's pages say: one
+// request whose tiles pair up over the CUs with the longest and with no context (prompts of 1000, 2000, 4000, 8192: 33, 59,
+// 133, 520 us whole, 54, 95, 207, 645 cut), requests too short to be worth cutting, and many tiles none of which
+// can be longer than a CU's share.  They are cut where there are few rows (33 tokens over 32700 keys).  Else the
+// device finds out: both kernels run, and one of them, and perhaps the join, has nothing to do, which costs 9 us where
+// tiles stay whole and 3 where not (a prompt of 8192 beside a token with 100 thousand keys: 1970 us whole, 745 so).
 AttnPlan attn_plan(int S, int R, int HQ, int HKV, int D, long keys) {
   AttnPlan p;
   p.small = S <= R;
   const int g = HQ / HKV;
-  const long tiles = (long)S * g / kLargeRows;  // at least, were all of the tokens one request's
-  const int slots = p.small ? 2 * kCUs : kCUs;  // workgroups that run at once
-  const double share = (double)S * S * g / (2.0 * kLargeRows * R) * HKV / kCUs;
-  p.split = p.small || tiles * HKV < 3 * slots ? kCut : R == 1 || (double)keys <= share ? kWhole : kEither;
-  p.grid = p.split == kCut ? 0 : (int)(tiles + (R < S ? R : S));  // whole tiles of a key head, at most
-  p.target = p.split == kWhole ? 0 : (slots + HKV - 1) / HKV;
-  const long rows = (long)HKV * p.target * 2 * (p.small ? kSmallRows : kLargeRows);
-  p.ws_bytes = rows * (D + 2) * 4 + (long)HKV * p.target * (long)sizeof(int4);
+  const long rows = (long)S * g, tiles = (rows + kLargeRows - 1) / kLargeRows;  // were all of the tokens one request's
+  const long s = slots_of(HKV), tau = (kLargeRows + g - 1) / g;
+  bool whole;
+  if (R == 1)  // both conditions are linear in the context or the larger of two such: the ends say it all
+    whole = whole_pays_alone(s, tiles, 0, tau) && whole_pays_alone(s, tiles, keys > S ? keys - S : 0, tau);
+  else  // S tokens have S^2 / 2R keys at least, with no context and the same length each
+    whole = whole_pays(s, rows / kLargeRows, keys, (long)((double)S * rows / (2.0 * kLargeRows * R)));
+  p.split = p.small ? kCut : whole ? kWhole : tiles < 8 ? kCut : kEither;
+  p.grid = p.split == kCut ? 0 : (int)(rows / kLargeRows + (R < S ? R : S));  // whole tiles of a key head, at most
+  p.target = p.split == kWhole ? 0 : ((p.small ? 2 : 1) * kCUs + HKV - 1) / HKV;  // workgroups that run at once
+  const long kept = (long)HKV * p.target * 2 * (p.small ? kSmallRows : kLargeRows);
+  p.ws_bytes = kept * (D + 2) * 4 + (long)HKV * p.target * (long)sizeof(int4);
   return p;
 }
 
