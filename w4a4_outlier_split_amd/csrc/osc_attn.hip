@@ -34,7 +34,7 @@
 // its part, tile by tile.  A tile that a cut goes through has its unnormalised outputs left in the workspace, at
 // most two tiles for a workgroup, and a second launch joins them in a fixed order.  The lengths are on the
 // device, so each wavefront works the cuts out for itself.  (Four chunks of up to 1024 tokens behind up to 8192, 135 GFLOP:
-// 154 us and 20 for the join of 67 MB.)  Where there are many tiles they are left whole instead, see attn_plan.
+// 154 us and 20 for the join of 58 MB.)  Where there are many tiles they are left whole instead, see attn_plan.
 #include "osc_device.h"
 #include "osc_internal.h"
 
@@ -130,6 +130,10 @@ __device__ __forceinline__ float sum_wave(float v) {
 }
 
 // ------------------------------------------------------------------ small tiles
+// Rows are the query heads of a token (and the next tokens'), so a decode with 4 heads to a key head uses 4 of 16:
+// the products are idle anyway where every key is read once.  No LDS on the way: a key's row and a channel's run of
+// keys are 16-byte pieces in the very lanes that the products want, and four wavefronts with a step each in flight
+// and 512 workgroups cover the latency.  (64 decodes: 284 us with pages looked up in the step, 189 so, 5.7 TB/s.)
 template <int D>
 __device__ __forceinline__ void small_tile(const AttnArgs& a, const Tile& t, int h, float* lds) {
   constexpr int DK = D / 32, DB = D / 16;
@@ -309,7 +313,11 @@ __device__ __forceinline__ void load_v(const AttnArgs& a, long block, int at, in
 }
 
 // Eight wavefronts, a ring of kRing tiles of 64 keys in LDS filled three tiles ahead; one barrier a tile, behind
-// which the tile before is free.
+// which the tile before is free.  A wavefront holds 32 rows' queries (64 registers' worth with a tile's keys in
+// flight) and output (64): 64 rows would halve the LDS reads a product but need the accumulation registers, whose copies
+// cost more; four wavefronts, two workgroups a CU, read each key twice from LDS (587 us for the prompt of 8192, 495 to 535
+// so).  A step has 32 products of 32 cycles for each wavefront, 2048 cycles a SIMD, and takes about 3500: one wavefront's
+// exponentials run beside the other's products, the rest is LDS and the barrier.
 template <int D>
 __device__ __forceinline__ void large_tile(const AttnArgs& a, const Tile& t, int h, uint8_t* lds) {
   constexpr int DK = D / 16, DB = D / 32, CH = D / 8, HALF = 64 * D * 2, TILE = 2 * HALF;
@@ -769,7 +777,7 @@ __device__ __forceinline__ vE weigh(const float* src, Place place, int ns, float
 
 // Joins the parts of the tile that part w noted: o = sum_k 2^(m_k - m) o_k / sum_k 2^(m_k - m) l_k with m the largest
 // m_k, in the order of the parts.  A row a wavefront: lane k holds the maximum and sum of part w + k, and the lanes
-// D / 64 values of the row each.  HBM-bound where the parts are many (67 MB in 20 us, launch and all); a few rows
+// D / 64 values of the row each.  HBM-bound where the parts are many (58 MB in 20 us, launch and all); a few rows
 // (4 us) are bound by the launch and two loads one after the other, so the values' loads all start at once.
 // (A workgroup a tile took 9 us for one decode and 24 for 33 tokens over 32700 keys, whose 132 rows have 31 parts each: 9 now.)
 template <int D, int ROWS>

@@ -12,8 +12,8 @@
 // time, neighbours side by side, so that every load and store instruction covers whole contiguous lines.
 // A row takes the four wavefronts of a workgroup, which meet in LDS once for its sum.  (A row a wavefront,
 // without the barrier, leaves a lane eight times the arithmetic of a 4096-wide row one after the other and
-// fewer wavefronts to overlap it: 4096 rows of 4096 into E4M3 take 33.3 us that way, 25.2 this way at 4.7
-// TB/s, 16 rows 8.6 and 3.5.)  All streams are read or written once and go past the caches' residents.
+// fewer wavefronts to overlap it: 4096 rows of 4096 into E4M3 take 33.3 us that way, 23.2 to 25.3 this way at 4.7
+// to 5.1 TB/s, 16 rows into E2M1 8.6 and 3.7; 1537 rows of 8192 take 17.1 to 18.)  All streams are read or written once and go past the caches' residents.
 #include "osc_quant_blk.h"
 
 namespace osc {
