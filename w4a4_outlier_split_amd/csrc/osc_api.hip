@@ -297,6 +297,7 @@ osc_status osc_rmsnorm_quant(const void* X, const void* RES, const void* W, int 
     st = pack_table(L, H / G, m, G, &tab);
     if (st != OSC_OK) return st;
   }
+  if (!osc::launch_rmsnorm) return OSC_E_DEVICE;
   osc::NormArgs a{X, RES, W, S, H, eps, G, m, L ? &tab : nullptr, afmt, RES_OUT, QX, SX, B};
   return from_hip(osc::launch_rmsnorm(a, static_cast<hipStream_t>(stream)));
 }
@@ -309,6 +310,7 @@ osc_status osc_rmsnorm(const void* X, const void* RES, const void* W, int S, int
   if (S == 0) return OSC_OK;
   if (!X || !W || !Y || (RES == nullptr) != (RES_OUT == nullptr)) return OSC_E_NULL;
   if (!aligned16(X) || !aligned16(RES) || !aligned16(W) || !aligned16(RES_OUT) || !aligned16(Y)) return OSC_E_ALIGN;
+  if (!osc::launch_rmsnorm) return OSC_E_DEVICE;
   osc::NormArgs a{X, RES, W, S, H, eps, 64, 1, nullptr, OSC_MXFP4, RES_OUT, Y, nullptr, nullptr};
   return from_hip(osc::launch_rmsnorm(a, static_cast<hipStream_t>(stream)));
 }
@@ -328,6 +330,7 @@ osc_status osc_page_plan(const int32_t* CTX, const int32_t* NEW, int R, int page
     return OSC_E_ALIGN;
   // every workgroup reads the inputs, one of them writes these outputs
   if ((R > 0 && (KV == CTX || KV == NEW)) || USED == HEAD) return OSC_E_SHAPE;
+  if (!osc::launch_page_plan) return OSC_E_DEVICE;
   osc::PlanArgs a{CTX, NEW, R, sh, NP, FREE, F, HEAD, T, TABLE, MB, CU, KV, SLOT, POS, USED};
   return from_hip(osc::launch_page_plan(a, static_cast<hipStream_t>(stream)));
 }
@@ -345,6 +348,7 @@ osc_status osc_qkv_append(const void* QKV, int S, int HQ, int HKV, int D, const 
   if (!aligned16(QKV) || !aligned16(WQ) || !aligned16(WK) || !aligned16(CS) || !aligned16(Q) || !aligned16(KC) ||
       !aligned16(VC) || !aligned4(POS) || !aligned4(SLOT))
     return OSC_E_ALIGN;
+  if (!osc::launch_qkv_append) return OSC_E_DEVICE;
   osc::AppendArgs a{QKV, S, HQ, HKV, D, WQ, WK, eps, CS, P, POS, SLOT, Q, KC, VC, NP, sh};
   return from_hip(osc::launch_qkv_append(a, static_cast<hipStream_t>(stream)));
 }
@@ -361,6 +365,7 @@ osc_status osc_attn_workspace(int S, int R, int HQ, int HKV, int D, int page, in
   const osc_status st = check_attn(S, R, HQ, HKV, D, page, MB);
   if (st != OSC_OK) return st;
   if (!bytes) return OSC_E_NULL;
+  if (!osc::attn_plan) return OSC_E_DEVICE;
   *bytes = S == 0 || R == 0 ? 0 : osc::attn_plan(S, R, HQ, HKV, D, (long)MB * page).ws_bytes;
   return OSC_OK;
 }
@@ -376,6 +381,7 @@ osc_status osc_attn_paged(const void* Q, const void* KC, const void* VC, int S, 
   if (!isfinite(scale_log2)) return OSC_E_SHAPE;
   if (S == 0 || R == 0) return OSC_OK;
   if (!Q || !KC || !VC || !TABLE || !CU || !KV || !O) return OSC_E_NULL;
+  if (!osc::attn_plan || !osc::launch_attn) return OSC_E_DEVICE;
   const osc::AttnPlan p = osc::attn_plan(S, R, HQ, HKV, D, (long)MB * page);
   if (p.ws_bytes > 0 && !WS) return OSC_E_NULL;
   if (ws_bytes < p.ws_bytes) return OSC_E_SHAPE;

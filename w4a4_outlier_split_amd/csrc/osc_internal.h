@@ -83,6 +83,11 @@ struct FusedArgs {
 long fused_lds_bytes(int H, int G, int kc);
 hipError_t launch_linear_dec(const FusedArgs& a, hipStream_t st);
 
+// What lies between the projections.  The functions are weak references: a library linked from the linear layers'
+// objects alone (the sanitizer build of the validation) loads and checks every argument, and answers OSC_E_DEVICE
+// where it would launch.
+#define OSC_STEP __attribute__((weak))
+
 // Residual add + RMS norm of S rows of H bf16; SX == nullptr: y itself to QX (row-major bf16), else its
 // quantization, tab == nullptr without extraction.
 struct NormArgs {
@@ -97,7 +102,7 @@ struct NormArgs {
   uint8_t* SX;
   void* B;
 };
-hipError_t launch_rmsnorm(const NormArgs& a, hipStream_t st);
+OSC_STEP hipError_t launch_rmsnorm(const NormArgs& a, hipStream_t st);
 
 // Page tables and slot maps of one step (osc_page_plan); sh = log2(page).
 struct PlanArgs {
@@ -111,7 +116,7 @@ struct PlanArgs {
   int MB;
   int32_t *CU, *KV, *SLOT, *POS, *USED;
 };
-hipError_t launch_page_plan(const PlanArgs& a, hipStream_t st);
+OSC_STEP hipError_t launch_page_plan(const PlanArgs& a, hipStream_t st);
 
 // Head norm, rotary embedding and cache write (osc_qkv_append); sh = log2(page).
 struct AppendArgs {
@@ -125,7 +130,7 @@ struct AppendArgs {
   void *Q, *KC, *VC;
   int NP, sh;
 };
-hipError_t launch_qkv_append(const AppendArgs& a, hipStream_t st);
+OSC_STEP hipError_t launch_qkv_append(const AppendArgs& a, hipStream_t st);
 
 // Attention over the paged cache (osc_attn_paged).
 enum AttnSplit { kCut, kWhole, kEither };  // tiles cut for even work, left whole, or as the device finds the lengths
@@ -136,7 +141,7 @@ struct AttnPlan {
   int grid;         // workgroups for each key head where tiles are whole
   long ws_bytes;
 };
-AttnPlan attn_plan(int S, int R, int HQ, int HKV, int D, long keys);  // keys: of a table's row
+OSC_STEP AttnPlan attn_plan(int S, int R, int HQ, int HKV, int D, long keys);  // keys: of a table's row
 struct AttnArgs {
   const void *Q, *KC, *VC;
   int S, R, HQ, HKV, g;  // g = HQ / HKV
@@ -151,6 +156,6 @@ struct AttnArgs {
   int4* NOTE;
   int target;
 };
-hipError_t launch_attn(const AttnArgs& a, int D, const AttnPlan& p, hipStream_t st);
+OSC_STEP hipError_t launch_attn(const AttnArgs& a, int D, const AttnPlan& p, hipStream_t st);
 
 }  // namespace osc
