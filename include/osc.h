@@ -396,7 +396,7 @@ osc_status osc_qkv_append(const void* QKV, int S, int HQ, int HKV, int D, const 
  * What the cache holds behind a request's KV keys is never used, whatever it is; NaN in a
  * key reaches the rows that see it, NaN in a value may reach every row of its request.
  *   WS, ws_bytes: device workspace of at least osc_attn_workspace's bytes for the same
- *   sizes (WS may be NULL when that is 0), free again when the call's work is done: calls
+ *   sizes (WS may be NULL when that is 0; fewer tokens may need more), free again when the call's work is done: calls
  *   that can overlap, two graphs replayed on two streams included, need one each.
  * The result does not depend on what else runs (sums are joined in a fixed order).
  * Constraints: S >= 0, S < 2^24, 0 <= R <= OSC_MAX_REQUESTS, HQ a multiple of HKV, both in

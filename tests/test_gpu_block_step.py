@@ -162,6 +162,27 @@ def test_two_blocks_captured():
         assert torch.equal(a, b), i
 
 
+def test_buffers_hold_for_steps_of_fewer_rows():
+    """One set of buffers, steps of every kernel: a prompt, a chunk, single tokens, a padded chunk."""
+    t, mb = 2400, 2048
+    b = make_block(12, "osc")
+    pages = blk.Pages(torch, R, 400, PAGE, mb, t, DEV)
+    cache, bufs = blk.LayerCache(torch, pages, HKV, D, DEV), b.buffers(t, pages, DEV)
+    assert all(osc.osc_attn_workspace(s, R, HQ, HKV, D, PAGE, mb) <= bufs["attn"]["ws"].numel() for s in range(t + 1))
+    g = torch.Generator(device=DEV).manual_seed(6)
+    for S, counts in ((2400, (2300, 0, 90)), (65, (0, 64, 1)), (3, (1, 1, 1)), (2, (1, 0, 1)), (48, (1, 0, 30)), (4, (2, 1, 1))):
+        pages.new.copy_(torch.tensor(counts, dtype=torch.int32))
+        x, Y = torch.randn((S, H), generator=g, device=DEV).bfloat16(), torch.empty((S, H), dtype=torch.bfloat16, device=DEV)
+        other = {**bufs["attn"], "ws": torch.empty((osc.osc_attn_workspace(S, R, HQ, HKV, D, PAGE, mb),), dtype=torch.uint8, device=DEV)}
+        pages.plan()
+        b.forward(x.clone(), None, S, pages, cache, bufs, Y)
+        again = torch.empty_like(Y)
+        b.forward(x.clone(), None, S, pages, cache, {**bufs, "attn": other}, again)
+        pages.advance()
+        n = sum(counts)
+        assert torch.equal(Y[:n], again[:n]) and bool(torch.isfinite(Y[:n].float()).all())
+
+
 def test_refusals():
     b, pages = make_block(11, "osc"), make_pages()
     with pytest.raises(ValueError):

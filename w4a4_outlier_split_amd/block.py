@@ -279,9 +279,11 @@ class Attention:
         self.scale = D ** -0.5
 
     def buffers(self, S: int, pages: Pages, device):
+        """Buffers for steps of up to S rows."""
         t = self.qkv.torch
         bf = lambda *n: t.zeros(n, dtype=t.bfloat16, device=device)  # padding rows stay finite through the output projection
-        ws = osc_attn_workspace(S, pages.R, self.HQ, self.HKV, self.D, pages.page, pages.MB)
+        # steps of fewer rows may need more of a workspace than those of many: single tokens, and the fewest rows of the other kernel
+        ws = max(osc_attn_workspace(s, pages.R, self.HQ, self.HKV, self.D, pages.page, pages.MB) for s in {S, min(S, pages.R), min(S, pages.R + 1)})
         return {"x": self.qkv.act_buffers(S, device), "qkv": bf(S, self.qkv.N), "q": bf(S, self.HQ, self.D), "o": bf(S, self.HQ, self.D),
                 "ws": t.empty((ws,), dtype=t.uint8, device=device), "ox": self.out.act_buffers(S, device)}
 

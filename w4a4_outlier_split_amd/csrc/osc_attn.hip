@@ -824,9 +824,9 @@ AttnPlan attn_plan(int S, int R, int HQ, int HKV, int D, long keys) {
   const int g = HQ / HKV;
   const long rows = (long)S * g, tiles = (rows + kLargeRows - 1) / kLargeRows;  // were all of the tokens one request's
   const long s = slots_of(HKV), tau = (kLargeRows + g - 1) / g;
-  bool whole;
+  bool whole = whole_pays(s, 0, keys, 0);  // too short to be worth cutting
   if (R == 1)  // both conditions are linear in the context or the larger of two such: the ends say it all
-    whole = whole_pays_alone(s, tiles, 0, tau) && whole_pays_alone(s, tiles, keys > S ? keys - S : 0, tau);
+    whole = whole || (whole_pays_alone(s, tiles, 0, tau) && whole_pays_alone(s, tiles, keys > S ? keys - S : 0, tau));
   else  // S tokens have S^2 / 2R keys at least, with no context and the same length each
     whole = whole_pays(s, rows / kLargeRows, keys, (long)((double)S * rows / (2.0 * kLargeRows * R)));
   p.split = p.small ? kCut : whole ? kWhole : tiles < 8 ? kCut : kEither;
