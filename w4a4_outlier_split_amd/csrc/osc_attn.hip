@@ -809,9 +809,9 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
 
 }  // namespace
 
-// Small tiles where there are at most as many tokens as requests: single tokens, in all likelihood.  A chunk
-// among as many idle requests would be slow there but right; with more tokens than requests a large tile
-// of a few rows still takes no longer than its keys take from memory.
+// Small tiles where there are at most as many tokens as requests: single tokens, in all likelihood.  (Of 2125 keys, 64
+// of them: 105 us, 122 in large tiles; 256 of 500: 104 and 138; 16 of 8000: 100 either way.)  A chunk among as many idle
+// requests is right there but slow (512 tokens behind 8000 among 511 idle ones: 477 us, 200 in large tiles).
 // Large tiles are left whole where that is quicker whatever the lengths are, as far as the table's pages say: one
 // request whose tiles pair up over the CUs with the longest and with no context (prompts of 1000, 2000, 4000, 8192: 33, 59,
 // 133, 520 us whole, 54, 95, 207, 645 cut), requests too short to be worth cutting, and many tiles none of which
