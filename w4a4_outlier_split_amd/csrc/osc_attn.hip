@@ -815,7 +815,8 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
 // Large tiles are left whole where that is quicker whatever the lengths are, as far as the table's pages say: one
 // request whose tiles pair up over the CUs with the longest and with no context (prompts of 1000, 2000, 4000, 8192: 33, 59,
 // 133, 520 us whole, 54, 95, 207, 645 cut), requests too short to be worth cutting, and many tiles none of which
-// can be longer than a CU's share.  They are cut where there are few rows (33 tokens over 32700 keys).  Else the
+// can be longer than a CU's share.  They are cut where there are few rows (33 tokens over 32700 keys) or, of
+// several requests, less than a tile a CU (300 tokens of three in a long table: 31 us cut, 19 and 9 whole).  Else the
 // device finds out: both kernels run, and one of them, and perhaps the join, has nothing to do, which costs 9 us where
 // tiles stay whole and 3 where not (a prompt of 8192 beside a token with 100 thousand keys: 1970 us whole, 745 so).
 AttnPlan attn_plan(int S, int R, int HQ, int HKV, int D, long keys) {
@@ -829,7 +830,7 @@ AttnPlan attn_plan(int S, int R, int HQ, int HKV, int D, long keys) {
     whole = whole || (whole_pays_alone(s, tiles, 0, tau) && whole_pays_alone(s, tiles, keys > S ? keys - S : 0, tau));
   else  // S tokens have S^2 / 2R keys at least, with no context and the same length each
     whole = whole_pays(s, rows / kLargeRows, keys, (long)((double)S * rows / (2.0 * kLargeRows * R)));
-  p.split = p.small ? kCut : whole ? kWhole : tiles < 8 ? kCut : kEither;
+  p.split = p.small ? kCut : whole ? kWhole : tiles < (R == 1 ? 8 : s) ? kCut : kEither;
   p.grid = p.split == kCut ? 0 : (int)(rows / kLargeRows + (R < S ? R : S));  // whole tiles of a key head, at most
   p.target = p.split == kWhole ? 0 : ((p.small ? 2 : 1) * kCUs + HKV - 1) / HKV;  // workgroups that run at once
   const long kept = (long)HKV * p.target * 2 * (p.small ? kSmallRows : kLargeRows);
