@@ -1,0 +1,65 @@
+"""Steps of which some tokens find no row, page or room in their table row: the requests go on without them, over what
+was written and nothing else.  Checked against 64 bits over the tokens that the lengths say are there."""
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():
+    pytest.skip("no GPU", allow_module_level=True)
+
+from w4a4_outlier_split_amd import block as blk  # noqa: E402
+from gpu_util import DEV  # noqa: E402
+from test_gpu_block_step import D, H, HKV, MB, PAGE, R, T, attention_reference, make_block  # noqa: E402
+
+# counts, rows of the call, and how many of them are to be written: more tokens than rows, negative counts, fewer rows than
+# the plan, a pool of 7 pages that ends inside a request, rows of 6 pages
+STEPS = [((30, 40, 5), 48, (30, 18, 0)), ((1, -9, 3), 48, (1, 0, 3)), ((1, 30, 9), 20, (1, 19, 0)), ((-1, 1, 1), 48, (0, 1, 1)),
+         ((15, 30, 2), 48, (15, 10, 2)), ((5, 1, 1), 48, (1, 0, 1))]
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_steps_that_lose_tokens(captured):
+    b = make_block(41, "osc").attention
+    pages = blk.Pages(torch, R, 7, PAGE, MB, T, DEV)
+    cache = blk.LayerCache(torch, pages, HKV, D, DEV)
+    cache.KC.fill_(1000.0), cache.VC.fill_(1000.0)  # what no step has written
+    bufs, y = b.buffers(T, pages, DEV), torch.empty((T, H), dtype=torch.bfloat16, device=DEV)
+    x = torch.zeros((T, H), dtype=torch.bfloat16, device=DEV)
+
+    def step(S):
+        pages.plan()
+        b.qkv.quantize(x, S, bufs["x"])
+        b.forward_quantized(S, pages, cache, bufs, y)
+        pages.advance()
+
+    graphs = {}
+    if captured:
+        for S in sorted({S for _, S, _ in STEPS}):
+            graphs[S] = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graphs[S], stream=torch.cuda.Stream()):
+                step(S)
+    g = torch.Generator(device=DEV).manual_seed(8)
+    history, lost = [[] for _ in range(R)], 0
+    for counts, S, wrote in STEPS:
+        pages.new.copy_(torch.tensor(counts, dtype=torch.int32))
+        x.copy_(torch.randn((T, H), generator=g, device=DEV).bfloat16())
+        torch.cuda.synchronize()
+        graphs[S].replay() if captured else step(S)
+        torch.cuda.synchronize()
+        t0 = np.concatenate([[0], np.cumsum(np.maximum(counts, 0))])
+        for r in range(R):
+            history[r] += list(bufs["qkv"][t0[r]:t0[r] + wrote[r]].clone())
+        lost += sum(max(c, 0) for c in counts) - sum(wrote)
+        assert pages.ctx.tolist() == [len(h) for h in history] and int(pages.lost) == lost
+        ref, tol = attention_reference(b, history, bufs["qkv"], wrote, t0)
+        ok = (bufs["o"].double() - ref).abs() <= tol
+        for r in range(R):
+            assert bool(ok[t0[r]:t0[r] + wrote[r]].all()), (counts, r)
+    used = int(pages.head)
+    held = [id for r in range(R) for id in pages.table[r, :-(-len(history[r]) // PAGE)].tolist()]
+    assert sorted(held + pages.free[used:].tolist()) == list(range(7))
+    with pytest.raises(RuntimeError, match=f"{lost} tokens"):
+        pages.check()
+    pages.check()

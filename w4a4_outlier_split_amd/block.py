@@ -219,24 +219,48 @@ def rope_table(torch, P: int, D: int, theta: float, device):
 class Pages:
     """The page tables of R requests, shared by all layers: NP pages of ``page`` tokens, at most MB
     pages a request, steps of at most T new tokens.  One step: set ``new`` (int32 [R], device), call
-    ``plan``, run the blocks, call ``advance``.  All three are captureable in a graph."""
+    ``plan``, run the blocks, call ``advance``.  All three are captureable in a graph.
+
+    New tokens that find no row of the step, no free page or no room in their request's MB pages are
+    lost: nothing of them is written, their rows of the step's output mean nothing, ``ctx`` does not count
+    them, and ``lost`` (int32 [1], device) does.  They are a request's last ones, so ``ctx`` tells what is
+    left to be given again.  ``rows`` is how many rows the blocks ran with since the plan (T until then).
+    Table entries behind a request's ceil(ctx / page) first mean nothing."""
 
     def __init__(self, torch, R: int, NP: int, page: int, MB: int, T: int, device):
-        self.torch, self.R, self.NP, self.page, self.MB, self.T = torch, R, NP, page, MB, T
+        self.torch, self.R, self.NP, self.page, self.MB, self.T, self.rows = torch, R, NP, page, MB, T, T
         i32 = lambda *n: torch.zeros(n, dtype=torch.int32, device=device)
         self.ctx, self.new, self.kv, self.cu = i32(R), i32(R), i32(R), i32(R + 1)
-        self.slot, self.pos, self.used, self.head = i32(T), i32(T), i32(1), i32(1)
+        self.slot, self.pos, self.used, self.head, self.lost = i32(T), i32(T), i32(1), i32(1), i32(1)
+        self.placed = i32(2, T + 1)  # advance's
         self.table = torch.full((R, MB), -1, dtype=torch.int32, device=device)
         self.free = torch.arange(NP, dtype=torch.int32, device=device)
 
     def plan(self, stream=None) -> None:
+        self.rows = self.T
         osc_page_plan(self.ctx, self.new, self.R, self.page, self.NP, self.free, self.free.numel(), self.head, self.T, self.table,
                       self.MB, self.cu, self.kv, self.slot, self.pos, self.used, stream)
 
     def advance(self) -> None:
         """The step's tokens are in the cache now (on torch's current stream)."""
-        self.ctx.add_(self.new)
-        self.head.add_(self.used)
+        torch, rows = self.torch, self.rows
+        # tokens with a slot ahead of each row.  (The second line is for nothing: a single one would be scanned by a
+        # library call whose fitness for a graph is not known.)
+        torch.ge(self.slot[:rows], 0, out=self.placed[0, 1:rows + 1])
+        ahead = self.placed[:, :rows + 1].cumsum(1, dtype=torch.int32)[0].index_select(0, self.cu.clamp(max=rows))
+        # a request's written tokens are its first ones, and their pages the first of those that the step took
+        wrote = ahead[1:] - ahead[:-1]
+        in_last = (self.ctx - 1) & (self.page - 1)  # of a request's last page, less one; a whole page where there is none
+        self.head.add_(((in_last + wrote) >> (self.page.bit_length() - 1)).sum(0, keepdim=True, dtype=torch.int32))
+        self.ctx.add_(wrote)
+        self.lost.add_(self.cu[-1:]).sub_(ahead[-1:])
+
+    def check(self) -> None:
+        """Raises if tokens were lost since the last check.  Waits for the device; not inside a captured graph."""
+        n = int(self.lost)
+        if n:
+            self.lost.zero_()
+            raise RuntimeError(f"{n} tokens found no row, free page or room in their request's {self.MB} pages")
 
     def release(self, rows) -> None:
         """The pages of the finished requests ``rows`` go back to the free list and their rows become
@@ -291,6 +315,7 @@ class Attention:
         """From the QKV projection's quantized input in bufs["x"], by the plan in ``pages``."""
         if S > pages.T:
             raise ValueError(f"{S} rows, and a plan of {pages.T}")
+        pages.rows = min(pages.rows, S)
         self.qkv.gemm(bufs["x"], S, bufs["qkv"], OSC_Y_BF16, stream)
         osc_qkv_append(bufs["qkv"], S, self.HQ, self.HKV, self.D, self.wq, self.wk, self.eps, self.cs,
                        0 if self.cs is None else self.cs.shape[0], pages.pos, pages.slot, bufs["q"], cache.KC, cache.VC, pages.NP,
