@@ -63,3 +63,26 @@ def test_steps_that_lose_tokens(captured):
     with pytest.raises(RuntimeError, match=f"{lost} tokens"):
         pages.check()
     pages.check()
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_steps_on_another_stream(handle):
+    """A step on a stream that lags behind torch's current one: advance goes with it, check and release wait for it."""
+    pages, side = blk.Pages(torch, 2, 8, PAGE, 4, 64, DEV), torch.cuda.Stream()
+    stream = side.cuda_stream if handle else side
+    pages.new.copy_(torch.tensor([40, 3], dtype=torch.int32))
+    torch.cuda.synchronize()
+    for _ in range(2):
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(40_000_000)
+        pages.plan(stream)
+        pages.advance(stream)
+    pages.release([1])
+    assert pages.ctx.tolist() == [64, 0] and int(pages.head) == 4
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(40_000_000)
+    pages.plan(stream)
+    pages.advance(stream)
+    with pytest.raises(RuntimeError, match=f"{16 + 40} tokens"):
+        pages.check()
+    assert pages.ctx.tolist() == [64, 3] and int(pages.head) == 5

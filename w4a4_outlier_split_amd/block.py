@@ -16,6 +16,7 @@ the glue output h = silu(gate) * up of the calibration rows pushed through the u
 """
 from __future__ import annotations
 
+from contextlib import nullcontext
 from dataclasses import dataclass
 from typing import Optional
 
@@ -216,10 +217,17 @@ def rope_table(torch, P: int, D: int, theta: float, device):
     return torch.cat([angle.cos(), angle.sin()], 1).float().contiguous()
 
 
+def _on(torch, stream):
+    """torch's own work on ``stream`` (a Stream or a handle; None: torch's current stream)."""
+    if stream is None:
+        return nullcontext()
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+
+
 class Pages:
     """The page tables of R requests, shared by all layers: NP pages of ``page`` tokens, at most MB
     pages a request, steps of at most T new tokens.  One step: set ``new`` (int32 [R], device), call
-    ``plan``, run the blocks, call ``advance``.  All three are captureable in a graph.
+    ``plan``, run the blocks, call ``advance``, all on one stream.  All three are captureable in a graph.
 
     New tokens that find no row of the step, no free page or no room in their request's MB pages are
     lost: nothing of them is written, their rows of the step's output mean nothing, ``ctx`` does not count
@@ -241,26 +249,34 @@ class Pages:
         osc_page_plan(self.ctx, self.new, self.R, self.page, self.NP, self.free, self.free.numel(), self.head, self.T, self.table,
                       self.MB, self.cu, self.kv, self.slot, self.pos, self.used, stream)
 
-    def advance(self) -> None:
-        """The step's tokens are in the cache now (on torch's current stream)."""
+    def advance(self, stream=None) -> None:
+        """The step's tokens are in the cache now."""
         torch, rows = self.torch, self.rows
-        # tokens with a slot ahead of each row.  (The second line is for nothing: a single one would be scanned by a
-        # library call whose fitness for a graph is not known.)
-        torch.ge(self.slot[:rows], 0, out=self.placed[0, 1:rows + 1])
-        ahead = self.placed[:, :rows + 1].cumsum(1, dtype=torch.int32)[0].index_select(0, self.cu.clamp(max=rows))
-        # a request's written tokens are its first ones, and their pages the first of those that the step took
-        wrote = ahead[1:] - ahead[:-1]
-        in_last = (self.ctx - 1) & (self.page - 1)  # of a request's last page, less one; a whole page where there is none
-        self.head.add_(((in_last + wrote) >> (self.page.bit_length() - 1)).sum(0, keepdim=True, dtype=torch.int32))
-        self.ctx.add_(wrote)
-        self.lost.add_(self.cu[-1:]).sub_(ahead[-1:])
+        with _on(torch, stream):
+            # tokens with a slot ahead of each row.  (The second line is for nothing: a single one would be scanned by a
+            # library call whose fitness for a graph is not known.)
+            torch.ge(self.slot[:rows], 0, out=self.placed[0, 1:rows + 1])
+            ahead = self.placed[:, :rows + 1].cumsum(1, dtype=torch.int32)[0].index_select(0, self.cu.clamp(max=rows))
+            # a request's written tokens are its first ones, and their pages the first of those that the step took
+            wrote = ahead[1:] - ahead[:-1]
+            in_last = (self.ctx - 1) & (self.page - 1)  # of a request's last page, less one; a whole page where there is none
+            self.head.add_(((in_last + wrote) >> (self.page.bit_length() - 1)).sum(0, keepdim=True, dtype=torch.int32))
+            self.ctx.add_(wrote)
+            self.lost.add_(self.cu[-1:]).sub_(ahead[-1:])
 
     def check(self) -> None:
         """Raises if tokens were lost since the last check.  Waits for the device; not inside a captured graph."""
+        self._wait()
         n = int(self.lost)
         if n:
             self.lost.zero_()
+            self._wait()
             raise RuntimeError(f"{n} tokens found no row, free page or room in their request's {self.MB} pages")
+
+    def _wait(self) -> None:
+        """For the device's work on every stream: a step may run on another than torch's current one."""
+        if self.ctx.is_cuda:
+            self.torch.cuda.synchronize(self.ctx.device)
 
     def release(self, rows) -> None:
         """The pages of the finished requests ``rows`` go back to the free list and their rows become
@@ -269,6 +285,7 @@ class Pages:
         rows = [int(r) for r in rows]
         if len(set(rows)) != len(rows) or any(not 0 <= r < self.R for r in rows):
             raise ValueError("rows are distinct requests of this table")
+        self._wait()
         ctx, head = self.ctx.tolist(), int(self.head)
         back = [self.table[r, :-(-ctx[r] // self.page)] for r in rows]
         left = t.cat([self.free[head:], *[b[b >= 0] for b in back]])
@@ -280,6 +297,7 @@ class Pages:
         at = t.tensor(rows, dtype=t.long, device=self.ctx.device)
         self.table[at] = -1
         self.ctx[at] = 0
+        self._wait()
 
 
 class LayerCache:
