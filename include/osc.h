@@ -370,8 +370,9 @@ osc_status osc_page_plan(const int32_t* CTX, const int32_t* NEW, int R, int page
  *   POS, SLOT  int32 [S]: position (read only with CS) and cache slot of each token.
  *   Q    [S][HQ][D] bf16, written (rounded once); KC, VC: the slots of the S tokens written.
  * A token whose slot is outside [0, NP * page), or whose position is outside [0, P), writes
- * nothing: its row of Q stays as it was.  No input overlaps an output.  Slots must be distinct: of two tokens with one slot
- * the cache holds channels of either.
+ * nothing: its row of Q stays as it was.  One that is passed over for its position has a slot all the same, and
+ * osc_page_plan's KV counts it: that row of the attention, and those of the request's later tokens, mean nothing.
+ * No input overlaps an output.  Slots must be distinct: of two tokens with one slot the cache holds channels of either.
  * Constraints: S >= 0, S < 2^24, 1 <= HQ, HKV <= 1024, D in {64, 128}, S (HQ + 2 HKV) D <
  * 2^34, NP >= 1, NP * page < 2^31, eps positive and finite with WQ, P >= 1 with CS.
  */

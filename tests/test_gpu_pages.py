@@ -86,3 +86,46 @@ def test_steps_on_another_stream(handle):
     with pytest.raises(RuntimeError, match=f"{16 + 40} tokens"):
         pages.check()
     assert pages.ctx.tolist() == [64, 3] and int(pages.head) == 5
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_positions_behind_the_rotary_table(captured):
+    """The table ends at 40 of 96 positions: check says how many tokens are behind it, the others are as ever."""
+    b = make_block(43, "osc").attention
+    b.cs = b.cs[:40]
+    pages = blk.Pages(torch, R, 18, PAGE, MB, T, DEV)
+    cache, bufs = blk.LayerCache(torch, pages, HKV, D, DEV), b.buffers(T, pages, DEV)
+    x, y = (torch.zeros((T, H), dtype=torch.bfloat16, device=DEV) for _ in range(2))
+
+    def step():
+        pages.plan()
+        b.qkv.quantize(x, T, bufs["x"])
+        b.forward_quantized(T, pages, cache, bufs, y)
+        pages.advance()
+
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+            step()
+    g = torch.Generator(device=DEV).manual_seed(9)
+    history, seen = [[] for _ in range(R)], [0] * R
+    for counts, lost in (((30, 5, 2), 0), ((8, 1, 38), 0), ((5, 20, 1), 3 + 1), ((1, 13, 0), 1)):
+        pages.new.copy_(torch.tensor(counts, dtype=torch.int32))
+        x.copy_(torch.randn((T, H), generator=g, device=DEV).bfloat16())
+        torch.cuda.synchronize()
+        graph.replay() if captured else step()
+        torch.cuda.synchronize()
+        t0 = np.concatenate([[0], np.cumsum(counts)])
+        good = [min(n, max(0, 40 - seen[r])) for r, n in enumerate(counts)]
+        for r in range(R):
+            history[r] += list(bufs["qkv"][t0[r]:t0[r] + good[r]].clone())
+            seen[r] += counts[r]
+        ref, tol = attention_reference(b, history, bufs["qkv"], good, t0)
+        ok = (bufs["o"].double() - ref).abs() <= tol
+        for r in range(R):
+            assert bool(ok[t0[r]:t0[r] + good[r]].all()), (counts, r)
+        assert pages.ctx.tolist() == seen
+        if lost:
+            with pytest.raises(RuntimeError, match=f"{lost} tokens"):
+                pages.check()
+        pages.check()

@@ -92,6 +92,27 @@ def test_negative_counts_are_idle():
     p.check()
 
 
+def test_positions_behind_the_rotary_table():
+    """The blocks wrote nothing for them: ``lost`` says so, and the request keeps its pages."""
+    p = HostPages(torch, 2, 12, 16, 4, 100, "cpu")
+
+    def run(new, rows=100):
+        p.new.copy_(torch.tensor(new, dtype=torch.int32))
+        p.plan()
+        p.rows, p.positions = rows, 40
+        p.advance()
+
+    run([30, 40])
+    p.check()
+    run([15, 2])
+    assert p.ctx.tolist() == [45, 42] and int(p.lost) == 5 + 2 and int(p.head) == 6
+    run([3, 60], rows=10)
+    assert p.ctx.tolist() == [48, 49] and int(p.lost) == 7 + 3 + 60 and int(p.head) == 7
+    p.release([1])
+    run([0, 50])
+    assert p.ctx.tolist() == [48, 50] and int(p.lost) == 70 + 10 and int(p.head) == 7
+
+
 def test_pool_and_row_run_out():
     p, cache = HostPages(torch, 3, 5, 16, 4, 200, "cpu"), {}
     step(p, cache, [30, 70, 5])  # two pages, then room for 64 and pages for 48, then none

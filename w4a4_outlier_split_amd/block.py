@@ -232,20 +232,22 @@ class Pages:
     New tokens that find no row of the step, no free page or no room in their request's MB pages are
     lost: nothing of them is written, their rows of the step's output mean nothing, ``ctx`` does not count
     them, and ``lost`` (int32 [1], device) does.  They are a request's last ones, so ``ctx`` tells what is
-    left to be given again.  ``rows`` is how many rows the blocks ran with since the plan (T until then).
-    Table entries behind a request's ceil(ctx / page) first mean nothing."""
+    left to be given again.  A request that passes the end of the blocks' rotary table cannot go on: ``ctx``
+    does count those tokens, with their pages, and so does ``lost``.  ``rows`` is how many rows the blocks ran
+    with since the plan (T until then), ``positions`` how many their rotary table has.  Table entries behind a request's ceil(ctx / page) first mean nothing."""
 
     def __init__(self, torch, R: int, NP: int, page: int, MB: int, T: int, device):
         self.torch, self.R, self.NP, self.page, self.MB, self.T, self.rows = torch, R, NP, page, MB, T, T
+        self.positions = MB * page
         i32 = lambda *n: torch.zeros(n, dtype=torch.int32, device=device)
         self.ctx, self.new, self.kv, self.cu = i32(R), i32(R), i32(R), i32(R + 1)
         self.slot, self.pos, self.used, self.head, self.lost = i32(T), i32(T), i32(1), i32(1), i32(1)
-        self.placed = i32(2, T + 1)  # advance's
+        self.placed = i32(2, T + 1)  # advance's: which rows have a slot, and which were written
         self.table = torch.full((R, MB), -1, dtype=torch.int32, device=device)
         self.free = torch.arange(NP, dtype=torch.int32, device=device)
 
     def plan(self, stream=None) -> None:
-        self.rows = self.T
+        self.rows, self.positions = self.T, self.MB * self.page
         osc_page_plan(self.ctx, self.new, self.R, self.page, self.NP, self.free, self.free.numel(), self.head, self.T, self.table,
                       self.MB, self.cu, self.kv, self.slot, self.pos, self.used, stream)
 
@@ -253,16 +255,21 @@ class Pages:
         """The step's tokens are in the cache now."""
         torch, rows = self.torch, self.rows
         with _on(torch, stream):
-            # tokens with a slot ahead of each row.  (The second line is for nothing: a single one would be scanned by a
-            # library call whose fitness for a graph is not known.)
-            torch.ge(self.slot[:rows], 0, out=self.placed[0, 1:rows + 1])
-            ahead = self.placed[:, :rows + 1].cumsum(1, dtype=torch.int32)[0].index_select(0, self.cu.clamp(max=rows))
-            # a request's written tokens are its first ones, and their pages the first of those that the step took
+            # tokens with a slot, and written tokens, ahead of each row.  (A single line would be scanned by a library
+            # call whose fitness for a graph is not known.)
+            flags = self.placed[:, :rows + 1]
+            torch.ge(self.slot[:rows], 0, out=flags[0, 1:])
+            short = self.positions < self.MB * self.page
+            if short:
+                torch.mul(flags[0, 1:], self.pos[:rows] < self.positions, out=flags[1, 1:])
+            sums = flags.cumsum(1, dtype=torch.int32)
+            ahead = sums[0].index_select(0, self.cu.clamp(max=rows))
+            # a request's tokens with a slot are its first ones, and their pages the first of those that the step took
             wrote = ahead[1:] - ahead[:-1]
             in_last = (self.ctx - 1) & (self.page - 1)  # of a request's last page, less one; a whole page where there is none
             self.head.add_(((in_last + wrote) >> (self.page.bit_length() - 1)).sum(0, keepdim=True, dtype=torch.int32))
             self.ctx.add_(wrote)
-            self.lost.add_(self.cu[-1:]).sub_(ahead[-1:])
+            self.lost.add_(self.cu[-1:]).sub_(sums[1 if short else 0, -1:])
 
     def check(self) -> None:
         """Raises if tokens were lost since the last check.  Waits for the device; not inside a captured graph."""
@@ -271,7 +278,7 @@ class Pages:
         if n:
             self.lost.zero_()
             self._wait()
-            raise RuntimeError(f"{n} tokens found no row, free page or room in their request's {self.MB} pages")
+            raise RuntimeError(f"{n} tokens found no row, free page, room in their request's {self.MB} pages or rotary table")
 
     def _wait(self) -> None:
         """For the device's work on every stream: a step may run on another than torch's current one."""
@@ -334,6 +341,8 @@ class Attention:
         if S > pages.T:
             raise ValueError(f"{S} rows, and a plan of {pages.T}")
         pages.rows = min(pages.rows, S)
+        if self.cs is not None:  # tokens behind its end are passed over by the append
+            pages.positions = min(pages.positions, self.cs.shape[0])
         self.qkv.gemm(bufs["x"], S, bufs["qkv"], OSC_Y_BF16, stream)
         osc_qkv_append(bufs["qkv"], S, self.HQ, self.HKV, self.D, self.wq, self.wk, self.eps, self.cs,
                        0 if self.cs is None else self.cs.shape[0], pages.pos, pages.slot, bufs["q"], cache.KC, cache.VC, pages.NP,
