@@ -294,11 +294,13 @@ def osc_attn_workspace(S: int, R: int, HQ: int, HKV: int, D: int, page: int, MB:
 
 def osc_attn_paged(Q, KC, VC, S: int, R: int, HQ: int, HKV: int, D: int, page: int, MB: int, NP: int, TABLE, CU, KV,
                    scale: float, O, WS, stream=None) -> None:
-    """Causal attention of the new tokens of R requests over the paged cache; WS: a tensor of at least
-    osc_attn_workspace bytes, or None where that is 0."""
+    """Causal attention of the new tokens of R requests over the paged cache; WS: a tensor (or the
+    address) of at least osc_attn_workspace bytes, or None where that is 0."""
     c = "osc_attn_paged"
     d = torch.cuda.current_device()
     n, q = 2 * NP * HKV * page * D, 2 * S * HQ * D
+    # the caller of an address answers for its bytes, as everywhere
+    ws = 0 if WS is None else osc_attn_workspace(S, R, HQ, HKV, D, page, MB) if type(WS) is int else WS.nbytes
     _check(_lib.osc_attn_paged(_at(c, d, Q, q), _at(c, d, KC, n), _at(c, d, VC, n), S, R, HQ, HKV, D, page, MB, NP,
                                _at(c, d, TABLE, 4 * R * MB), _at(c, d, CU, 4 * R + 4), _at(c, d, KV, 4 * R), scale, _at(c, d, O, q),
-                               _at(c, d, WS, 0), 0 if WS is None else WS.nbytes, _stream(stream)), c)
+                               _at(c, d, WS, 0), ws, _stream(stream)), c)
