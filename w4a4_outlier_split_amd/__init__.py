@@ -225,13 +225,20 @@ def osc_build_table_multi(Xcal, R: int, H: int, G: int, alpha: float, rho: float
 
 # ---- between the projections: norm, paged cache, attention
 
-def _at(call: str, dev: int, t, need: int) -> Optional[int]:
+_BF16 = (torch.bfloat16, torch.int16, torch.uint16)  # the values or their bits
+_I32 = (torch.int32,)
+_F32 = (torch.float32,)
+
+
+def _at(call: str, dev: int, t, need: int, types=None) -> Optional[int]:
     """Address of a tensor (or an address, or None) of which the call reads or writes ``need`` contiguous
-    bytes on the current device ``dev``."""
+    bytes on the current device ``dev``; types: those that the elements may have, None for plain bytes."""
     if t is None or type(t) is int:
         return t
     if t.get_device() != dev:
         raise OscError(2, call, f"a tensor on {t.device}, the current device is cuda:{dev}")
+    if types is not None and t.dtype not in types:
+        raise OscError(5, call, f"a tensor of {t.dtype} where {types[0]} is read or written")
     if not t.is_contiguous() or t.nbytes < need:
         raise OscError(2, call, f"a tensor of {t.nbytes} bytes, strides {tuple(t.stride())}, where {need} contiguous "
                                 "bytes are needed")
@@ -248,9 +255,9 @@ def osc_rmsnorm_quant(X, RES, W, S: int, H: int, eps: float, G: int, L, m: int, 
     if keep is not None and keep.size < H // g * m:
         raise OscError(3, c, f"{keep.size} table entries for {H // g} groups of {m}")
     d = torch.cuda.current_device()
-    _check(_lib.osc_rmsnorm_quant(_at(c, d, X, n), _at(c, d, RES, n), _at(c, d, W, 2 * H), S, H, eps, G, lp, m, afmt,
-                                  _at(c, d, RES_OUT, n), _at(c, d, QX, code_bytes(S, H, afmt)),
-                                  _at(c, d, SX, scale_bytes(S, H, g, afmt)), _at(c, d, B, 2 * side_elems(S, H, g, m)),
+    _check(_lib.osc_rmsnorm_quant(_at(c, d, X, n, _BF16), _at(c, d, RES, n, _BF16), _at(c, d, W, 2 * H, _BF16),
+                                  S, H, eps, G, lp, m, afmt, _at(c, d, RES_OUT, n, _BF16), _at(c, d, QX, code_bytes(S, H, afmt)),
+                                  _at(c, d, SX, scale_bytes(S, H, g, afmt)), _at(c, d, B, 2 * side_elems(S, H, g, m), _BF16),
                                   _stream(stream)), c)
 
 
@@ -259,8 +266,8 @@ def osc_rmsnorm(X, RES, W, S: int, H: int, eps: float, RES_OUT, Y, stream=None) 
     c = "osc_rmsnorm"
     n = 2 * S * H
     d = torch.cuda.current_device()
-    _check(_lib.osc_rmsnorm(_at(c, d, X, n), _at(c, d, RES, n), _at(c, d, W, 2 * H), S, H, eps, _at(c, d, RES_OUT, n),
-                            _at(c, d, Y, n), _stream(stream)), c)
+    _check(_lib.osc_rmsnorm(_at(c, d, X, n, _BF16), _at(c, d, RES, n, _BF16), _at(c, d, W, 2 * H, _BF16),
+                            S, H, eps, _at(c, d, RES_OUT, n, _BF16), _at(c, d, Y, n, _BF16), _stream(stream)), c)
 
 
 def osc_page_plan(CTX, NEW, R: int, page: int, NP: int, FREE, F: int, HEAD, T: int, TABLE, MB: int, CU, KV, SLOT, POS, USED,
@@ -268,10 +275,10 @@ def osc_page_plan(CTX, NEW, R: int, page: int, NP: int, FREE, F: int, HEAD, T: i
     """Page tables and slot maps of one step from request lengths (all int32 device tensors)."""
     c = "osc_page_plan"
     d = torch.cuda.current_device()
-    _check(_lib.osc_page_plan(_at(c, d, CTX, 4 * R), _at(c, d, NEW, 4 * R), R, page, NP, _at(c, d, FREE, 4 * F), F,
-                              _at(c, d, HEAD, 4), T, _at(c, d, TABLE, 4 * R * MB), MB, _at(c, d, CU, 4 * R + 4),
-                              _at(c, d, KV, 4 * R), _at(c, d, SLOT, 4 * T), _at(c, d, POS, 4 * T), _at(c, d, USED, 4),
-                              _stream(stream)), c)
+    _check(_lib.osc_page_plan(_at(c, d, CTX, 4 * R, _I32), _at(c, d, NEW, 4 * R, _I32), R, page, NP,
+                              _at(c, d, FREE, 4 * F, _I32), F, _at(c, d, HEAD, 4, _I32), T, _at(c, d, TABLE, 4 * R * MB, _I32), MB,
+                              _at(c, d, CU, 4 * R + 4, _I32), _at(c, d, KV, 4 * R, _I32), _at(c, d, SLOT, 4 * T, _I32),
+                              _at(c, d, POS, 4 * T, _I32), _at(c, d, USED, 4, _I32), _stream(stream)), c)
 
 
 def osc_qkv_append(QKV, S: int, HQ: int, HKV: int, D: int, WQ, WK, eps: float, CS, P: int, POS, SLOT, Q, KC, VC, NP: int,
@@ -280,9 +287,10 @@ def osc_qkv_append(QKV, S: int, HQ: int, HKV: int, D: int, WQ, WK, eps: float, C
     c = "osc_qkv_append"
     d = torch.cuda.current_device()
     n = 2 * NP * HKV * page * D
-    _check(_lib.osc_qkv_append(_at(c, d, QKV, 2 * S * (HQ + 2 * HKV) * D), S, HQ, HKV, D, _at(c, d, WQ, 2 * D), _at(c, d, WK, 2 * D),
-                               eps, _at(c, d, CS, 4 * P * D), P, _at(c, d, POS, 4 * S), _at(c, d, SLOT, 4 * S),
-                               _at(c, d, Q, 2 * S * HQ * D), _at(c, d, KC, n), _at(c, d, VC, n), NP, page, _stream(stream)), c)
+    _check(_lib.osc_qkv_append(_at(c, d, QKV, 2 * S * (HQ + 2 * HKV) * D, _BF16), S, HQ, HKV, D,
+                               _at(c, d, WQ, 2 * D, _BF16), _at(c, d, WK, 2 * D, _BF16), eps, _at(c, d, CS, 4 * P * D, _F32), P,
+                               _at(c, d, POS, 4 * S, _I32), _at(c, d, SLOT, 4 * S, _I32), _at(c, d, Q, 2 * S * HQ * D, _BF16),
+                               _at(c, d, KC, n, _BF16), _at(c, d, VC, n, _BF16), NP, page, _stream(stream)), c)
 
 
 def osc_attn_workspace(S: int, R: int, HQ: int, HKV: int, D: int, page: int, MB: int) -> int:
@@ -301,6 +309,6 @@ def osc_attn_paged(Q, KC, VC, S: int, R: int, HQ: int, HKV: int, D: int, page: i
     n, q = 2 * NP * HKV * page * D, 2 * S * HQ * D
     # the caller of an address answers for its bytes, as everywhere
     ws = 0 if WS is None else osc_attn_workspace(S, R, HQ, HKV, D, page, MB) if type(WS) is int else WS.nbytes
-    _check(_lib.osc_attn_paged(_at(c, d, Q, q), _at(c, d, KC, n), _at(c, d, VC, n), S, R, HQ, HKV, D, page, MB, NP,
-                               _at(c, d, TABLE, 4 * R * MB), _at(c, d, CU, 4 * R + 4), _at(c, d, KV, 4 * R), scale, _at(c, d, O, q),
-                               _at(c, d, WS, 0), ws, _stream(stream)), c)
+    _check(_lib.osc_attn_paged(_at(c, d, Q, q, _BF16), _at(c, d, KC, n, _BF16), _at(c, d, VC, n, _BF16), S, R, HQ, HKV, D, page,
+                               MB, NP, _at(c, d, TABLE, 4 * R * MB, _I32), _at(c, d, CU, 4 * R + 4, _I32), _at(c, d, KV, 4 * R, _I32),
+                               scale, _at(c, d, O, q, _BF16), _at(c, d, WS, 0), ws, _stream(stream)), c)
