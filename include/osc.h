@@ -302,7 +302,7 @@ osc_status osc_swiglu(const void* GU, int S, int F, void* Hout, void* stream);
  *        block's input, without RES).
  *   RES  [S][H] bf16 residual stream or NULL; RES_OUT [S][H] bf16, written, NULL
  *        exactly when RES is.  RES_OUT may be RES itself (updated in place); no other
- *        operand may overlap an output.
+ *        operand may overlap an output (OSC_E_SHAPE).
  *   W    [H] bf16 norm weight.
  *   r = RES ? bf16(X + RES) : X, to RES_OUT;  y = bf16(r * (1 / sqrt(mean(r^2) + eps)) * w)
  *   with the mean, the root and the products in binary32 and one rounding (nearest,
@@ -349,7 +349,7 @@ osc_status osc_rmsnorm(const void* X, const void* RES, const void* W, int S, int
  * What does not fit: a page behind FREE's end or outside [0, NP) is entered as -1, and
  * tokens in it, or at positions >= MB * page, get slot -1 (osc_qkv_append skips them; USED
  * > F - *HEAD tells).  Tokens >= T are counted in CU but not mapped.  Sums saturate at 2^31 - 1.
- * No input overlaps an output (KV is not CTX or NEW, USED is not HEAD: OSC_E_SHAPE).
+ * No operand overlaps an output (KV is not CTX or NEW, USED is not HEAD, ...: OSC_E_SHAPE).
  * The call reads no entry that it writes: repeated on the same inputs (a replayed graph) it
  * gives the same tables.  One launch.
  * Constraints: 0 <= R <= OSC_MAX_REQUESTS, F, T >= 0, NP, MB >= 1, NP * page < 2^31,
@@ -372,7 +372,7 @@ osc_status osc_page_plan(const int32_t* CTX, const int32_t* NEW, int R, int page
  * A token whose slot is outside [0, NP * page), or whose position is outside [0, P), writes
  * nothing: its row of Q stays as it was.  One that is passed over for its position has a slot all the same, and
  * osc_page_plan's KV counts it: that row of the attention, and those of the request's later tokens, mean nothing.
- * No input overlaps an output.  Slots must be distinct: of two tokens with one slot the cache holds channels of either.
+ * No operand overlaps an output (OSC_E_SHAPE).  Slots must be distinct: of two tokens with one slot the cache holds channels of either.
  * Constraints: S >= 0, S < 2^24, 1 <= HQ, HKV <= 1024, D in {64, 128}, S (HQ + 2 HKV) D <
  * 2^34, NP >= 1, NP * page < 2^31, eps positive and finite with WQ, P >= 1 with CS.
  */
@@ -388,7 +388,7 @@ osc_status osc_qkv_append(const void* QKV, int S, int HQ, int HKV, int D, const 
  * with scores, softmax and sums in binary32 and the weights rounded to bf16 for the second
  * product.  n = 1 is a decode step, KV = n a whole prompt, anything between a chunk; the
  * requests of one call may differ.
- *   Q, O [S][HQ][D] bf16 (O overlaps no other operand); CU int32 [R + 1], 0 <= CU[r] <=
+ *   Q, O [S][HQ][D] bf16 (no operand overlaps O or WS: OSC_E_SHAPE); CU int32 [R + 1], 0 <= CU[r] <=
  *   CU[r + 1]; KV int32 [R] (negative counts as 0).
  * A token that sees no key (KV < n, or no page of its keys exists) gets zeros; keys whose
  * page does not exist, and those at positions >= MB * page, are left out, and tokens >= S

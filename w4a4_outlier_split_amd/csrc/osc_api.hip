@@ -6,6 +6,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <initializer_list>
+
 #include "osc_internal.h"
 
 namespace {
@@ -69,6 +71,27 @@ int page_shift(int page) {
 // heads of a projection row or of the cache
 bool valid_heads(int HQ, int HKV, int D) {
   return HQ >= 1 && HKV >= 1 && HQ <= 1024 && HKV <= 1024 && (D == 64 || D == 128);
+}
+
+// an operand's bytes
+struct Span {
+  const void* p;
+  long long bytes;
+};
+
+// does an output share bytes with an input, or with another output?
+bool overlap(std::initializer_list<Span> out, std::initializer_list<Span> in) {
+  auto share = [](const Span& a, const Span& b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return a.p && b.p && a.bytes > 0 && b.bytes > 0 && (x < y ? y - x < (uintptr_t)a.bytes : x - y < (uintptr_t)b.bytes);
+  };
+  for (auto o = out.begin(); o != out.end(); ++o) {
+    for (const Span& i : in)
+      if (share(*o, i)) return true;
+    for (auto q = o + 1; q != out.end(); ++q)
+      if (share(*o, *q)) return true;
+  }
+  return false;
 }
 
 // the HIP error behind the calling thread's most recent OSC_E_DEVICE
@@ -297,6 +320,11 @@ osc_status osc_rmsnorm_quant(const void* X, const void* RES, const void* W, int 
     st = pack_table(L, H / G, m, G, &tab);
     if (st != OSC_OK) return st;
   }
+  const long long n = (long long)S * H, K = H / G;
+  const long long codes = afmt == OSC_MXFP4 ? n / 2 : afmt == OSC_MXFP8 ? n : n / 4 * 3;
+  if (overlap({{RES_OUT, 2 * n}, {QX, codes}, {SX, afmt == OSC_FP6P ? n / 32 : S * K}, {B, (m * K + 31) / 32 * 64 * S}},
+              {{X, 2 * n}, {RES == RES_OUT ? nullptr : RES, 2 * n}, {W, 2 * H}}))
+    return OSC_E_SHAPE;
   if (!osc::launch_rmsnorm) return OSC_E_DEVICE;
   osc::NormArgs a{X, RES, W, S, H, eps, G, m, L ? &tab : nullptr, afmt, RES_OUT, QX, SX, B};
   return from_hip(osc::launch_rmsnorm(a, static_cast<hipStream_t>(stream)));
@@ -310,6 +338,8 @@ osc_status osc_rmsnorm(const void* X, const void* RES, const void* W, int S, int
   if (S == 0) return OSC_OK;
   if (!X || !W || !Y || (RES == nullptr) != (RES_OUT == nullptr)) return OSC_E_NULL;
   if (!aligned16(X) || !aligned16(RES) || !aligned16(W) || !aligned16(RES_OUT) || !aligned16(Y)) return OSC_E_ALIGN;
+  const long long n = 2LL * S * H;
+  if (overlap({{RES_OUT, n}, {Y, n}}, {{X, n}, {RES == RES_OUT ? nullptr : RES, n}, {W, 2 * H}})) return OSC_E_SHAPE;
   if (!osc::launch_rmsnorm) return OSC_E_DEVICE;
   osc::NormArgs a{X, RES, W, S, H, eps, 64, 1, nullptr, OSC_MXFP4, RES_OUT, Y, nullptr, nullptr};
   return from_hip(osc::launch_rmsnorm(a, static_cast<hipStream_t>(stream)));
@@ -328,8 +358,10 @@ osc_status osc_page_plan(const int32_t* CTX, const int32_t* NEW, int R, int page
   if (!aligned4(CTX) || !aligned4(NEW) || !aligned4(FREE) || !aligned4(HEAD) || !aligned4(TABLE) || !aligned4(CU) ||
       !aligned4(KV) || !aligned4(SLOT) || !aligned4(POS) || !aligned4(USED))
     return OSC_E_ALIGN;
-  // every workgroup reads the inputs, one of them writes these outputs
-  if ((R > 0 && (KV == CTX || KV == NEW)) || USED == HEAD) return OSC_E_SHAPE;
+  // every workgroup reads the inputs while others write
+  const long long r = 4LL * R, t = 4LL * T;
+  if (overlap({{TABLE, r * MB}, {CU, r + 4}, {KV, r}, {SLOT, t}, {POS, t}, {USED, 4}}, {{CTX, r}, {NEW, r}, {FREE, 4LL * F}, {HEAD, 4}}))
+    return OSC_E_SHAPE;
   if (!osc::launch_page_plan) return OSC_E_DEVICE;
   osc::PlanArgs a{CTX, NEW, R, sh, NP, FREE, F, HEAD, T, TABLE, MB, CU, KV, SLOT, POS, USED};
   return from_hip(osc::launch_page_plan(a, static_cast<hipStream_t>(stream)));
@@ -348,6 +380,10 @@ osc_status osc_qkv_append(const void* QKV, int S, int HQ, int HKV, int D, const 
   if (!aligned16(QKV) || !aligned16(WQ) || !aligned16(WK) || !aligned16(CS) || !aligned16(Q) || !aligned16(KC) ||
       !aligned16(VC) || !aligned4(POS) || !aligned4(SLOT))
     return OSC_E_ALIGN;
+  const long long row = 2LL * S * D, cache = (2LL * NP * HKV * D) << sh;
+  if (overlap({{Q, row * HQ}, {KC, cache}, {VC, cache}},
+              {{QKV, row * (HQ + 2 * HKV)}, {WQ, 2 * D}, {WK, 2 * D}, {CS, 4LL * P * D}, {POS, CS ? 4LL * S : 0}, {SLOT, 4LL * S}}))
+    return OSC_E_SHAPE;
   if (!osc::launch_qkv_append) return OSC_E_DEVICE;
   osc::AppendArgs a{QKV, S, HQ, HKV, D, WQ, WK, eps, CS, P, POS, SLOT, Q, KC, VC, NP, sh};
   return from_hip(osc::launch_qkv_append(a, static_cast<hipStream_t>(stream)));
@@ -388,6 +424,9 @@ osc_status osc_attn_paged(const void* Q, const void* KC, const void* VC, int S, 
   if (!aligned16(Q) || !aligned16(KC) || !aligned16(VC) || !aligned16(O) || !aligned16(WS) || !aligned4(TABLE) ||
       !aligned4(CU) || !aligned4(KV))
     return OSC_E_ALIGN;
+  const long long rows = 2LL * S * HQ * D, cache = (2LL * NP * HKV * D) << sh, r = 4LL * R;
+  if (overlap({{O, rows}, {WS, p.ws_bytes}}, {{Q, rows}, {KC, cache}, {VC, cache}, {TABLE, r * MB}, {CU, r + 4}, {KV, r}}))
+    return OSC_E_SHAPE;
   osc::AttnArgs a{Q,  KC,   VC, S,  R,  HQ, HKV, HQ / HKV, sh, page - 1, MB, NP, TABLE, CU, KV, scale_log2,
                   O,  nullptr, nullptr, nullptr, p.target};
   if (p.ws_bytes > 0) {  // notes, then 2 and D values a row
