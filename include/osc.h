@@ -399,7 +399,9 @@ osc_status osc_qkv_append(const void* QKV, int S, int HQ, int HKV, int D, const 
  *   WS, ws_bytes: device workspace of at least osc_attn_workspace's bytes for the same
  *   sizes (WS may be NULL when that is 0; fewer tokens may need more), free again when the call's work is done: calls
  *   that can overlap, two graphs replayed on two streams included, need one each.
- * The result does not depend on what else runs (sums are joined in a fixed order).
+ * The result does not depend on what else runs (sums are joined in a fixed order).  Rows that no request has (room in
+ * a captured step) cost little, but: with S <= R the work is laid out for single tokens, and that of a single request
+ * whose table holds no more than S + 256 keys for S tokens, whatever it brings.
  * Constraints: S >= 0, S < 2^24, 0 <= R <= OSC_MAX_REQUESTS, HQ a multiple of HKV, both in
  * 1..1024, D in {64, 128}, S * HQ * D < 2^34, NP, MB >= 1, NP * page < 2^31, MB * page <=
  * 2^30, scale positive and scale * log2 e finite; too small a workspace is OSC_E_SHAPE.

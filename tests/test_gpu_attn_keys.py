@@ -97,3 +97,24 @@ def test_any_lengths(seed):
         reqs.append((kv, int(rng.choice([0, 1, min(kv, 33), int(rng.integers(0, min(kv, 1200) + 1))]))))
     reqs.append((50, 3))
     check_every_key(reqs, HQ, HKV, int(rng.choice([64, 128])), int(rng.choice([16, 32, 64, 128, 256])), int(rng.choice([0, 30000])))
+
+
+@pytest.mark.parametrize("reqs", [[(9000, 1)], [(5000, 40)], [(700, 700)]])
+@pytest.mark.parametrize("HQ,HKV,D", [(32, 8, 128), (8, 1, 64)])
+def test_room_for_more_rows_changes_no_bit(reqs, HQ, HKV, D):
+    """A call's rows without a token neither change how the others' work is cut, nor the results."""
+    (kv, n), page, MB = reqs[0], 64, 640
+    g = torch.Generator(device=DEV).manual_seed(kv)
+    NP = -(-kv // page)
+    KC, VC = (torch.randn((NP, HKV, page * D), generator=g, device=DEV).bfloat16() for _ in range(2))
+    Q = torch.randn((8192, HQ, D), generator=g, device=DEV).bfloat16()
+    table = torch.full((1, MB), -1, dtype=torch.int32, device=DEV)
+    table[0, :NP] = torch.arange(NP, device=DEV)
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device=DEV)
+    got = []
+    for S in (max(n, 2), n + 300, 8192):
+        O = poisoned((S, HQ, D), torch.bfloat16)
+        ws = poisoned((osc.osc_attn_workspace(S, 1, HQ, HKV, D, page, MB),), torch.uint8)
+        osc.osc_attn_paged(Q, KC, VC, S, 1, HQ, HKV, D, page, MB, NP, table, i32(0, n), i32(kv), D ** -0.5, O, ws)
+        got.append(O[:n])
+    assert torch.equal(got[1], got[0]) and torch.equal(got[2], got[0])

@@ -33,8 +33,11 @@
 // that it sees, and the row is cut into as many equal parts as workgroups run at once.  A workgroup takes
 // its part, tile by tile.  A tile that a cut goes through has its unnormalised outputs left in the workspace, at
 // most two tiles for a workgroup, and a second launch joins them in a fixed order.  The lengths are on the
-// device, so each wavefront works the cuts out for itself.  (Four chunks of up to 1024 tokens behind up to 8192, 135 GFLOP:
-// 154 us and 20 for the join of 58 MB.)  Where there are many tiles they are left whole instead, see attn_plan.
+// device, so each wavefront works the cuts out for itself.  (Chunks of 1024 and 765 tokens behind 1320 and 7946 keys, beside two
+// idle requests, 135 GFLOP: 168 to 175 us, 20 of them for the join of 58 MB.)  Large tiles are left whole instead where that is
+// quicker (whole_pays), which each wavefront finds from the lengths as well: one launch serves both.  (A choice by the host could
+// go by the call's rows only, tokens or not: one token over 32000 keys in a call with room for 8192 then took 480 us, 39 so.  Two
+// launches of which one has nothing to do take 2 to 3 us more.)
 #include "osc_device.h"
 #include "osc_internal.h"
 
@@ -563,25 +566,29 @@ __device__ __forceinline__ long divide(long a, long b) {
 }
 
 // Whole tiles or cut ones?  A key head has s CUs to itself.  Whole, its tiles take as long as the CU that has most of
-// them; cut, a CU's even share, a quarter more for partial outputs and keys that are no longer read in step,
-// and what 1500 keys take for the second launch.  With three tiles a CU and more, the share is what counts as long as
-// no tile is longer; with fewer, a CU has the longest tile beside its share at worst.
+// them; cut, a CU's even share, a quarter more for partial outputs and keys that are no longer read in step, and `once` keys' time
+// for pieces of tiles and the join: 1000, and 500 more where whole tiles would save the join's launch.  With three tiles a CU
+// and more, the share is what counts as long as no tile is longer; with fewer, a CU has the longest tile beside its share at
+// worst.  (Of 551 calls with both sides measured, 2 to 6000 tokens of 1 to 40 requests on 1 to 32 key heads, this takes the slower
+// side's time by more than a twentieth in 28, by more than an eighth in 14; with 1500 keys in 76 and 53.)
+constexpr int kOnce = 1000, kOnceAndLaunch = 1500;
 __host__ __device__ inline long slots_of(int HKV) { return HKV < kCUs ? kCUs / HKV : 1; }
-__host__ __device__ inline bool whole_pays(long s, long tiles, long most, long all) {
-  return 4 * most * s <= all + 6000 * s || (tiles >= 3 * s && most * s <= all);
+__host__ __device__ inline bool whole_pays(long s, long tiles, long most, long all, long once) {
+  return 4 * most * s <= all + 4 * once * s || (tiles >= 3 * s && most * s <= all);
 }
 // One request with tiles of base + tau, base + 2 tau, ... keys, the longest first: a CU has one, or two of which the
 // longest pair is the s-th and the next.
-__host__ __device__ inline bool whole_pays_alone(long s, long tiles, long base, long tau) {
+__host__ __device__ inline bool whole_pays_alone(long s, long tiles, long base, long tau, long once) {
   if (tiles > 2 * s) return true;
   const long one = base + tau * tiles, two = tiles > s ? 2 * base + tau * (2 * tiles + 1 - 2 * s) : 0;
   const long all = tiles * base + tau * (tiles * (tiles + 1) / 2);
-  return 4 * (one > two ? one : two) * s <= 5 * all + 6000 * s;
+  return 4 * (one > two ? one : two) * s <= 5 * all + 4 * once * s;
 }
 
-// All tiles of a key head in a row, cut into `parts` equal parts (WHOLE: a tile each).  A wavefront's lanes hold
-// a share of the requests each.  IF: no parts unless the lengths call for this way of the two.
-template <int ROWS, bool WHOLE, bool IF>
+// All tiles of a key head in a row, cut into `parts` equal parts, or each tile a part: as the caller says, or as the
+// lengths are (whole_pays).  A wavefront's lanes hold a share of the requests each.
+enum How { kCut, kWhole, kEither };
+template <int ROWS, How HOW>
 struct Cuts {
   typedef Request<ROWS> Req;
   long all, upto;  // the row's length; the lane's requests end there
@@ -589,6 +596,7 @@ struct Cuts {
   long each;       // all / parts
   int over;        // all % parts
   int r0, r1, parts;
+  bool whole;
 
   __device__ __forceinline__ Cuts(const AttnArgs& a) {
     const int lane = threadIdx.x & 63;
@@ -600,7 +608,7 @@ struct Cuts {
     mine = 0;
 #pragma unroll 4
     for (int r = r0; r < r1; ++r) {
-      const Req q(a, r, WHOLE && !IF);
+      const Req q(a, r, HOW == kWhole);
       mine += q.all();
       const long last = q.tiles > 0 ? q.base + q.tiles * q.tau : 0;
       most = last > most ? last : most;
@@ -610,7 +618,7 @@ struct Cuts {
     const int lanes = (a.R + per - 1) / per;
     for (int d = 1; d < lanes; d <<= 1) {  // up to each lane
       const long up = __shfl_up(upto, d), other = __shfl_up(most, d);
-      const long tiles = IF ? __shfl_up(counted, d) : 0;
+      const long tiles = HOW == kEither ? __shfl_up(counted, d) : 0;
       if (lane >= d) {
         upto += up, counted += tiles;
         most = other > most ? other : most;
@@ -618,20 +626,20 @@ struct Cuts {
     }
     all = lane_of(upto, lanes - 1);
     most = lane_of(most, lanes - 1);
-    bool even = false;
-    if (IF) {
+    whole = HOW == kWhole;
+    if (HOW == kEither) {
       const long s = slots_of(a.HKV);
-      even = whole_pays(s, lane_of(counted, lanes - 1), most, all);
+      whole = whole_pays(s, lane_of(counted, lanes - 1), most, all, kOnce);
       if (a.R == 1) {
         const Req q(a, 0, false);
-        even = even || whole_pays_alone(s, q.tiles, q.base, q.tau);
+        whole = whole || whole_pays_alone(s, q.tiles, q.base, q.tau, kOnce);
       }
     }
-    if (IF && WHOLE) {
-      mine = count, upto = counted;
-      all = lane_of(upto, lanes - 1);
-    }
-    if (WHOLE) {
+    if (whole) {
+      if (HOW == kEither) {
+        mine = count, upto = counted;
+        all = lane_of(upto, lanes - 1);
+      }
       parts = (int)all;
       each = 1, over = 0;
     } else {
@@ -642,7 +650,6 @@ struct Cuts {
       each = divide(all, parts);
       over = (int)(all - each * parts);
     }
-    if (IF && even != WHOLE) parts = 0;
   }
   // where part w begins
   __device__ __forceinline__ long cut(int w) const { return each * w + over * w / parts; }
@@ -653,10 +660,10 @@ struct Cuts {
     long from = upto - mine;
     int hit = r0, i = 0;
     for (int x = r0; x < r1; ++x) {
-      const Req q(a, x, WHOLE);
+      const Req q(a, x, whole);
       const long len = q.all();
       if (at - from < len) {
-        if (WHOLE) {
+        if (whole) {
           i = (int)(at - from);
         } else if (q.tiles > 1) {
           // the largest i with before(i) <= at - from: the root of the parabola, put right by whole numbers
@@ -685,17 +692,17 @@ struct Cuts {
 // and goes on behind it, for the join.
 // What outlives a tile is held in scalar registers and no more than needed: the body needs all vector registers
 // that there are.
-template <int ROWS, bool WHOLE, bool IF, typename Body>
+template <int ROWS, How HOW, typename Body>
 __device__ __forceinline__ void each_tile(const AttnArgs& a, Body body) {
   const int h = blockIdx.x % a.HKV, w = blockIdx.x / a.HKV;
   auto noted = [&](const int4& note) {
-    if (!WHOLE && threadIdx.x == 0) a.NOTE[h * a.target + w] = note;
+    if (threadIdx.x == 0 && w < a.target) a.NOTE[h * a.target + w] = note;
   };
-  bool any;
+  bool any, whole;
   int r = 0, i = 0, parts, over;
   long begin = 0, first = 0, end = 0, each;
   {
-    const Cuts<ROWS, WHOLE, IF> cuts(a);
+    const Cuts<ROWS, HOW> cuts(a);
     any = w < cuts.parts && cuts.all > 0;
     if (any) {
       first = uniform(cuts.cut(w)), end = uniform(cuts.cut(w + 1));
@@ -703,11 +710,13 @@ __device__ __forceinline__ void each_tile(const AttnArgs& a, Body body) {
     }
     parts = __builtin_amdgcn_readfirstlane(cuts.parts), over = __builtin_amdgcn_readfirstlane(cuts.over);
     each = uniform(cuts.each);
+    whole = HOW == kEither ? __builtin_amdgcn_readfirstlane(cuts.whole) : HOW == kWhole;
   }
-  if (!any) return noted(int4{0, 0, 0, 0});
+  if (!any || whole) noted(int4{0, 0, 0, 0});
+  if (!any) return;
   for (;;) {
-    const Request<ROWS> q(a, r, WHOLE);
-    const long len = uniform(WHOLE ? 1 : q.before(i + 1) - q.before(i));
+    const Request<ROWS> q(a, r, whole);
+    const long len = uniform(whole ? 1 : q.before(i + 1) - q.before(i));
     const int tiles = __builtin_amdgcn_readfirstlane(q.tiles);
     Tile t;
     t.tok0 = __builtin_amdgcn_readfirstlane(q.c0);
@@ -715,12 +724,12 @@ __device__ __forceinline__ void each_tile(const AttnArgs& a, Body body) {
     t.kv = __builtin_amdgcn_readfirstlane(q.kv);
     t.pages = a.TABLE + (long)r * a.MB;
     t.rows = __builtin_amdgcn_readfirstlane(q.n) * a.g;
-    t.row0 = (WHOLE ? tiles - 1 - i : i) * ROWS;
+    t.row0 = (whole ? tiles - 1 - i : i) * ROWS;
     const int tile_end = t.row0 + ROWS < t.rows ? t.row0 + ROWS : t.rows;
     const int steps = (clampi(t.first + (tile_end - 1) / a.g + 1, 0, t.kv) + 63) >> 6;
     t.lo = 0, t.hi = __builtin_amdgcn_readfirstlane(steps), t.part = -1;
-    const bool last = WHOLE || begin + len >= end;
-    if (!WHOLE) {
+    const bool last = whole || begin + len >= end;
+    if (!whole) {
       if (begin < first) t.lo = (int)uniform(divide((first - begin) * steps, len));
       if (begin + len > end) t.hi = (int)uniform(divide((end - begin) * steps, len));
       // a tile of several parts: in the workgroup's second place where it begins there, in the first behind a cut
@@ -746,13 +755,13 @@ __device__ __forceinline__ void each_tile(const AttnArgs& a, Body body) {
 template <int D>
 __global__ __launch_bounds__(256, 2) void k_attn_small(AttnArgs a) {
   __shared__ __align__(16) float lds[128 + 4 * 16 * (D + 4)];
-  each_tile<kSmallRows, false, false>(a, [&](const Tile& t, int h) { small_tile<D>(a, t, h, lds); });
+  each_tile<kSmallRows, kCut>(a, [&](const Tile& t, int h) { small_tile<D>(a, t, h, lds); });
 }
 
-template <int D, bool WHOLE, bool IF>
-__global__ __launch_bounds__(512, 2) void k_attn_large(AttnArgs a) {
+template <int D, How HOW>
+__global__ __launch_bounds__(512, D == 64 ? 4 : 2) void k_attn_large(AttnArgs a) {
   extern __shared__ __align__(16) uint8_t dlds[];
-  each_tile<kLargeRows, WHOLE, IF>(a, [&](const Tile& t, int h) { large_tile<D>(a, t, h, dlds); });
+  each_tile<kLargeRows, HOW>(a, [&](const Tile& t, int h) { large_tile<D>(a, t, h, dlds); });
 }
 
 // The weighted sum of a row's parts 0 .. ns - 1 in their order, FLY of them in flight: part k at src + place(k) * D,
@@ -812,59 +821,50 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
 // Small tiles where there are at most as many tokens as requests: single tokens, in all likelihood.  (Of 2125 keys, 64
 // of them: 105 us, 122 in large tiles; 256 of 500: 104 and 138; 16 of 8000: 100 either way.)  A chunk among as many idle
 // requests is right there but slow (512 tokens behind 8000 among 511 idle ones: 477 us, 200 in large tiles).
-// Large tiles are left whole where that is quicker whatever the lengths are, as far as the table's pages say: one
-// request whose tiles pair up over the CUs with the longest and with no context (prompts of 1000, 2000, 4000, 8192: 33, 59,
-// 133, 520 us whole, 54, 95, 207, 645 cut), requests too short to be worth cutting, and many tiles none of which
-// can be longer than a CU's share.  They are cut where there are few rows (33 tokens over 32700 keys) or, of
-// several requests, less than a tile a CU (300 tokens of three in a long table: 31 us cut, 19 and 9 whole).  Else the
-// device finds out: both kernels run, and one of them, and perhaps the join, has nothing to do, which costs 9 us where
-// tiles stay whole and 3 where not (a prompt of 8192 beside a token with 100 thousand keys: 1970 us whole, 745 so).
+// Large tiles are left whole by the host, without a workspace and a join, where the table is too short for a cut to pay, or where it
+// holds no more than one request's tokens and a tile, if they fill the call's rows: a call of fewer tokens takes no longer
+// than that.  Else the device chooses, which costs whole tiles 6 to 8 us for the lengths and the join that has nothing to do
+// (a prompt of 300 in a table of 40960 keys 22 us, 16 in its own; 2000: 65 and 58; 8192: 501 and 493).
 AttnPlan attn_plan(int S, int R, int HQ, int HKV, int D, long keys) {
   AttnPlan p;
   p.small = S <= R;
   const int g = HQ / HKV;
   const long rows = (long)S * g, tiles = (rows + kLargeRows - 1) / kLargeRows;  // were all of the tokens one request's
   const long s = slots_of(HKV), tau = (kLargeRows + g - 1) / g;
-  bool whole = whole_pays(s, 0, keys, 0);  // too short to be worth cutting
-  if (R == 1)  // both conditions are linear in the context or the larger of two such: the ends say it all
-    whole = whole || (whole_pays_alone(s, tiles, 0, tau) && whole_pays_alone(s, tiles, keys > S ? keys - S : 0, tau));
-  else  // S tokens have S^2 / 2R keys at least, with no context and the same length each
-    whole = whole_pays(s, rows / kLargeRows, keys, (long)((double)S * rows / (2.0 * kLargeRows * R)));
-  p.split = p.small ? kCut : whole ? kWhole : tiles < (R == 1 ? 8 : s) ? kCut : kEither;
-  p.grid = p.split == kCut ? 0 : (int)(rows / kLargeRows + (R < S ? R : S));  // whole tiles of a key head, at most
-  p.target = p.split == kWhole ? 0 : ((p.small ? 2 : 1) * kCUs + HKV - 1) / HKV;  // workgroups that run at once
+  const bool whole = whole_pays(s, 0, keys, 0, kOnceAndLaunch) ||
+                     (R == 1 && keys - S <= kLargeRows && whole_pays_alone(s, tiles, 0, tau, kOnceAndLaunch) &&
+                      whole_pays_alone(s, tiles, keys > S ? keys - S : 0, tau, kOnceAndLaunch));
+  p.target = whole && !p.small ? 0 : ((p.small ? 2 : 1) * kCUs + HKV - 1) / HKV;  // workgroups that run at once
+  p.grid = p.small ? 0 : (int)(rows / kLargeRows + (R < S ? R : S));  // whole tiles of a key head, at most
+  if (p.grid < p.target) p.grid = p.target;
   const long kept = (long)HKV * p.target * 2 * (p.small ? kSmallRows : kLargeRows);
   p.ws_bytes = kept * (D + 2) * 4 + (long)HKV * p.target * (long)sizeof(int4);
   return p;
 }
 
 // At most S HQ / 256 + R HKV < 2^20 + 2^22 workgroups of 512 threads: under a launch's 2^32.
-template <int D, bool WHOLE, bool IF>
-static hipError_t launch_large(const AttnArgs& a, int grid, hipStream_t st) {
+template <int D, How HOW>
+static hipError_t launch_large(const AttnArgs& a, unsigned grid, hipStream_t st) {
   constexpr int bytes = kRing * 64 * D * 4;
-  const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k_attn_large<D, WHOLE, IF>),
-                                           hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  const hipError_t e =
+      hipFuncSetAttribute(reinterpret_cast<const void*>(k_attn_large<D, HOW>), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((k_attn_large<D, WHOLE, IF>), dim3((unsigned)grid * (unsigned)a.HKV), dim3(512), bytes, st, a);
+  hipLaunchKernelGGL((k_attn_large<D, HOW>), dim3(grid), dim3(512), bytes, st, a);
   return hipGetLastError();
 }
 
 template <int D>
 static hipError_t launch_d(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
-  const unsigned joins = (unsigned)(p.target * a.HKV);
+  const unsigned grid = (unsigned)p.grid * (unsigned)a.HKV, joins = (unsigned)(p.target * a.HKV);
   const long rows = (long)a.S * a.g;  // of a tile at most, too
   if (p.small) {
-    hipLaunchKernelGGL(k_attn_small<D>, dim3(joins), dim3(256), 0, st, a);
+    hipLaunchKernelGGL(k_attn_small<D>, dim3(grid), dim3(256), 0, st, a);
     const unsigned jy = (unsigned)(((rows < kSmallRows ? rows : kSmallRows) + 3) / 4);
     hipLaunchKernelGGL((k_attn_join<D, kSmallRows>), dim3(joins, jy), dim3(256), 0, st, a);
     return hipGetLastError();
   }
-  if (p.split != kCut) {
-    const hipError_t e = p.split == kWhole ? launch_large<D, true, false>(a, p.grid, st) : launch_large<D, true, true>(a, p.grid, st);
-    if (e != hipSuccess || p.split == kWhole) return e;
-  }
-  const hipError_t e = p.split == kCut ? launch_large<D, false, false>(a, p.target, st) : launch_large<D, false, true>(a, p.target, st);
-  if (e != hipSuccess) return e;
+  const hipError_t e = joins == 0 ? launch_large<D, kWhole>(a, grid, st) : launch_large<D, kEither>(a, grid, st);
+  if (e != hipSuccess || joins == 0) return e;
   const unsigned jy = (unsigned)(((rows < kLargeRows ? rows : kLargeRows) + 3) / 4);
   hipLaunchKernelGGL((k_attn_join<D, kLargeRows>), dim3(joins, jy), dim3(256), 0, st, a);
   return hipGetLastError();

@@ -133,12 +133,10 @@ struct AppendArgs {
 OSC_STEP hipError_t launch_qkv_append(const AppendArgs& a, hipStream_t st);
 
 // Attention over the paged cache (osc_attn_paged).
-enum AttnSplit { kCut, kWhole, kEither };  // tiles cut for even work, left whole, or as the device finds the lengths
 struct AttnPlan {
   bool small;       // 16-row tiles
-  AttnSplit split;
   int target;       // workgroups for each key head that cut tiles are dealt to (0: none is cut)
-  int grid;         // workgroups for each key head where tiles are whole
+  int grid;         // workgroups for each key head
   long ws_bytes;
 };
 OSC_STEP AttnPlan attn_plan(int S, int R, int HQ, int HKV, int D, long keys);  // keys: of a table's row
