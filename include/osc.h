@@ -385,8 +385,8 @@ osc_status osc_qkv_append(const void* QKV, int S, int HQ, int HKV, int D, const 
  * token i of the n = CU[r+1] - CU[r] new tokens of request r sees the keys j <= KV[r] - n + i
  * (its own included; KV counts the new ones, already appended), and
  *   O = sum_j softmax_j(scale q . k_j) v_j,   query head h on key head h / (HQ / HKV),
- * with scores, softmax and sums in binary32 and the weights rounded to bf16 for the second
- * product.  n = 1 is a decode step, KV = n a whole prompt, anything between a chunk; the
+ * with scores, softmax and sums in binary32.  The weights are rounded to bf16 for the second
+ * product where S > R, and to two bf16 (2^-16 of each) where S <= R.  n = 1 is a decode step, KV = n a whole prompt, anything between a chunk; the
  * requests of one call may differ.
  *   Q, O [S][HQ][D] bf16 (no operand overlaps O or WS: OSC_E_SHAPE); CU int32 [R + 1], 0 <= CU[r] <=
  *   CU[r + 1]; KV int32 [R] (negative counts as 0).
