@@ -53,3 +53,17 @@ def test_elements_of_another_type_are_refused():
                 refused(f, args, i, torch.zeros(a.numel() * 2, dtype=t, device=DEV))
             if a.dtype == torch.bfloat16:
                 f(*[x.view(torch.int16) if x is a else x for x in args])
+
+
+def test_block_refuses_an_output_inside_its_inputs():
+    from test_gpu_block_step import H, T, make_block, make_pages
+    b, pages = make_block(51, "osc"), make_pages()
+    both = torch.zeros((2 * T, H), dtype=torch.bfloat16, device=DEV)
+    x, res = both[:T], both[T:]
+    for y in (x, x.view(-1).view(T, H), both[1:T + 1], res, both[T - 1:2 * T - 1]):
+        with pytest.raises(ValueError):
+            b.forward(x, res, T, pages, None, None, y)
+    with pytest.raises(ValueError):
+        b.forward(x, None, T, pages, None, None, both[T - 1:2 * T - 1])
+    with pytest.raises(ValueError):
+        b.forward(x.data_ptr(), None, T, pages, None, None, x)

@@ -352,6 +352,12 @@ class Attention:
         self.out.forward(bufs["o"], S, bufs["ox"], Y, OSC_Y_BF16, stream)
 
 
+def _meet(a, b) -> bool:
+    """Do two contiguous tensors (of an address, its first byte) share bytes?"""
+    (at, an), (bt, bn) = ((t, 1) if isinstance(t, int) else (t.data_ptr(), t.nbytes) for t in (a, b))
+    return at < bt + bn and bt < at + an
+
+
 class Block:
     """One pre-norm transformer block on the residual stream: stream += x; attention(norm(stream));
     stream += that; MLP(norm(stream)), whose output is the next block's x."""
@@ -370,7 +376,7 @@ class Block:
         """X: [S, H] bf16, the block before's Y; res: the residual stream, updated in place.  The first
         block takes res = None: X is the stream then, and is updated in place.  Writes the MLP's
         output to Y (neither X nor res) and returns the stream."""
-        if Y is X or Y is res:
+        if any(t is not None and _meet(Y, t) for t in (X, res)):
             raise ValueError("Y is written while X and the residual stream are in use")
         self.attention.qkv.norm_quantize(X, res, self.w_attn, self.eps, S, bufs["attn"]["x"], stream)
         stream_rows = X if res is None else res
