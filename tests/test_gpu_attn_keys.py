@@ -87,6 +87,13 @@ def test_calls_with_room_for_more_rows(reqs, pad, HQ, HKV, D, page, room, idle):
     check_every_key(reqs, HQ, HKV, D, page, room, pad, idle)
 
 
+@pytest.mark.parametrize("reqs", [[(130, 2)] * 300, [(40, 1)] * 290 + [(700, 400)] * 2, [(500, 1), (0, 0)] * 150 + [(4000, 300)]])
+@pytest.mark.parametrize("HQ,HKV,D", [(8, 1, 64), (32, 8, 128)])
+@pytest.mark.parametrize("room", [0, 40000])
+def test_more_tiles_than_workgroups(reqs, HQ, HKV, D, room):
+    check_every_key(reqs, HQ, HKV, D, 64, room)
+
+
 @pytest.mark.parametrize("seed", range(24))
 def test_any_lengths(seed):
     rng = np.random.default_rng(seed)

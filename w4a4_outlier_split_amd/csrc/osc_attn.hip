@@ -295,9 +295,8 @@ __device__ __forceinline__ void small_tile(const AttnArgs& a, const Tile& t, int
 // V's alike; from slot `at`): the keys 8 part .. of K, the rows D/2 part .. of V^T.  off: the lane's place in the
 // first 1024 bytes.
 template <int D>
-__device__ __forceinline__ int k_place() {
+__device__ __forceinline__ int k_place(int lane) {
   constexpr int CH = D / 8;  // 16-byte pieces of a K row
-  const int lane = threadIdx.x & 63;
   return lane / CH * D * 2 + (((lane % CH) ^ (lane / CH)) << 4);
 }
 template <int D>
@@ -308,8 +307,7 @@ __device__ __forceinline__ void load_k(const AttnArgs& a, long block, int at, in
   for (int i = 0; i < D / 64; ++i)
     dma16s(r, off ^ (D == 128 ? part * 128 + i * 64 : 0), (at + 8 * part) * D * 2 + i * 1024, buf + i * 1024);
 }
-__device__ __forceinline__ int v_place(int sh) {  // row d = lane / 2, its halves in turn
-  const int lane = threadIdx.x & 63;
+__device__ __forceinline__ int v_place(int lane, int sh) {  // row d = lane / 2, its halves in turn
   return ((lane >> 1) << (sh + 1)) + (((lane & 1) ^ ((lane >> 4) & 1)) << 4);
 }
 template <int D>
@@ -329,8 +327,10 @@ __device__ __forceinline__ void load_v(const AttnArgs& a, long block, int at, in
 template <int D>
 __device__ __forceinline__ void large_tile(const AttnArgs& a, const Tile& t, int h, uint8_t* lds) {
   constexpr int DK = D / 16, DB = D / 32, CH = D / 8, HALF = 64 * D * 2, TILE = 2 * HALF;
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  int tid = threadIdx.x;
+  asm volatile("" : "+v"(tid));  // worked out again for each tile: nothing of the lane's places is kept from one to the next
+  const int lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = lane & 31, half = lane >> 5;
   const int g = a.g;
   const int row0 = t.row0 + wave * 32, row = row0 + col;
@@ -364,7 +364,7 @@ __device__ __forceinline__ void large_tile(const AttnArgs& a, const Tile& t, int
     };
     // A wavefront loads half a run: 8 keys of K, half the rows of V^T.
     const int run = wave >> 1, part = wave & 1;
-    const int koff = k_place<D>(), voff = v_place(a.sh);
+    const int koff = k_place<D>(lane), voff = v_place(lane, a.sh);
     lds_u8* const lk = (lds_u8*)lds + (run * 16 + part * 8) * D * 2;
     lds_u8* const lv = (lds_u8*)lds + HALF + run * D * 32 + part * D * 16;
     auto load = [&](int n) {
@@ -403,7 +403,7 @@ __device__ __forceinline__ void large_tile(const AttnArgs& a, const Tile& t, int
       bads = (int)((unsigned)bads >> 8);
       if (rare(bad != 0)) {  // V of keys that do not exist may hold anything, and 0 * NaN is not 0
         uint16_t* v = reinterpret_cast<uint16_t*>(lds + slot + HALF);
-        int first = threadIdx.x;
+        int first = tid;
         asm volatile("" : "+v"(first));  // rarely run: nothing of it is kept in registers over the loop
         for (int i = first; i < 64 * D; i += 512) {
           const int u = i / (16 * D), d = (i / 16) % D, e = i & 15;
@@ -604,7 +604,8 @@ struct Cuts {
   bool whole;
 
   __device__ __forceinline__ Cuts(const AttnArgs& a) {
-    const int lane = threadIdx.x & 63;
+    int lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));  // as in large_tile
     const int per = (a.R + 63) >> 6;
     r0 = lane * per < a.R ? lane * per : a.R;
     r1 = r0 + per < a.R ? r0 + per : a.R;
@@ -640,24 +641,26 @@ struct Cuts {
         whole = whole || whole_pays_alone(s, q.tiles, q.base, q.tau, kOnce);
       }
     }
-    if (whole) {
+    if (whole) {  // a workgroup takes several only where there are more tiles than workgroups
       if (HOW == kEither) {
         mine = count, upto = counted;
         all = lane_of(upto, lanes - 1);
       }
-      parts = (int)all;
-      each = 1, over = 0;
+      const long p = HOW == kEither ? gridDim.x / a.HKV : all;
+      parts = (int)(p < all ? p : all > 0 ? all : 1);
     } else {
       long p = a.target;
       if (p > all / kMinKeys) p = all / kMinKeys;
       if (most > 0 && p > kMaxCuts && p > kMaxCuts * divide(all, most)) p = kMaxCuts * divide(all, most);
       parts = p < 1 ? 1 : (int)p;
-      each = divide(all, parts);
-      over = (int)(all - each * parts);
     }
+    each = HOW == kWhole ? 1 : divide(all, parts);
+    over = HOW == kWhole ? 0 : (int)(all - each * parts);
   }
   // where part w begins
-  __device__ __forceinline__ long cut(int w) const { return each * w + over * w / parts; }
+  __device__ __forceinline__ long cut(int w) const {
+    return each * w + (HOW == kCut ? over * w / parts : divide((long)over * w, parts));
+  }
 
   // The tile at `at` of the row (0 <= at < all): its request, its number there, and where it begins.
   __device__ __forceinline__ void find(const AttnArgs& a, long at, int& r, int& tile, long& begin) const {
@@ -692,8 +695,8 @@ struct Cuts {
 
 // Workgroup: key head h = blockIdx % HKV (an XCD takes every eighth workgroup, so with eight key heads each XCD's
 // L2 holds one head's cache), part w = blockIdx / HKV of the head's row; body(t, h) for each tile of the part in
-// turn.  Whole tiles take a request's later tiles first, which see the most keys, and all from their first key, so that
-// the tiles that run together stream the same keys.  Otherwise the workgroup notes a tile that begins in its part
+// turn.  Whole tiles, one for a part or a few neighbours, take a request's later tiles first, which see the most keys, and all
+// from their first key, so that the tiles that run together stream the same keys.  Otherwise the workgroup notes a tile that begins in its part
 // and goes on behind it, for the join.
 // What outlives a tile is held in scalar registers and no more than needed: the body needs all vector registers
 // that there are.
@@ -733,7 +736,7 @@ __device__ __forceinline__ void each_tile(const AttnArgs& a, Body body) {
     const int tile_end = t.row0 + ROWS < t.rows ? t.row0 + ROWS : t.rows;
     const int steps = (clampi(t.first + (tile_end - 1) / a.g + 1, 0, t.kv) + 63) >> 6;
     t.lo = 0, t.hi = __builtin_amdgcn_readfirstlane(steps), t.part = -1;
-    const bool last = whole || begin + len >= end;
+    const bool last = HOW == kWhole || begin + len >= end;
     if (!whole) {
       if (begin < first) t.lo = (int)uniform(divide((first - begin) * steps, len));
       if (begin + len > end) t.hi = (int)uniform(divide((end - begin) * steps, len));
@@ -747,10 +750,11 @@ __device__ __forceinline__ void each_tile(const AttnArgs& a, Body body) {
           ns = 1 + __popcll(__ballot(p < parts && each * p + over * p / parts < begin + len));
         }
         noted(int4{ns, t.row0, t.rows, t.tok0});
-      } else {
-        begin += len;
-        if (++i == tiles) i = 0, r = next_request(a, r);
       }
+    }
+    if (!last) {
+      begin += len;
+      if (++i == tiles) i = 0, r = next_request(a, r);
     }
     body(t, h);
     if (last) return;
@@ -763,6 +767,8 @@ __global__ __launch_bounds__(256, 2) void k_attn_small(AttnArgs a) {
   each_tile<kSmallRows, kCut>(a, [&](const Tile& t, int h) { small_tile<D>(a, t, h, lds); });
 }
 
+// Heads of 64 need half the LDS and may have two workgroups a CU, if 128 registers do.  (8192 tokens in a table of 40960 keys:
+// 315 us, 350 with the 140 registers that the cuts would take; 33 tokens over 32700 keys 39 and 38.)
 template <int D, How HOW>
 __global__ __launch_bounds__(512, D == 64 ? 4 : 2) void k_attn_large(AttnArgs a) {
   extern __shared__ __align__(16) uint8_t dlds[];
@@ -841,6 +847,10 @@ AttnPlan attn_plan(int S, int R, int HQ, int HKV, int D, long keys) {
                       whole_pays_alone(s, tiles, keys > S ? keys - S : 0, tau, kOnceAndLaunch));
   p.target = whole && !p.small ? 0 : ((p.small ? 2 : 1) * kCUs + HKV - 1) / HKV;  // workgroups that run at once
   p.grid = p.small ? 0 : (int)(rows / kLargeRows + (R < S ? R : S));  // whole tiles of a key head, at most
+  // Where requests may have no token or few, several tiles for a workgroup are cheaper than workgroups without any, each of
+  // which looks for its part through all requests.  (512 tokens behind 8000 keys among 511 idle requests, 513 rows: 114 us, 190 with a
+  // workgroup for every tile that there could be; 512 requests of 2 tokens: 214, 325.)
+  if (p.target > 0 && p.grid > 2 * rows / kLargeRows + p.target) p.grid = (int)(2 * rows / kLargeRows) + p.target;
   if (p.grid < p.target) p.grid = p.target;
   const long kept = (long)HKV * p.target * 2 * (p.small ? kSmallRows : kLargeRows);
   p.ws_bytes = kept * (D + 2) * 4 + (long)HKV * p.target * (long)sizeof(int4);
