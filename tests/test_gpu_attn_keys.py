@@ -94,6 +94,12 @@ def test_more_tiles_than_workgroups(reqs, HQ, HKV, D, room):
     check_every_key(reqs, HQ, HKV, D, 64, room)
 
 
+@pytest.mark.parametrize("HQ,HKV", [(40, 40), (600, 300), (1024, 1), (1024, 1024)])
+@pytest.mark.parametrize("reqs,room", [([(900, 1), (33, 1)], 0), ([(900, 3), (70, 70)], 0), ([(900, 3), (70, 70)], 9000), ([(1100, 9)], 9000)])
+def test_many_heads(HQ, HKV, reqs, room):
+    check_every_key(reqs, HQ, HKV, 64, 16, room)
+
+
 @pytest.mark.parametrize("seed", range(24))
 def test_any_lengths(seed):
     rng = np.random.default_rng(seed)

@@ -129,3 +129,28 @@ def test_positions_behind_the_rotary_table(captured):
             with pytest.raises(RuntimeError, match=f"{lost} tokens"):
                 pages.check()
         pages.check()
+
+
+@pytest.mark.parametrize("requests,pool,rows", [(4096, 9000, 5000), (513, 700, 20000), (1, 40, 8192)])
+def test_many_requests_replayed(requests, pool, rows):
+    """Plan and advance in one graph, replayed with eager work in between, against the same steps on the host."""
+    from test_pages_host import HostPages
+    args = (requests, pool, 16, 40, rows)
+    pages, host = blk.Pages(torch, *args, DEV), HostPages(torch, *args, "cpu")
+    pages.plan(), pages.advance()  # what the first call of a library loads
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+        pages.plan()
+        pages.advance()
+    g = torch.Generator().manual_seed(requests)
+    for it in range(6):
+        new = torch.randint(-1, 3 if requests > 1 else 300, (requests,), generator=g, dtype=torch.int32)
+        pages.new.copy_(new), host.new.copy_(new)
+        torch.cuda.synchronize()
+        graph.replay()
+        host.plan(), host.advance()
+        for name in ("ctx", "head", "lost", "slot", "pos", "cu", "kv"):
+            assert torch.equal(getattr(pages, name).cpu(), getattr(host, name)), (it, name)
+        held = -(-host.ctx // 16)
+        own = torch.arange(40)[None] < held[:, None]
+        assert torch.equal(pages.table.cpu()[own], host.table[own])
