@@ -372,7 +372,8 @@ osc_status osc_page_plan(const int32_t* CTX, const int32_t* NEW, int R, int page
  * A token whose slot is outside [0, NP * page), or whose position is outside [0, P), writes
  * nothing: its row of Q stays as it was.  One that is passed over for its position has a slot all the same, and
  * osc_page_plan's KV counts it: that row of the attention, and those of the request's later tokens, mean nothing.
- * No operand overlaps an output (OSC_E_SHAPE).  Slots must be distinct: of two tokens with one slot the cache holds channels of either.
+ * The sum of squares of a normed head must stay below 2^128.  No operand overlaps an output (OSC_E_SHAPE).  Slots must
+ * be distinct: of two tokens with one slot the cache holds channels of either.
  * Constraints: S >= 0, S < 2^24, 1 <= HQ, HKV <= 1024, D in {64, 128}, S (HQ + 2 HKV) D <
  * 2^34, NP >= 1, NP * page < 2^31, eps positive and finite with WQ, P >= 1 with CS.
  */
@@ -386,8 +387,8 @@ osc_status osc_qkv_append(const void* QKV, int S, int HQ, int HKV, int D, const 
  * (its own included; KV counts the new ones, already appended), and
  *   O = sum_j softmax_j(scale q . k_j) v_j,   query head h on key head h / (HQ / HKV),
  * with scores, softmax and sums in binary32.  The weights are rounded to bf16 for the second
- * product where S > R, and to two bf16 (2^-16 of each) where S <= R.  n = 1 is a decode step, KV = n a whole prompt, anything between a chunk; the
- * requests of one call may differ.
+ * product where S > R, and to two bf16 (2^-16 of each) where S <= R.  n = 1 is a decode step,
+ * KV = n a whole prompt, anything between a chunk; the requests of one call may differ.
  *   Q, O [S][HQ][D] bf16 (no operand overlaps O or WS: OSC_E_SHAPE); CU int32 [R + 1], 0 <= CU[r] <=
  *   CU[r + 1]; KV int32 [R] (negative counts as 0).
  * A token that sees no key (KV < n, or no page of its keys exists) gets zeros; keys whose

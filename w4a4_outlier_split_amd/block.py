@@ -233,8 +233,9 @@ class Pages:
     lost: nothing of them is written, their rows of the step's output mean nothing, ``ctx`` does not count
     them, and ``lost`` (int32 [1], device) does.  They are a request's last ones, so ``ctx`` tells what is
     left to be given again.  A request that passes the end of the blocks' rotary table cannot go on: ``ctx``
-    does count those tokens, with their pages, and so does ``lost``.  ``rows`` is how many rows the blocks ran
-    with since the plan (T until then), ``positions`` how many their rotary table has.  Table entries behind a request's ceil(ctx / page) first mean nothing."""
+    does count those tokens, with their pages, and so does ``lost``.  ``rows`` is how many rows the blocks
+    ran with since the plan (T until then), ``positions`` how many their rotary table has.  Table entries
+    behind a request's ceil(ctx / page) first mean nothing."""
 
     def __init__(self, torch, R: int, NP: int, page: int, MB: int, T: int, device):
         self.torch, self.R, self.NP, self.page, self.MB, self.T, self.rows = torch, R, NP, page, MB, T, T

@@ -7,7 +7,7 @@
 // exp(s - m), a tile of keys adds P = exp(S - m) to l and P V to the unnormalised output, and where
 // m grows both are scaled by exp(m_old - m_new).  Scores, m, l and the output are binary32.  The matrix instruction
 // takes no operand wider than bf16 beside bf16 values.  The small kernel, whose products wait for memory, takes a weight as two
-// bf16, itself and what its rounding leaves out (2^-16 of it is lost; 64 decodes take the same 189 us, one 0.2 us more).  The
+// bf16, itself and what its rounding leaves out (2^-16 of it is lost; 64 decodes take 191 us as before, one 0.2 us more).  The
 // large one, bound by its products, takes it rounded (each weight off by at most 2^-8 of itself, in either direction), and
 // sums it into l as rounded, two weights a dot product.
 //
@@ -21,14 +21,14 @@
 // Two kernels, by the call's tokens and requests:
 //   small (single tokens): tiles of 16 rows, the cache read from memory straight into registers, every byte once;
 //     the four wavefronts take 32 keys each in turn and are merged at the end.  HBM-bound: 64 decodes over 136
-//     thousand keys (1.07 GB of cache) take 189 us, 5.7 TB/s.  A single decode over 4000 keys takes 9 us and 4 for the
+//     thousand keys (1.07 GB of cache) take 191 us, 5.6 TB/s.  A single decode over 4000 keys takes 10 us and 4 for the
 //     join, bound by the chain of page table, keys, scores and two launches (its 16 MB are worth 3.5 us).
 //   large: tiles of 256 rows, eight wavefronts of 32 rows each, one workgroup a CU; 64 keys of K and V^T at a
 //     time in a ring in LDS, loaded by LDS-DMA three tiles ahead, so that a key is fetched once for 256 rows.  Bound
 //     by what the matrix unit and the rest draw together: the card lowers its clock under this load, so
-//     what counts is work per product.  A prompt of 8192 (32 query and 8 key heads of 128): 495 to 535 us with the
+//     what counts is work per product.  A prompt of 8192 (32 query and 8 key heads of 128): 493 to 535 us with the
 //     clock of the card, 1.03 to 1.11 PFLOP/s of the 1.35 to 1.55 that large matrix products reach; without loads,
-//     barriers and exponentials it would be 458 us.  33 tokens over 32700 keys take 43 us and 9 for the join: a
+//     barriers and exponentials it would be 458 us.  33 tokens over 32700 keys take 45 us and 10 for the join: a
 //     tile of 132 rows on eight wavefronts, whose rate the chain through a step's two products sets.
 // The work is cut evenly, whatever the lengths: all tiles of a key head stand in a row, each as long as the keys
 // that it sees, and the row is cut into as many equal parts as workgroups run at once.  A workgroup takes
@@ -137,7 +137,7 @@ __device__ __forceinline__ float sum_wave(float v) {
 // Rows are the query heads of a token (and the next tokens'), so a decode with 4 heads to a key head uses 4 of 16:
 // the products are idle anyway where every key is read once.  No LDS on the way: a key's row and a channel's run of
 // keys are 16-byte pieces in the very lanes that the products want, and four wavefronts with a step each in flight
-// and 512 workgroups cover the latency.  (64 decodes: 284 us with pages looked up in the step, 189 so, 5.7 TB/s.)
+// and 512 workgroups cover the latency.  (64 decodes: 284 us with pages looked up in the step, 191 so, 5.6 TB/s.)
 template <int D>
 __device__ __forceinline__ void small_tile(const AttnArgs& a, const Tile& t, int h, float* lds) {
   constexpr int DK = D / 32, DB = D / 16;
@@ -799,7 +799,7 @@ __device__ __forceinline__ vE weigh(const float* src, Place place, int ns, float
 // m_k, in the order of the parts.  A row a wavefront: lane k holds the maximum and sum of part w + k, and the lanes
 // D / 64 values of the row each.  HBM-bound where the parts are many (58 MB in 20 us, launch and all); a few rows
 // (4 us) are bound by the launch and two loads one after the other, so the values' loads all start at once.
-// (A workgroup a tile took 9 us for one decode and 24 for 33 tokens over 32700 keys, whose 132 rows have 31 parts each: 9 now.)
+// (A workgroup a tile took 9 us for one decode and 24 for 33 tokens over 32700 keys, whose 132 rows have 31 parts each: 4 and 10 now.)
 template <int D, int ROWS>
 __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
   constexpr int E = D / 64;
@@ -831,7 +831,7 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
 
 // Small tiles where there are at most as many tokens as requests: single tokens, in all likelihood.  (Of 2125 keys, 64
 // of them: 105 us, 122 in large tiles; 256 of 500: 104 and 138; 16 of 8000: 100 either way.)  A chunk among as many idle
-// requests is right there but slow (512 tokens behind 8000 among 511 idle ones: 477 us, 200 in large tiles).
+// requests is right there but slow (512 tokens behind 8000 among 511 idle ones: 440 us, 114 in large tiles).
 // Large tiles are left whole by the host, without a workspace and a join, where the table is too short for a cut to pay, or where it
 // holds no more than one request's tokens and a tile, if they fill the call's rows: a call of fewer tokens takes no longer
 // than that.  Else the device chooses, which costs whole tiles 6 to 8 us for the lengths and the join that has nothing to do

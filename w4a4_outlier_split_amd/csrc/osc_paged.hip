@@ -113,7 +113,7 @@ __global__ __launch_bounds__(256) void k_page_plan(PlanArgs a) {
 // Per head of a token: q and k are normed over the head (binary32 sum of D squares, if asked),
 // rotated (the halves x1, x2 of the head by the position's angles: x1 cos - x2 sin, x2 cos + x1 sin)
 // and rounded once; v is copied.  HBM-bound: every element is read and written once (4097 tokens of 32 + 8 + 8 heads
-// of 128, 103 MB: 19 us, 5.4 TB/s, part of it from the caches; 16 tokens 3 us, the latency of slot, row and store).
+// of 128, 103 MB: 22.5 us, 4.6 TB/s, as a copy; 16 tokens 3 us, the latency of slot, row and store).
 // One launch for both parts, so that small steps pay one; neither part waits for the other:
 //   blocks of the first part: 256 threads take 2048 / D heads of q and k, D/16 lanes a head, each
 //     with 8 channels of both halves, so the rotation stays in a lane and the norm crosses D/16.
