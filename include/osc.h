@@ -107,6 +107,9 @@ typedef OSC_ENUM(osc_ytype_e) {
 #define OSC_MAX_GROUPS 1024
 #define OSC_MAX_CHANNELS 3 /* protected channels per group in the *_multi calls */
 #define OSC_MAX_REQUESTS 4096 /* requests of one step in the paged-cache calls */
+#define OSC_MAX_TREE 256      /* nodes of a request's tree of drafted tokens */
+#define OSC_MAX_TOP 64        /* alternatives of osc_logprobs */
+#define OSC_MAX_LAYERS 128    /* layers of one osc_tree_commit */
 
 /*
  * osc_pack_weights -- offline weight preparation (§3.2 weight side, §3.3).
@@ -412,6 +415,96 @@ osc_status osc_attn_workspace(int S, int R, int HQ, int HKV, int D, int page, in
 osc_status osc_attn_paged(const void* Q, const void* KC, const void* VC, int S, int R, int HQ, int HKV, int D, int page,
                           int MB, int NP, const int32_t* TABLE, const int32_t* CU, const int32_t* KV, float scale,
                           void* O, void* WS, int64_t ws_bytes, void* stream);
+
+/*
+ * ---- Steps with drafted tokens.
+ * The new tokens of a request may be a tree of up to N drafted ones instead of a run: node i of the n = CU[r+1] - CU[r]
+ * tokens of request r has the parent PARENT[CU[r] + i] in [0, i), a node of the same request, or none (any other
+ * value; -1 by custom): it follows the request's context then.  A node's ancestors are its parent's and the node itself.
+ * A step is osc_page_plan (a node a new token, in slots one behind the other), osc_tree_plan, for each layer
+ * osc_qkv_append and osc_attn_tree, and behind the last one osc_logprobs (or whatever else chooses a token for each
+ * node), osc_tree_accept and osc_tree_commit.  N is the most nodes that a tree may have, 1 to OSC_MAX_TREE, and the same in
+ * all calls of a step; W = ceil(N / 64).  Nodes behind a request's N first take part in nothing: position -1, seen by none, never accepted.
+ *
+ * osc_tree_plan -- positions and masks of the trees' nodes.
+ *   PARENT int32 [T], CU int32 [R + 1] (0 <= CU[r] <= CU[r + 1]), CTX int32 [R]: tokens of request r in the cache (negative counts as 0).
+ *   POS int32 [T], written: CTX + the number of the node's ancestors less itself (at most 2^31 - 1).
+ *   MASK uint64 [T][W], written: bit j % 64 of word j / 64 is set for the node's ancestors j and itself.
+ *   Rows outside [CU[0], CU[R]) and nodes behind the N first get -1 and 0.
+ * Constraints: 0 <= R <= OSC_MAX_REQUESTS, T >= 0, T * W < 2^31, 1 <= N <= OSC_MAX_TREE.  CU is required even when R is 0; MASK
+ * is 8-byte aligned.  No operand overlaps an output (OSC_E_SHAPE).
+ */
+osc_status osc_tree_plan(const int32_t* PARENT, const int32_t* CU, const int32_t* CTX, int R, int T, int N, int32_t* POS,
+                         uint64_t* MASK, void* stream);
+
+/*
+ * osc_attn_tree -- osc_attn_paged with a mask of each token's own among the new ones: token i of the n new tokens of request r
+ * sees the keys j < KV[r] - n, its context, and of the new keys KV[r] - n + b those with bit b of MASK[CU[r] + i] set,
+ *   O = sum_j softmax_j(scale q . k_j) v_j,
+ * with scores, softmax and sums in binary32.  The weights are rounded to bf16 for the second product where N * HQ / HKV > 64, and to
+ * two bf16 (2^-16 of each) otherwise.
+ *   MASK uint64 [S][W], 8-byte aligned, as osc_tree_plan writes it, or any other: bits of tokens that the request does not have, and of keys
+ *   that do not exist, count for nothing.  Everything else is as osc_attn_paged has it.
+ * A token that sees no key gets zeros.  Context that holds a NaN may reach every row of its request.  A new token whose
+ * key or value is not finite reaches those rows alone that see it, all channels of which become NaN (a key that is infinite: or
+ * as its score has it).
+ *   WS, ws_bytes: device workspace of at least osc_attn_tree_workspace's bytes for the same sizes, free again when the call's work is
+ *   done: calls that can overlap, two graphs replayed on two streams included, need one each.
+ * The result does not depend on what else runs.  N goes into the choice of the kernel, not into the result's meaning: a request of more tokens
+ * than N is right, but its rows see new keys below 64 W only.
+ * Constraints: as osc_attn_paged, and 1 <= N <= OSC_MAX_TREE.
+ */
+osc_status osc_attn_tree_workspace(int S, int R, int HQ, int HKV, int D, int page, int MB, int N, int64_t* bytes);
+osc_status osc_attn_tree(const void* Q, const void* KC, const void* VC, int S, int R, int HQ, int HKV, int D, int page, int MB,
+                         int NP, const int32_t* TABLE, const int32_t* CU, const int32_t* KV, const uint64_t* MASK, int N,
+                         float scale, void* O, void* WS, int64_t ws_bytes, void* stream);
+
+/*
+ * osc_logprobs -- log probabilities from rows of logits, p = softmax(scale x) over a row's V values:
+ *   X    [S][ld] bf16 or fp32 (xt, as osc_gemm wrote them), device, read only; columns V .. ld - 1 are not looked at, and
+ *        behind the last row's V values nothing need exist.
+ *   ID   int32 [S][M], LP fp32 [S][M], written: log p of the given tokens; -inf for an id outside [0, V).
+ *   ENT  fp32 [S] or NULL, written: - sum p log p.
+ *   TOPV fp32 [S][K], TOPI int32 [S][K], written: the K most likely tokens' log p and ids, the most likely first, of
+ *        equal logits the lower id.  Tokens of logit -inf (masked out) are no alternatives: where fewer than K are left, -inf and -1.
+ * in binary32; logits of -inf are tokens of probability 0.  A row that has no distribution, with a NaN or +inf or -inf alone, gets
+ * NaN in LP (ids outside [0, V) too), ENT and TOPV, and ids -1.
+ *   WS, ws_bytes: device workspace of at least osc_logprobs_workspace's bytes for the same sizes (WS may be NULL when that is 0; fewer rows may
+ *   need more), free again when the call's work is done: calls that can overlap need one each.
+ * M = 0: no given tokens, K = 0: no alternatives; their pointers are not looked at.
+ * Constraints: 0 <= S < 2^24, 1 <= V < 2^24, ld >= V, S * ld < 2^34, 0 <= M <= 65536, S * M < 2^31, 0 <= K <= OSC_MAX_TOP, scale
+ * positive, scale and scale * log2 e finite; scale * x must stay below 2^120 in size.  Arrays of int32 and fp32 other than X need
+ * 4-byte alignment only.  No operand overlaps an output or WS (OSC_E_SHAPE).
+ */
+osc_status osc_logprobs_workspace(int S, int V, int K, int64_t* bytes);
+osc_status osc_logprobs(const void* X, osc_ytype xt, int S, int V, int ld, float scale, const int32_t* ID, int M, int K,
+                        float* LP, float* ENT, float* TOPV, int32_t* TOPI, void* WS, int64_t ws_bytes, void* stream);
+
+/*
+ * osc_tree_accept -- the path of each tree that agrees with the chosen tokens.
+ *   TOKEN, PARENT int32 [T], CU int32 [R + 1]: the trees; a tree's node 0 is the last token that is certain, without which nothing follows.
+ *   CHOICE int32, ldc >= 1: the token chosen behind node t is CHOICE[t * ldc] (TOPI of osc_logprobs with ldc = K; negative: none).
+ *   SLOT int32 [T]: the nodes' cache slots; a negative one has not been written.  With P > 0, neither has one whose POS (int32
+ *   [T]) is outside [0, P), the rotary table's end; P = 0: POS is not looked at.  Such nodes are not accepted.
+ * From node 0, if it is written, the path goes on to the first child whose token is the one chosen, and ends where there is none.
+ *   ACC int32 [R], written: nodes on the path (0 without a written node 0).  PATH int32 [R][N]: them, in order; -1 behind.
+ *   NEXT int32 [R]: the token chosen behind the path's last node; -1 where ACC is 0.
+ * Constraints: 0 <= R <= OSC_MAX_REQUESTS, T >= 0, T * ldc < 2^34, P >= 0, 1 <= N <= OSC_MAX_TREE.  With T = 0 the arrays of T are not looked
+ * at.  No operand overlaps an output (OSC_E_SHAPE).
+ *
+ * osc_tree_commit -- the path's keys and values become the request's next tokens: in each layer, those of node PATH[r][k] go to the slot
+ * of node k, for k in [1, ACC[r]).  A node that stands in its place stays.
+ *   KC, VC  HOST arrays of `layers` device pointers to the layers' caches (layout above), read during the call; written.
+ *   SLOT, CU, ACC, PATH  as osc_tree_accept has them.
+ * Entries of ACC behind the tree's nodes or N, of PATH below their own number or behind the tree's nodes, and slots outside [0, NP * page) move nothing.
+ * Slots must be distinct.  No two caches share bytes, nor does one with another operand (OSC_E_SHAPE).
+ * Constraints: 0 <= layers <= OSC_MAX_LAYERS, 1 <= HKV <= 1024, D in {64, 128}, NP >= 1, NP * page < 2^31, and as osc_tree_accept.
+ */
+osc_status osc_tree_accept(const int32_t* TOKEN, const int32_t* PARENT, const int32_t* CHOICE, int ldc, const int32_t* SLOT,
+                           const int32_t* POS, int P, const int32_t* CU, int R, int T, int N, int32_t* ACC, int32_t* PATH,
+                           int32_t* NEXT, void* stream);
+osc_status osc_tree_commit(void* const* KC, void* const* VC, int layers, int NP, int HKV, int D, int page, const int32_t* SLOT,
+                           const int32_t* CU, const int32_t* ACC, const int32_t* PATH, int R, int T, int N, void* stream);
 
 /* Human-readable name of a status code (static storage). */
 const char* osc_status_str(osc_status s);

@@ -33,6 +33,9 @@ OSC_Y_F32 = 1
 OSC_MAX_GROUPS = 1024
 OSC_MAX_CHANNELS = 3
 OSC_MAX_REQUESTS = 4096
+OSC_MAX_TREE = 256    # nodes of a request's tree of drafted tokens
+OSC_MAX_TOP = 64      # alternatives of osc_logprobs
+OSC_MAX_LAYERS = 128  # layers of one osc_tree_commit
 
 STATUS = {0: "OSC_OK", 1: "OSC_E_NULL", 2: "OSC_E_SHAPE", 3: "OSC_E_TABLE", 4: "OSC_E_ALIGN",
           5: "OSC_E_FORMAT", 6: "OSC_E_DEVICE"}
@@ -40,8 +43,9 @@ STATUS = {0: "OSC_OK", 1: "OSC_E_NULL", 2: "OSC_E_SHAPE", 3: "OSC_E_TABLE", 4: "
 EXPORTS = ("osc_pack_weights", "osc_quant_act", "osc_gemm", "osc_gemm_fp8", "osc_build_table",
            "osc_pack_weights_multi", "osc_quant_act_multi", "osc_gemm_multi", "osc_build_table_multi",
            "osc_swiglu_quant", "osc_swiglu", "osc_linear_decode", "osc_gemm_fp6p", "osc_rmsnorm_quant",
-           "osc_rmsnorm", "osc_page_plan", "osc_qkv_append", "osc_attn_workspace", "osc_attn_paged", "osc_status_str",
-           "osc_last_device_error")
+           "osc_rmsnorm", "osc_page_plan", "osc_qkv_append", "osc_attn_workspace", "osc_attn_paged", "osc_tree_plan",
+           "osc_attn_tree_workspace", "osc_attn_tree", "osc_logprobs_workspace", "osc_logprobs", "osc_tree_accept",
+           "osc_tree_commit", "osc_status_str", "osc_last_device_error")
 
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"libosc.so is not built ({LIB_PATH}); run python w4a4_outlier_split_amd/build.py")
@@ -71,6 +75,13 @@ _lib.osc_page_plan.argtypes = [_P, _P, _I, _I, _I, _P, _I, _P, _I, _P, _I, _P, _
 _lib.osc_qkv_append.argtypes = [_P, _I, _I, _I, _I, _P, _P, _F, _P, _I, _P, _P, _P, _P, _P, _I, _I, _P]
 _lib.osc_attn_workspace.argtypes = [_I, _I, _I, _I, _I, _I, _I, _P]
 _lib.osc_attn_paged.argtypes = [_P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _P, _P, _P, _F, _P, _P, _L, _P]
+_lib.osc_tree_plan.argtypes = [_P, _P, _P, _I, _I, _I, _P, _P, _P]
+_lib.osc_attn_tree_workspace.argtypes = [_I, _I, _I, _I, _I, _I, _I, _I, _P]
+_lib.osc_attn_tree.argtypes = [_P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _P, _P, _P, _P, _I, _F, _P, _P, _L, _P]
+_lib.osc_logprobs_workspace.argtypes = [_I, _I, _I, _P]
+_lib.osc_logprobs.argtypes = [_P, _I, _I, _I, _I, _F, _P, _I, _I, _P, _P, _P, _P, _P, _L, _P]
+_lib.osc_tree_accept.argtypes = [_P, _P, _P, _I, _P, _P, _I, _P, _I, _I, _I, _P, _P, _P, _P]
+_lib.osc_tree_commit.argtypes = [_P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _I, _I, _I, _P]
 for _f in EXPORTS[:-2]:
     getattr(_lib, _f).restype = _I
 _lib.osc_status_str.argtypes = [_I]
@@ -312,3 +323,100 @@ def osc_attn_paged(Q, KC, VC, S: int, R: int, HQ: int, HKV: int, D: int, page: i
     _check(_lib.osc_attn_paged(_at(c, d, Q, q, _BF16), _at(c, d, KC, n, _BF16), _at(c, d, VC, n, _BF16), S, R, HQ, HKV, D, page,
                                MB, NP, _at(c, d, TABLE, 4 * R * MB, _I32), _at(c, d, CU, 4 * R + 4, _I32), _at(c, d, KV, 4 * R, _I32),
                                scale, _at(c, d, O, q, _BF16), _at(c, d, WS, 0), ws, _stream(stream)), c)
+
+
+# ---- steps with drafted tokens
+
+_U64 = (torch.uint64, torch.int64)  # bit masks
+
+
+def osc_tree_plan(PARENT, CU, CTX, R: int, T: int, N: int, POS, MASK, stream=None) -> None:
+    """Positions POS [T] and masks MASK [T, ceil(N / 64)] (64-bit) of the nodes of R requests' trees of at most N nodes."""
+    c = "osc_tree_plan"
+    d = torch.cuda.current_device()
+    _check(_lib.osc_tree_plan(_at(c, d, PARENT, 4 * T, _I32), _at(c, d, CU, 4 * R + 4, _I32), _at(c, d, CTX, 4 * R, _I32), R, T, N,
+                              _at(c, d, POS, 4 * T, _I32), _at(c, d, MASK, 8 * T * ((N + 63) // 64), _U64), _stream(stream)), c)
+
+
+def osc_attn_tree_workspace(S: int, R: int, HQ: int, HKV: int, D: int, page: int, MB: int, N: int) -> int:
+    """Bytes of the workspace that osc_attn_tree needs at these sizes."""
+    n = _L(0)
+    _check(_lib.osc_attn_tree_workspace(S, R, HQ, HKV, D, page, MB, N, ctypes.byref(n)), "osc_attn_tree_workspace")
+    return n.value
+
+
+def osc_attn_tree(Q, KC, VC, S: int, R: int, HQ: int, HKV: int, D: int, page: int, MB: int, NP: int, TABLE, CU, KV, MASK, N: int,
+                  scale: float, O, WS, stream=None) -> None:
+    """Attention of R requests' trees over the paged cache: each token sees its request's context and the new keys in its
+    MASK [S, ceil(N / 64)] (64-bit); WS: a tensor (or the address) of at least osc_attn_tree_workspace bytes."""
+    c = "osc_attn_tree"
+    d = torch.cuda.current_device()
+    n, q = 2 * NP * HKV * page * D, 2 * S * HQ * D
+    ws = 0 if WS is None else osc_attn_tree_workspace(S, R, HQ, HKV, D, page, MB, N) if type(WS) is int else WS.nbytes
+    _check(_lib.osc_attn_tree(_at(c, d, Q, q, _BF16), _at(c, d, KC, n, _BF16), _at(c, d, VC, n, _BF16), S, R, HQ, HKV, D, page, MB, NP,
+                              _at(c, d, TABLE, 4 * R * MB, _I32), _at(c, d, CU, 4 * R + 4, _I32), _at(c, d, KV, 4 * R, _I32),
+                              _at(c, d, MASK, 8 * S * ((N + 63) // 64), _U64), N, scale, _at(c, d, O, q, _BF16), _at(c, d, WS, 0), ws,
+                              _stream(stream)), c)
+
+
+def osc_logprobs_workspace(S: int, V: int, K: int) -> int:
+    """Bytes of the workspace that osc_logprobs needs at these sizes."""
+    n = _L(0)
+    _check(_lib.osc_logprobs_workspace(S, V, K, ctypes.byref(n)), "osc_logprobs_workspace")
+    return n.value
+
+
+def osc_logprobs(X, xt: int, S: int, V: int, ld: int, scale: float, ID, M: int, K: int, LP, ENT, TOPV, TOPI, WS, stream=None) -> None:
+    """Of S rows of V logits (X: rows of ld, bf16 or fp32 by xt), p = softmax(scale x): log p of the tokens ID [S, M] to LP, the
+    entropy to ENT [S] (or None), the K most likely tokens' log p and ids to TOPV and TOPI [S, K]; WS: a tensor (or the
+    address) of at least osc_logprobs_workspace bytes, or None where that is 0."""
+    c = "osc_logprobs"
+    d = torch.cuda.current_device()
+    ws = 0 if WS is None else osc_logprobs_workspace(S, V, K) if type(WS) is int else WS.nbytes
+    f32 = xt == OSC_Y_F32
+    need = max(0, (S - 1) * ld + V) * (4 if f32 else 2) if S > 0 else 0
+    if M == 0:
+        ID = LP = None
+    if K == 0:
+        TOPV = TOPI = None
+    _check(_lib.osc_logprobs(_at(c, d, X, need, _F32 if f32 else _BF16), xt, S, V, ld, scale, _at(c, d, ID, 4 * S * M, _I32), M, K,
+                             _at(c, d, LP, 4 * S * M, _F32), _at(c, d, ENT, 4 * S, _F32), _at(c, d, TOPV, 4 * S * K, _F32),
+                             _at(c, d, TOPI, 4 * S * K, _I32), _at(c, d, WS, 0), ws, _stream(stream)), c)
+
+
+def osc_tree_accept(TOKEN, PARENT, CHOICE, ldc: int, SLOT, POS, P: int, CU, R: int, T: int, N: int, ACC, PATH, NEXT, stream=None) -> None:
+    """The path of each tree along the chosen tokens CHOICE [T, ldc] (column 0): its length ACC [R], its nodes PATH [R, N], the token
+    behind it NEXT [R]."""
+    c = "osc_tree_accept"
+    d = torch.cuda.current_device()
+    t, r = 4 * T, 4 * R
+    _check(_lib.osc_tree_accept(_at(c, d, TOKEN, t, _I32), _at(c, d, PARENT, t, _I32), _at(c, d, CHOICE, max(0, t * ldc - 4 * (ldc - 1)), _I32),
+                                ldc, _at(c, d, SLOT, t, _I32), _at(c, d, POS, t if P > 0 else 0, _I32), P, _at(c, d, CU, r + 4, _I32), R, T, N,
+                                _at(c, d, ACC, r, _I32), _at(c, d, PATH, r * N, _I32), _at(c, d, NEXT, r, _I32), _stream(stream)), c)
+
+
+class LayerCaches:
+    """The layers' caches of osc_tree_commit, KC and VC of each (tensors, or addresses), checked once and kept."""
+
+    def __init__(self, KC, VC, NP: int, HKV: int, D: int, page: int):
+        c = "LayerCaches"
+        self.KC, self.VC, self.NP, self.HKV, self.D, self.page = list(KC), list(VC), NP, HKV, D, page
+        self.layers = len(self.KC)
+        if len(self.VC) != self.layers or self.layers > OSC_MAX_LAYERS:
+            raise OscError(2, c, f"{self.layers} layers of keys, {len(self.VC)} of values, at most {OSC_MAX_LAYERS}")
+        n = 2 * NP * HKV * page * D
+        held = [t for t in self.KC + self.VC if t is not None and type(t) is not int]
+        self.device = held[0].get_device() if held else None
+        at = lambda ts: (_P * max(1, self.layers))(*[_at(c, self.device, t, n, _BF16) for t in ts])
+        self._kc, self._vc = at(self.KC), at(self.VC)
+
+
+def osc_tree_commit(caches: LayerCaches, SLOT, CU, ACC, PATH, R: int, T: int, N: int, stream=None) -> None:
+    """Keys and values of each path's nodes to the slots behind the context, in all layers."""
+    c = "osc_tree_commit"
+    d = torch.cuda.current_device()
+    if caches.device is not None and caches.device != d:
+        raise OscError(2, c, f"caches on cuda:{caches.device}, the current device is cuda:{d}")
+    _check(_lib.osc_tree_commit(caches._kc, caches._vc, caches.layers, caches.NP, caches.HKV, caches.D, caches.page, _at(c, d, SLOT, 4 * T, _I32),
+                                _at(c, d, CU, 4 * R + 4, _I32), _at(c, d, ACC, 4 * R, _I32), _at(c, d, PATH, 4 * R * N, _I32), R, T, N,
+                                _stream(stream)), c)

@@ -6,6 +6,7 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <initializer_list>
 
 #include "osc_internal.h"
@@ -57,6 +58,7 @@ bool valid_m(int m) { return m >= 1 && m <= osc::kMaxChannels; }
 // rather than having its channels zeroed and then dropped.
 bool fmt_takes_table(osc_fmt f, const int32_t* L) { return !(f == OSC_MXFP8 && L != nullptr); }
 
+bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 bool positive(float v) { return v > 0.0f && isfinite(v); }
@@ -436,6 +438,162 @@ osc_status osc_attn_paged(const void* Q, const void* KC, const void* VC, int S, 
     a.PO = a.PM + (p.ws_bytes - notes * (long)sizeof(int4)) / 4 / (D + 2) * 2;
   }
   return from_hip(osc::launch_attn(a, D, p, static_cast<hipStream_t>(stream)));
+}
+
+// ---- steps with drafted tokens
+
+static bool valid_tree(int R, int T, int N) {
+  return R >= 0 && R <= OSC_MAX_REQUESTS && T >= 0 && N >= 1 && N <= OSC_MAX_TREE;
+}
+
+osc_status osc_tree_plan(const int32_t* PARENT, const int32_t* CU, const int32_t* CTX, int R, int T, int N, int32_t* POS,
+                         uint64_t* MASK, void* stream) {
+  const int W = (N + 63) / 64;
+  if (!valid_tree(R, T, N) || (long long)T * W > 0x7FFFFFFFLL) return OSC_E_SHAPE;
+  if (!CU || (R > 0 && !CTX)) return OSC_E_NULL;
+  if (T > 0 && (!PARENT || !POS || !MASK)) return OSC_E_NULL;
+  if (!aligned4(PARENT) || !aligned4(CU) || !aligned4(CTX) || !aligned4(POS) || !aligned8(MASK)) return OSC_E_ALIGN;
+  const long long t = 4LL * T, r = 4LL * R;
+  if (overlap({{POS, t}, {MASK, 2 * t * W}}, {{PARENT, t}, {CU, r + 4}, {CTX, r}})) return OSC_E_SHAPE;
+  if (T == 0) return OSC_OK;
+  if (!osc::launch_tree_plan) return OSC_E_DEVICE;
+  osc::TreeMaskArgs a{PARENT, CU, CTX, R, T, N, W, POS, reinterpret_cast<unsigned long long*>(MASK)};
+  return from_hip(osc::launch_tree_plan(a, static_cast<hipStream_t>(stream)));
+}
+
+osc_status osc_attn_tree_workspace(int S, int R, int HQ, int HKV, int D, int page, int MB, int N, int64_t* bytes) {
+  const osc_status st = check_attn(S, R, HQ, HKV, D, page, MB);
+  if (st != OSC_OK) return st;
+  if (!valid_tree(R, S, N)) return OSC_E_SHAPE;
+  if (!bytes) return OSC_E_NULL;
+  if (!osc::attn_tree_plan) return OSC_E_DEVICE;
+  *bytes = S == 0 || R == 0 ? 0 : osc::attn_tree_plan(R, HQ, HKV, D, N).ws_bytes;
+  return OSC_OK;
+}
+
+osc_status osc_attn_tree(const void* Q, const void* KC, const void* VC, int S, int R, int HQ, int HKV, int D, int page, int MB,
+                         int NP, const int32_t* TABLE, const int32_t* CU, const int32_t* KV, const uint64_t* MASK, int N,
+                         float scale, void* O, void* WS, int64_t ws_bytes, void* stream) {
+  const osc_status st = check_attn(S, R, HQ, HKV, D, page, MB);
+  if (st != OSC_OK) return st;
+  if (!valid_tree(R, S, N)) return OSC_E_SHAPE;
+  const int sh = page_shift(page), W = (N + 63) / 64;
+  if (NP < 1 || ((long long)NP << sh) > 0x7FFFFFFFLL || !positive(scale)) return OSC_E_SHAPE;
+  const float scale_log2 = scale * 1.4426950408889634f;
+  if (!isfinite(scale_log2)) return OSC_E_SHAPE;
+  if (S == 0 || R == 0) return OSC_OK;
+  if (!Q || !KC || !VC || !TABLE || !CU || !KV || !MASK || !O) return OSC_E_NULL;
+  if (!osc::attn_tree_plan || !osc::launch_attn_tree) return OSC_E_DEVICE;
+  const osc::TreePlan p = osc::attn_tree_plan(R, HQ, HKV, D, N);
+  if (p.ws_bytes > 0 && !WS) return OSC_E_NULL;
+  if (ws_bytes < p.ws_bytes) return OSC_E_SHAPE;
+  if (!aligned16(Q) || !aligned16(KC) || !aligned16(VC) || !aligned16(O) || !aligned16(WS) || !aligned4(TABLE) ||
+      !aligned4(CU) || !aligned4(KV) || !aligned8(MASK))
+    return OSC_E_ALIGN;
+  const long long rows = 2LL * S * HQ * D, cache = (2LL * NP * HKV * D) << sh, r = 4LL * R;
+  if (overlap({{O, rows}, {WS, p.ws_bytes}},
+              {{Q, rows}, {KC, cache}, {VC, cache}, {TABLE, r * MB}, {CU, r + 4}, {KV, r}, {MASK, 8LL * S * W}}))
+    return OSC_E_SHAPE;
+  osc::TreeArgs a;
+  static_cast<osc::AttnArgs&>(a) = {Q,  KC,   VC, S,  R,  HQ, HKV, HQ / HKV, sh, page - 1, MB, NP, TABLE, CU, KV, scale_log2,
+                                    O,  nullptr, nullptr, nullptr, p.target};
+  a.MASK = reinterpret_cast<const unsigned long long*>(MASK);
+  a.W = W;
+  const long notes = (long)HKV * p.target;
+  a.NOTE = static_cast<int4*>(WS);
+  a.PM = reinterpret_cast<float*>(a.NOTE + notes);
+  a.PO = a.PM + notes * 2 * p.rows * 2;
+  return from_hip(osc::launch_attn_tree(a, D, p, static_cast<hipStream_t>(stream)));
+}
+
+static osc_status check_logprobs(int S, int V, int K) {
+  return S < 0 || S >= (1 << 24) || V < 1 || V >= (1 << 24) || K < 0 || K > OSC_MAX_TOP ? OSC_E_SHAPE : OSC_OK;
+}
+
+osc_status osc_logprobs_workspace(int S, int V, int K, int64_t* bytes) {
+  const osc_status st = check_logprobs(S, V, K);
+  if (st != OSC_OK) return st;
+  if (!bytes) return OSC_E_NULL;
+  if (!osc::logprobs_plan) return OSC_E_DEVICE;
+  *bytes = S == 0 ? 0 : osc::logprobs_plan(S, V, K).ws_bytes;
+  return OSC_OK;
+}
+
+osc_status osc_logprobs(const void* X, osc_ytype xt, int S, int V, int ld, float scale, const int32_t* ID, int M, int K,
+                        float* LP, float* ENT, float* TOPV, int32_t* TOPI, void* WS, int64_t ws_bytes, void* stream) {
+  if (xt != OSC_Y_BF16 && xt != OSC_Y_F32) return OSC_E_FORMAT;
+  const osc_status st = check_logprobs(S, V, K);
+  if (st != OSC_OK) return st;
+  if (ld < V || (long long)S * ld >= (1LL << 34) || M < 0 || M > 65536 || (long long)S * M > 0x7FFFFFFFLL) return OSC_E_SHAPE;
+  const float scale_log2 = scale * 1.4426950408889634f;
+  if (!positive(scale) || !isfinite(scale_log2)) return OSC_E_SHAPE;
+  if (S == 0) return OSC_OK;
+  if (!X || (M > 0 && (!ID || !LP)) || (K > 0 && (!TOPV || !TOPI))) return OSC_E_NULL;
+  if (!osc::logprobs_plan || !osc::launch_logprobs) return OSC_E_DEVICE;
+  const osc::LogprobsPlan p = osc::logprobs_plan(S, V, K);
+  if (p.ws_bytes > 0 && !WS) return OSC_E_NULL;
+  if (ws_bytes < p.ws_bytes) return OSC_E_SHAPE;
+  if (M == 0) ID = nullptr, LP = nullptr;
+  if (K == 0) TOPV = nullptr, TOPI = nullptr;
+  if (!aligned16(X) || !aligned4(ID) || !aligned4(LP) || !aligned4(ENT) || !aligned4(TOPV) || !aligned4(TOPI) || !aligned16(WS))
+    return OSC_E_ALIGN;
+  const long long size = xt == OSC_Y_F32 ? 4 : 2, s = 4LL * S;
+  if (overlap({{LP, s * M}, {ENT, s}, {TOPV, s * K}, {TOPI, s * K}, {WS, p.ws_bytes}},
+              {{X, ((long long)(S - 1) * ld + V) * size}, {ID, s * M}}))
+    return OSC_E_SHAPE;
+  if (M == 0 && K == 0 && !ENT) return OSC_OK;
+  osc::LogprobsArgs a{X, xt, S, V, ld, scale_log2, ID, M, K, LP, ENT, TOPV, TOPI, WS, p.chunks};
+  return from_hip(osc::launch_logprobs(a, static_cast<hipStream_t>(stream)));
+}
+
+osc_status osc_tree_accept(const int32_t* TOKEN, const int32_t* PARENT, const int32_t* CHOICE, int ldc, const int32_t* SLOT,
+                           const int32_t* POS, int P, const int32_t* CU, int R, int T, int N, int32_t* ACC, int32_t* PATH,
+                           int32_t* NEXT, void* stream) {
+  if (!valid_tree(R, T, N) || ldc < 1 || P < 0 || (long long)T * ldc >= (1LL << 34)) return OSC_E_SHAPE;
+  if (R == 0) return OSC_OK;
+  if (!CU || !ACC || !PATH || !NEXT) return OSC_E_NULL;
+  if (T > 0 && (!TOKEN || !PARENT || !CHOICE || !SLOT || (P > 0 && !POS))) return OSC_E_NULL;
+  if (!aligned4(TOKEN) || !aligned4(PARENT) || !aligned4(CHOICE) || !aligned4(SLOT) || !aligned4(POS) || !aligned4(CU) ||
+      !aligned4(ACC) || !aligned4(PATH) || !aligned4(NEXT))
+    return OSC_E_ALIGN;
+  const long long t = 4LL * T, r = 4LL * R;
+  if (overlap({{ACC, r}, {PATH, r * N}, {NEXT, r}},
+              {{TOKEN, t}, {PARENT, t}, {CHOICE, T > 0 ? t * ldc - 4 * (ldc - 1) : 0}, {SLOT, t}, {POS, P > 0 ? t : 0}, {CU, r + 4}}))
+    return OSC_E_SHAPE;
+  if (!osc::launch_tree_accept) return OSC_E_DEVICE;
+  osc::AcceptArgs a{TOKEN, PARENT, CHOICE, ldc, SLOT, POS, P, CU, R, T, N, ACC, PATH, NEXT};
+  return from_hip(osc::launch_tree_accept(a, static_cast<hipStream_t>(stream)));
+}
+
+osc_status osc_tree_commit(void* const* KC, void* const* VC, int layers, int NP, int HKV, int D, int page, const int32_t* SLOT,
+                           const int32_t* CU, const int32_t* ACC, const int32_t* PATH, int R, int T, int N, void* stream) {
+  const int sh = page_shift(page);
+  if (sh < 0 || !valid_tree(R, T, N) || layers < 0 || layers > OSC_MAX_LAYERS || !valid_heads(1, HKV, D) || NP < 1) return OSC_E_SHAPE;
+  if (((long long)NP << sh) > 0x7FFFFFFFLL) return OSC_E_SHAPE;
+  if (R == 0 || T == 0 || layers == 0) return OSC_OK;
+  if (!KC || !VC || !SLOT || !CU || !ACC || !PATH) return OSC_E_NULL;
+  if (!aligned4(SLOT) || !aligned4(CU) || !aligned4(ACC) || !aligned4(PATH)) return OSC_E_ALIGN;
+  osc::CommitArgs a;
+  for (int l = 0; l < layers; ++l) {
+    if (!KC[l] || !VC[l]) return OSC_E_NULL;
+    if (!aligned16(KC[l]) || !aligned16(VC[l])) return OSC_E_ALIGN;
+    a.KC[l] = KC[l], a.VC[l] = VC[l];
+  }
+  // the caches in the order of their addresses: each ends before the next begins
+  const uintptr_t cache = (uintptr_t)((2LL * NP * HKV * D) << sh);
+  uintptr_t at[2 * OSC_MAX_LAYERS];
+  for (int l = 0; l < layers; ++l) at[2 * l] = reinterpret_cast<uintptr_t>(KC[l]), at[2 * l + 1] = reinterpret_cast<uintptr_t>(VC[l]);
+  std::sort(at, at + 2 * layers);
+  for (int i = 0; i + 1 < 2 * layers; ++i)
+    if (at[i + 1] - at[i] < cache) return OSC_E_SHAPE;
+  const long long t = 4LL * T, r = 4LL * R;
+  for (int i = 0; i < 2 * layers; ++i)
+    if (overlap({{reinterpret_cast<const void*>(at[i]), (long long)cache}}, {{SLOT, t}, {CU, r + 4}, {ACC, r}, {PATH, r * N}})) return OSC_E_SHAPE;
+  if (!osc::launch_tree_commit) return OSC_E_DEVICE;
+  a.layers = layers, a.NP = NP, a.HKV = HKV, a.D = D, a.sh = sh;
+  a.SLOT = SLOT, a.CU = CU, a.ACC = ACC, a.PATH = PATH;
+  a.R = R, a.T = T, a.N = N;
+  return from_hip(osc::launch_tree_commit(a, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -1,0 +1,415 @@
+// Attention of trees of drafted tokens over the paged cache.
+//
+//   O[t][hq] = sum_j softmax_j(scale * q . k_j) v_j      over the context j < kv - n, and the new keys that the
+//                                                        bits of MASK[t] name
+//
+// with the running maximum and sum, the transposed products and the layouts of osc_attn.hip.  A tree's rows all see the
+// context, which is nearly all of the keys: a tile's length is that of its request, and a mask is needed in the last
+// steps only.
+#include "osc_attn_dev.h"
+
+namespace osc {
+namespace {
+
+typedef unsigned long long u64;
+
+// Bits j0 .. j0 + 63 of what a row sees of the new keys, whose words are at m: all of the context ahead of them, nothing behind.
+__device__ __forceinline__ u64 window(const u64* m, int W, int j0) {
+  const int w = j0 >> 6, s = j0 & 63;
+  const u64 lo = w < 0 ? ~0ull : w < W ? m[w] : 0;
+  const u64 hi = w + 1 < 0 ? ~0ull : w + 1 < W ? m[w + 1] : 0;
+  return s ? lo >> s | hi << (64 - s) : lo;
+}
+
+// which of 8 values are not finite
+__device__ __forceinline__ int not_finite(v8bf v) {
+  const v4i w = __builtin_bit_cast(v4i, v);
+  int f = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f |= (((w[i >> 1] >> (i & 1 ? 16 : 0)) & 0x7F80) == 0x7F80 ? 1 : 0) << i;
+  return f;
+}
+
+// A bit pattern over the 16 lanes of a row
+__device__ __forceinline__ int or_row(int v) {
+  v |= __builtin_amdgcn_update_dpp(0, v, 0xB1, 0xF, 0xF, false);
+  v |= __builtin_amdgcn_update_dpp(0, v, 0x4E, 0xF, 0xF, false);
+  v |= __builtin_amdgcn_update_dpp(0, v, 0x141, 0xF, 0xF, false);
+  v |= __builtin_amdgcn_update_dpp(0, v, 0x140, 0xF, 0xF, false);
+  return v;
+}
+
+// ------------------------------------------------------------------ tiles of up to 64 rows
+// RB blocks of 16 rows; the four wavefronts take 32 keys each in turn, straight from memory into the registers that the
+// products want, every byte once, and are merged at the end.
+template <int D, int RB>
+__device__ __forceinline__ void tree_tile(const TreeArgs& a, const Tile& t, int h, float* lds) {
+  constexpr int DK = D / 32, DB = D / 16;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int col = lane & 15, grp = lane >> 4;
+  const int g = a.g;
+  const __bf16* Kc = static_cast<const __bf16*>(a.KC);
+  const __bf16* Vc = static_cast<const __bf16*>(a.VC);
+  const int nb = RB == 1 ? 1 : t.rows - t.row0 >= 16 * RB ? RB : (t.rows - t.row0 + 15) >> 4;  // blocks with rows
+  v8bf q[RB][DK];
+  const u64* words[RB];  // the row's mask
+#pragma unroll
+  for (int b = 0; b < RB; ++b) {
+    const int row = t.row0 + 16 * b + col, tok = row / g;
+    const bool live = row < t.rows;
+    words[b] = live ? a.MASK + (long)(t.tok0 + tok) * a.W : nullptr;
+    const long out_row = (long)(t.tok0 + tok) * a.HQ + h * g + (row - tok * g);
+#pragma unroll
+    for (int s = 0; s < DK; ++s) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) q[b][s][i] = (__bf16)0.0f;
+      if (live) q[b][s] = *reinterpret_cast<const v8bf*>(static_cast<const __bf16*>(a.Q) + out_row * D + s * 32 + grp * 8);
+    }
+  }
+  const int lo = 2 * t.lo, hi = clampi((t.kv + 31) >> 5, lo, 2 * t.hi);  // steps of 32 keys
+
+  v4f o[RB][DB];
+  float m[RB], mc[RB], l[RB];
+#pragma unroll
+  for (int b = 0; b < RB; ++b) {
+#pragma unroll
+    for (int d = 0; d < DB; ++d) o[b][d] = v4f{0, 0, 0, 0};
+    m[b] = neg_inf(), mc[b] = 0.0f, l[b] = 0.0f;
+  }
+  const float c = a.scale_log2;
+  // the pages of the wavefront's next 32 steps, a run of 16 keys a lane (a page holds at least one)
+  int ids = 0;
+  for (int st = lo + wave, n = 0; st < hi; st += 4, ++n) {
+    const int k0 = st * 32;
+    if ((n & 31) == 0) ids = page_of(a, t, k0 + (lane >> 1) * 128 + (lane & 1) * 16);
+    const int id0 = __builtin_amdgcn_readlane(ids, 2 * (n & 31)), id1 = __builtin_amdgcn_readlane(ids, 2 * (n & 31) + 1);
+    const bool whole = k0 + 32 <= t.kv && id0 >= 0 && id1 >= 0;
+    const int idl = (grp & 2) ? id1 : id0;  // V's keys 8 * grp ..
+    const int u = k0 + (grp & 2) * 8;
+    const __bf16* vp = Vc + block_at<D>(a, idl < 0 ? 0 : idl, h) + ((long)col << a.sh) + (u & a.mask) + (grp & 1) * 8;
+    v8bf kf[2][DK], vf[DB];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int kr = 8 * (col >> 2) + 4 * x + (col & 3);  // the key (of 32) in row col of score tile x
+      const int id = kr < 16 ? id0 : id1;
+      const int uk = k0 + (kr & 16);
+      const __bf16* kp = Kc + block_at<D>(a, id < 0 ? 0 : id, h) + (long)((uk & a.mask) + (kr & 15)) * D + grp * 8;
+#pragma unroll
+      for (int s = 0; s < DK; ++s) kf[x][s] = *reinterpret_cast<const v8bf*>(kp + s * 32);
+    }
+#pragma unroll
+    for (int d = 0; d < DB; ++d) vf[d] = *reinterpret_cast<const v8bf*>(vp + ((long)(16 * d) << a.sh));
+    const bool masked = !whole || k0 + 32 > t.first;
+    int there = 255, bad = 0;  // which of the lane's keys k0 + 8 grp .. exist, and have a value that is not finite
+    if (masked) {
+      const int nv = idl < 0 ? 0 : clampi(t.kv - (k0 + 8 * grp), 0, 8);
+      there = (1 << nv) - 1;
+#pragma unroll
+      for (int d = 0; d < DB; ++d) {  // 0 * NaN is not 0: such values go, and rows that see the key become NaN by its score
+        const int f = not_finite(vf[d]) | ~there;
+        bad |= f & there;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) vf[d][i] = (f >> i) & 1 ? (__bf16)0.0f : vf[d][i];
+      }
+      bad = or_row(bad);
+    }
+#pragma unroll
+    for (int b = 0; b < RB; ++b) {
+      if (b >= nb) break;
+      v4f sc[2];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        sc[x] = v4f{0, 0, 0, 0};
+#pragma unroll
+        for (int s = 0; s < DK; ++s) sc[x] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf[x][s], q[b][s], sc[x], 0, 0, 0);
+      }
+      // scores of keys k0 + 8 grp + 4 x + i; the masked ones are selected away, whatever they hold
+      if (masked) {
+        const int see = words[b] ? (int)window(words[b], a.W, k0 + 8 * grp - t.first) & there : 0;
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (((see & bad) >> (4 * x + i)) & 1) sc[x][i] = __builtin_nanf("");
+            if (!((see >> (4 * x + i)) & 1)) sc[x][i] = neg_inf();
+          }
+      }
+      float mx = neg_inf();
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mx = fmaxf(mx, sc[x][i]);
+      if (__any(mx * c > mc[b] + kSlack || (m[b] == neg_inf() && mx > neg_inf()))) {
+        const float mn = fmaxf(m[b], max_groups(mx));
+        const float ms = mn == neg_inf() ? 0.0f : mn;
+        const float f = __builtin_amdgcn_exp2f(m[b] * c - ms * c);
+        l[b] *= f;
+#pragma unroll
+        for (int d = 0; d < DB; ++d) o[b][d] *= f;
+        m[b] = mn;
+        mc[b] = ms * c;
+      }
+      v8bf p, rest;  // the weights, and what their rounding leaves out
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[x][i], c, -mc[b]));
+          l[b] += e;
+          p[4 * x + i] = (__bf16)e;
+          rest[4 * x + i] = (__bf16)(e - (float)p[4 * x + i]);
+        }
+#pragma unroll
+      for (int d = 0; d < DB; ++d) {
+        o[b][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf[d], p, o[b][d], 0, 0, 0);
+        o[b][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf[d], rest, o[b][d], 0, 0, 0);
+      }
+    }
+  }
+  // merge the wavefronts, a block of 16 rows at a time: m, l and O^T of each through LDS
+  float* ml = lds;                   // [4][2][16]
+  float* ob = lds + 128;             // [4][16][D + 4]
+  constexpr int PT = 16 * D / 256;  // values a thread joins
+  const int orow = threadIdx.x / (D / PT), d0 = (threadIdx.x % (D / PT)) * PT;
+#pragma unroll
+  for (int b = 0; b < RB; ++b) {
+    if (b >= nb) break;
+    l[b] += __shfl_xor(l[b], 16);
+    l[b] += __shfl_xor(l[b], 32);
+    __syncthreads();  // the block before is merged
+    if (grp == 0) ml[wave * 32 + col] = m[b], ml[wave * 32 + 16 + col] = l[b];
+#pragma unroll
+    for (int d = 0; d < DB; ++d) *reinterpret_cast<v4f*>(ob + (wave * 16 + col) * (D + 4) + 16 * d + 4 * grp) = o[b][d];
+    __syncthreads();
+    float mm = neg_inf();
+#pragma unroll
+    for (int w = 0; w < 4; ++w) mm = fmaxf(mm, ml[w * 32 + orow]);
+    const float ms = mm == neg_inf() ? 0.0f : mm;
+    float ll = 0.0f, acc[PT];
+#pragma unroll
+    for (int i = 0; i < PT; ++i) acc[i] = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const float f = __builtin_amdgcn_exp2f((ml[w * 32 + orow] - ms) * c);
+      ll += f * ml[w * 32 + 16 + orow];
+#pragma unroll
+      for (int i = 0; i < PT; ++i) acc[i] += f * ob[(w * 16 + orow) * (D + 4) + d0 + i];
+    }
+    const int r = t.row0 + 16 * b + orow;
+    if (r >= t.rows) continue;
+    if (t.part < 0) {
+      const int tk = r / g;
+      const long at = (long)(t.tok0 + tk) * a.HQ + h * g + (r - tk * g);
+      const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;  // no key: zeros
+#pragma unroll
+      for (int i = 0; i < PT; i += 4) {
+        v4bf w4;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w4[j] = (__bf16)(acc[i + j] * inv);
+        *reinterpret_cast<v4bf*>(static_cast<__bf16*>(a.O) + at * D + d0 + i) = w4;
+      }
+    } else {
+      const long at = t.part + 16 * b + orow;
+#pragma unroll
+      for (int i = 0; i < PT; i += 4)
+        *reinterpret_cast<v4f*>(a.PO + at * D + d0 + i) = v4f{acc[i], acc[i + 1], acc[i + 2], acc[i + 3]};
+      if (d0 == 0) *reinterpret_cast<float2*>(a.PM + at * 2) = float2{ms * c, ll};
+    }
+  }
+}
+
+// ------------------------------------------------------------------ the cuts
+// A request's tiles of ROWS rows, each as long as its keys (in steps of 64; 1 at least, so that rows without a key get their zeros).
+template <int ROWS>
+struct TreeRequest {
+  int c0, n, first, kv, tiles, steps;
+  __device__ __forceinline__ TreeRequest(const AttnArgs& a, int r) {
+    c0 = clampi(a.CU[r], 0, a.S);
+    const int c1 = clampi(a.CU[r + 1], 0, a.S);
+    n = c1 > c0 ? c1 - c0 : 0;
+    const int held = a.KV[r] > 0 ? a.KV[r] : 0, beyond = a.CU[r + 1] > a.S ? a.CU[r + 1] - a.S : 0;
+    const long at = (long)held - n - beyond;
+    constexpr long most = 1l << 30;  // as many positions as a table can hold: 32 bits do from here on
+    first = (int)(at < -most ? -most : at < most ? at : most);
+    kv = clampi(first + n, 0, (int)((long)a.MB << a.sh));
+    tiles = (int)(((long)n * a.g + ROWS - 1) / ROWS);
+    steps = kv > 0 ? (kv + 63) >> 6 : 1;
+  }
+  __device__ __forceinline__ long all() const { return (long)tiles * steps; }
+};
+
+// Steps that a workgroup's part has at least
+constexpr int kMinSteps = 2;
+
+// Workgroup: key head h = blockIdx % HKV, part w = blockIdx / HKV of the row in which all tiles of the head stand, cut into equal
+// parts, as many as workgroups run at once; body(t, h) for each tile of the part in turn.  A tile that a cut goes through has
+// its unnormalised outputs left in the workspace: in the workgroup's second place where it begins there, in the first behind a cut.
+// The workgroup in whose part such a tile begins notes it, for the join.
+template <int ROWS, typename Body>
+__device__ __forceinline__ void each_tree_tile(const TreeArgs& a, Body body) {
+  typedef TreeRequest<ROWS> Req;
+  const int h = blockIdx.x % a.HKV, w = blockIdx.x / a.HKV;
+  const int lane = threadIdx.x & 63;
+  const int per = (a.R + 63) >> 6;
+  int r = 0, i = 0, parts = 1, over = 0;
+  long begin = 0, first = 0, end = 0, each = 0, all;
+  {
+    const int r0 = lane * per < a.R ? lane * per : a.R, r1 = r0 + per < a.R ? r0 + per : a.R;
+    long mine = 0;
+#pragma unroll 4
+    for (int x = r0; x < r1; ++x) mine += Req(a, x).all();
+    long upto = mine;
+    const int lanes = (a.R + per - 1) / per;
+    for (int d = 1; d < lanes; d <<= 1) {
+      const long up = __shfl_up(upto, d);
+      if (lane >= d) upto += up;
+    }
+    all = lane_of(upto, lanes - 1);
+    long p = a.target;
+    if (p > all / kMinSteps) p = all / kMinSteps;
+    parts = p < 1 ? 1 : (int)p;
+    each = uniform(divide(all, parts));
+    over = (int)(all - each * parts);
+    if (w < parts && all > 0) {
+      first = each * w + (long)over * w / parts, end = each * (w + 1) + (long)over * (w + 1) / parts;
+      // the tile at `first`: its request, its number there, and where it begins
+      const int src = __ffsll(__ballot(first < upto)) - 1;
+      long from = upto - mine;
+      int hit = r0, num = 0;
+      for (int x = r0; x < r1; ++x) {
+        const Req q(a, x);
+        const long len = q.all();
+        if (first - from < len) {
+          num = (int)divide(first - from > 0 ? first - from : 0, q.steps);
+          from += (long)num * q.steps;
+          hit = x;
+          break;
+        }
+        from += len;
+      }
+      r = __builtin_amdgcn_readlane(hit, src);
+      i = __builtin_amdgcn_readlane(num, src);
+      begin = lane_of(from, src);
+    }
+  }
+  if (w >= parts || all == 0) {
+    if (threadIdx.x == 0 && w < a.target) a.NOTE[h * a.target + w] = int4{0, 0, 0, 0};
+    return;
+  }
+  for (;;) {
+    const Req q(a, r);
+    Tile t;
+    t.tok0 = __builtin_amdgcn_readfirstlane(q.c0);
+    t.first = __builtin_amdgcn_readfirstlane(q.first);
+    t.kv = __builtin_amdgcn_readfirstlane(q.kv);
+    t.pages = a.TABLE + (long)r * a.MB;
+    t.rows = __builtin_amdgcn_readfirstlane(q.n) * a.g;
+    t.row0 = i * ROWS;
+    const int len = __builtin_amdgcn_readfirstlane(q.steps), tiles = __builtin_amdgcn_readfirstlane(q.tiles);
+    t.lo = begin < first ? (int)(first - begin) : 0;
+    t.hi = begin + len > end ? (int)(end - begin) : len;
+    const bool last = begin + len >= end;
+    t.part = -1;
+    if (begin < first || begin + len > end) t.part = (((long)h * a.target + w) * 2 + (begin < first ? 0 : 1)) * ROWS;
+    if (last) {
+      int ns = 0;
+      if (begin >= first && begin + len > end) {  // the parts that begin in the tile
+        ns = 1;
+        for (int p0 = w + 1;; p0 += 64) {
+          const int p = p0 + lane;
+          const int more = __popcll(__ballot(p < parts && each * p + (long)over * p / parts < begin + len));
+          ns += more;
+          if (more < 64) break;
+        }
+      }
+      if (threadIdx.x == 0) a.NOTE[h * a.target + w] = int4{ns, t.row0, t.rows, t.tok0};
+    } else {
+      begin += len;
+      if (++i == tiles) i = 0, r = next_request(a, r);
+    }
+    body(t, h);
+    if (last) return;
+  }
+}
+
+template <int D, int RB>
+__global__ __launch_bounds__(256, 2) void k_attn_tree(TreeArgs a) {
+  __shared__ __align__(16) float lds[128 + 4 * 16 * (D + 4)];
+  each_tree_tile<16 * RB>(a, [&](const Tile& t, int h) { tree_tile<D, RB>(a, t, h, lds); });
+}
+
+// Joins the parts of the tile that part w noted: o = sum_k 2^(m_k - m) o_k / sum_k 2^(m_k - m) l_k with m the largest
+// m_k, in the order of the parts.  A row a wavefront: its lanes hold D / 64 values of the row each.
+template <int D>
+__global__ __launch_bounds__(256) void k_attn_tree_join(TreeArgs a, int rows) {
+  constexpr int E = D / 64, FLY = 8;
+  typedef float vE __attribute__((ext_vector_type(E)));
+  __shared__ float weight[4][2 * kCUs + 8];  // of a row's parts: as many as workgroups, at most
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int h = blockIdx.x % a.HKV, w = blockIdx.x / a.HKV;
+  const int4 note = a.NOTE[h * a.target + w];
+  const int ns = __builtin_amdgcn_readfirstlane(note.x < a.target - w ? note.x : a.target - w);
+  const int x = blockIdx.y * 4 + wave, row = note.y + x, tok = row / a.g;
+  if (ns <= 0 || x >= rows || row >= note.z) return;  // no barrier below: a wavefront keeps to itself
+  if (row < 0 || note.w < 0 || note.w >= a.S || tok >= a.S - note.w) return;  // a workspace that another call is writing: no row of this one
+  // row x of the tile in part w + k: in that workgroup's second place for k = 0, in its first for the others
+  auto place = [&](int k) { return (((long)h * a.target + w + k) * 2 + (k == 0 ? 1 : 0)) * rows + x; };
+  float m = neg_inf();
+  for (int k = lane; k < ns; k += 64) {
+    const float2 ml = *reinterpret_cast<const float2*>(a.PM + place(k) * 2);
+    if (ml.y != 0.0f) m = fmaxf(m, ml.x);  // a part of no keys has a sum of 0, and its output does not count
+  }
+  m = max_wave(m);
+  float l = 0.0f;
+  for (int k = lane; k < ns; k += 64) {
+    const float2 ml = *reinterpret_cast<const float2*>(a.PM + place(k) * 2);
+    const float f = ml.y != 0.0f ? __builtin_amdgcn_exp2f(ml.x - m) : 0.0f;
+    weight[wave][k] = f;
+    l += f * ml.y;
+  }
+  l = sum_wave(l);
+  __builtin_amdgcn_wave_barrier();
+  const float* src = a.PO + lane * E;
+  vE acc = {};
+  for (int k = 0; k < ns; k += FLY) {
+    vE v[FLY];
+#pragma unroll
+    for (int i = 0; i < FLY; ++i) v[i] = *reinterpret_cast<const vE*>(src + place(k + i < ns ? k + i : ns - 1) * D);
+#pragma unroll
+    for (int i = 0; i < FLY; ++i) {
+      const float wt = k + i < ns ? weight[wave][k + i] : 0.0f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] += wt != 0.0f ? v[i][e] * wt : 0.0f;
+    }
+  }
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  __bf16* out = static_cast<__bf16*>(a.O) + ((long)(note.w + tok) * a.HQ + h * a.g + (row - tok * a.g)) * D + lane * E;
+#pragma unroll
+  for (int e = 0; e < E; ++e) out[e] = (__bf16)(acc[e] * inv);
+}
+
+}  // namespace
+
+TreePlan attn_tree_plan(int R, int HQ, int HKV, int D, int N) {
+  TreePlan p;
+  (void)R, (void)N, (void)HQ;
+  p.rows = 16;
+  p.target = (2 * kCUs + HKV - 1) / HKV;  // workgroups that run at once
+  const long kept = (long)HKV * p.target * 2 * p.rows;
+  p.ws_bytes = kept * (D + 2) * 4 + (long)HKV * p.target * (long)sizeof(int4);
+  return p;
+}
+
+template <int D>
+static hipError_t launch_d(const TreeArgs& a, const TreePlan& p, hipStream_t st) {
+  const unsigned grid = (unsigned)p.target * (unsigned)a.HKV;
+  hipLaunchKernelGGL((k_attn_tree<D, 1>), dim3(grid), dim3(256), 0, st, a);
+  hipLaunchKernelGGL(k_attn_tree_join<D>, dim3(grid, (unsigned)p.rows / 4), dim3(256), 0, st, a, p.rows);
+  return hipGetLastError();
+}
+
+hipError_t launch_attn_tree(const TreeArgs& a, int D, const TreePlan& p, hipStream_t st) {
+  return D == 128 ? launch_d<128>(a, p, st) : launch_d<64>(a, p, st);
+}
+
+}  // namespace osc

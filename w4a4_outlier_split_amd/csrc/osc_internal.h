@@ -156,4 +156,64 @@ struct AttnArgs {
 };
 OSC_STEP hipError_t launch_attn(const AttnArgs& a, int D, const AttnPlan& p, hipStream_t st);
 
+// Attention with a mask among a request's new tokens (osc_attn_tree): MASK [S][W].
+struct TreePlan {
+  int rows;      // of a tile: 16, 32, 64 or 256
+  int target;    // workgroups for each key head
+  long ws_bytes;
+};
+OSC_STEP TreePlan attn_tree_plan(int R, int HQ, int HKV, int D, int N);
+struct TreeArgs : AttnArgs {
+  const unsigned long long* MASK;
+  int W;
+};
+OSC_STEP hipError_t launch_attn_tree(const TreeArgs& a, int D, const TreePlan& p, hipStream_t st);
+
+// Log probabilities (osc_logprobs); rows are cut into `chunks` parts where there are few.
+struct LogprobsPlan {
+  int chunks;
+  long ws_bytes;
+};
+OSC_STEP LogprobsPlan logprobs_plan(int S, int V, int K);
+struct LogprobsArgs {
+  const void* X;
+  osc_ytype xt;
+  int S, V, ld;
+  float scale_log2;  // scale * log2(e)
+  const int32_t* ID;
+  int M, K;
+  float *LP, *ENT, *TOPV;
+  int32_t* TOPI;
+  void* WS;
+  int chunks;
+};
+OSC_STEP hipError_t launch_logprobs(const LogprobsArgs& a, hipStream_t st);
+
+// Token trees (osc_tree_plan, osc_tree_accept, osc_tree_commit).
+struct TreeMaskArgs {
+  const int32_t *PARENT, *CU, *CTX;
+  int R, T, N, W;
+  int32_t* POS;
+  unsigned long long* MASK;
+};
+OSC_STEP hipError_t launch_tree_plan(const TreeMaskArgs& a, hipStream_t st);
+struct AcceptArgs {
+  const int32_t *TOKEN, *PARENT, *CHOICE;
+  int ldc;
+  const int32_t *SLOT, *POS;
+  int P;
+  const int32_t* CU;
+  int R, T, N;
+  int32_t *ACC, *PATH, *NEXT;
+};
+OSC_STEP hipError_t launch_tree_accept(const AcceptArgs& a, hipStream_t st);
+struct CommitArgs {  // by value: the pointers travel in the kernel's arguments
+  void* KC[OSC_MAX_LAYERS];
+  void* VC[OSC_MAX_LAYERS];
+  int layers, NP, HKV, D, sh;
+  const int32_t *SLOT, *CU, *ACC, *PATH;
+  int R, T, N;
+};
+OSC_STEP hipError_t launch_tree_commit(const CommitArgs& a, hipStream_t st);
+
 }  // namespace osc
