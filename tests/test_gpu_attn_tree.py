@@ -72,9 +72,9 @@ def check(p, got, S=None, what=""):
     S = p["S"] if S is None else S
     HQ, HKV, D, page, W = p["HQ"], p["HKV"], p["D"], p["page"], p["mask"].shape[1]
     g, cap = HQ // HKV, p["MB"] * p["page"]
-    # The weights are two bf16 (2^-16) up to 64 rows a tree, else one (2^-8); scores and exponents as D products of the terms' size in
+    # The weights are two bf16 (2^-16) up to 32 rows a tree, else one (2^-8); scores and exponents as D products of the terms' size in
     # binary32 (2^-24 each), the sums as much again; the output is rounded to bf16 (2^-8 of it).
-    wide = 2.0 ** -8 if p["N"] * g > 64 else 2.0 ** -16
+    wide = 2.0 ** -8 if p["N"] * g > 32 else 2.0 ** -16
     raw, got = got.view(torch.int16), got.double()
     covered = torch.zeros(p["S"], dtype=torch.bool, device=DEV)
     for r in range(p["R"]):
@@ -187,6 +187,10 @@ def test_attn_tree_not_finite_reaches_only_rows_that_see_it(HQ, HKV, N):
             else:
                 t[id, :, 5, at % 32] = value
         check(p, attend(p), what=kind)
+        # beside pages that do not exist one to four tiles ahead, and values of the context that are not finite behind one
+        for page in (4, 5, 6, 8):
+            p["table"][0, page] = -1
+            check(p, attend(p), what=(kind, page))
 
 
 @pytest.mark.parametrize("reqs,HQ,HKV,N", [([(60000, 16)], 8, 1, 16), ([(60000, 64)], 4, 1, 64), ([(33000, 256)], 32, 8, 256), ([(9000, 8)] * 3 + [(5, 8)] * 60, 32, 8, 8),

@@ -432,7 +432,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_small(AttnArgs a) {
 template <int D, How HOW>
 __global__ __launch_bounds__(512, D == 64 ? 4 : 2) void k_attn_large(AttnArgs a) {
   extern __shared__ __align__(16) uint8_t dlds[];
-  each_tile<kLargeRows, HOW>(a, [&](const Tile& t, int h) { large_tile<D>(a, t, h, dlds); });
+  each_tile<kLargeRows, HOW>(a, [&](const Tile& t, int h) { large_tile<D, false>(a, t, h, dlds); });
 }
 
 // The weighted sum of a row's parts 0 .. ns - 1 in their order, FLY of them in flight: part k at src + place(k) * D,

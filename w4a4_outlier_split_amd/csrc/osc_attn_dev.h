@@ -120,6 +120,43 @@ __device__ __forceinline__ long divide(long a, long b) {
   return q;
 }
 
+// A row's mask among the new keys, and bits j0 .. j0 + 63 of what it sees: all of the context ahead of them, nothing behind.
+// The words are read with the row's query: a load in the midst of the keys' would be waited for behind all that are under way.
+constexpr int kWords = OSC_MAX_TREE / 64;
+struct Words {
+  unsigned long long w[kWords];
+  template <typename Args>
+  __device__ __forceinline__ void load(const Args& a, long row) {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = i < a.W ? a.MASK[row * a.W + i] : 0;
+  }
+  __device__ __forceinline__ unsigned long long word(int i) const {
+    unsigned long long x = i < 0 ? ~0ull : 0;
+#pragma unroll
+    for (int j = 0; j < kWords; ++j) x = i == j ? w[j] : x;
+    return x;
+  }
+  __device__ __forceinline__ unsigned long long window(int j0) const {
+    const int i = j0 >> 6, s = j0 & 63;
+    const unsigned long long lo = word(i), hi = word(i + 1);
+    return s ? lo >> s | hi << (64 - s) : lo;
+  }
+};
+
+// which of 8 values are not finite
+__device__ __forceinline__ int not_finite(v4i w) {
+  int f = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f |= ((w[i] & 0x7F80) == 0x7F80 ? 1 << 2 * i : 0) | ((w[i] & 0x7F800000) == 0x7F800000 ? 2 << 2 * i : 0);
+  return f;
+}
+// values whose bits are set in f become 0
+__device__ __forceinline__ v4i without(v4i w, int f) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] &= ((f >> 2 * i) & 1 ? 0 : 0xFFFF) | ((f >> 2 * i) & 2 ? 0 : (int)0xFFFF0000);
+  return w;
+}
+
 // ------------------------------------------------------------------ large tiles
 // LDS: a ring of tiles of K [64 keys][D] and V^T [4 runs of 16 keys][D][16].  K rows hold their
 // 16-byte pieces at position piece ^ (row & (D/8 - 1)), V^T rows their two halves at half ^ (d >> 3 & 1):
@@ -157,9 +194,11 @@ __device__ __forceinline__ void load_v(const AttnArgs& a, long block, int at, in
 // cost more; four wavefronts, two workgroups a CU, read each key twice from LDS (587 us for the prompt of 8192, 495 to 535
 // so).  A step has 32 products of 32 cycles for each wavefront, 2048 cycles a SIMD, and takes about 3500: one wavefront's
 // exponentials run beside the other's products, the rest is LDS and the barrier.
-template <int D>
-__device__ __forceinline__ void large_tile(const AttnArgs& a, const Tile& t, int h, uint8_t* lds) {
+// TREE: behind the context, whose keys all rows see, a row's mask says which of the new keys it sees.
+template <int D, bool TREE, typename Args>
+__device__ __forceinline__ void large_tile(const Args& a, const Tile& t, int h, uint8_t* lds) {
   constexpr int DK = D / 16, DB = D / 32, CH = D / 8, HALF = 64 * D * 2, TILE = 2 * HALF;
+  unsigned* const flags = reinterpret_cast<unsigned*>(lds + kRing * TILE);  // TREE: keys of a tile with a value that is not finite, two in turn
   int tid = threadIdx.x;
   asm volatile("" : "+v"(tid));  // worked out again for each tile: nothing of the lane's places is kept from one to the next
   const int lane = tid & 63;
@@ -177,10 +216,12 @@ __device__ __forceinline__ void large_tile(const AttnArgs& a, const Tile& t, int
     for (int i = 0; i < 8; ++i) q[s][i] = (__bf16)0.0f;
     if (live) q[s] = *reinterpret_cast<const v8bf*>(static_cast<const __bf16*>(a.Q) + out_row * D + s * 16 + half * 8);
   }
+  Words words;
+  if constexpr (TREE) words.load(a, live ? t.tok0 + tok : t.tok0);
   const int base = t.first;
   const int last = live ? base + tok - 8 * half : -1;  // the last key the row sees, from the lane's first
   // the first row of the wavefront sees the fewest keys: tiles up to it need no mask
-  const int wfirst = base + row0 / g;
+  const int wfirst = TREE ? base - 1 : base + row0 / g;
   const int lo = t.lo, hi = t.hi;
   v16f o[DB];
 #pragma unroll
@@ -209,6 +250,7 @@ __device__ __forceinline__ void large_tile(const AttnArgs& a, const Tile& t, int
     };
     constexpr int LOADS = D / 32;  // of a wavefront for a tile
     lds_barrier();  // the tile before is done with the ring
+    if (TREE && tid < 4) flags[tid] = 0;
     int bads = 0;  // eight bits a tile: st, st + 1, st + 2 (the lowest first)
 #pragma unroll
     for (int i = 0; i < kRing - 1; ++i) {
@@ -220,6 +262,7 @@ __device__ __forceinline__ void large_tile(const AttnArgs& a, const Tile& t, int
     const int kr = 16 * (col >> 4) + 8 * ((col >> 2) & 1) + 4 * ((col >> 3) & 1) + (col & 3);
     const int ka = kr * D * 2 + ((half ^ (kr & (CH - 1))) << 4), va = HALF + col * 32 + ((half ^ ((col >> 3) & 1)) << 4);
     int slot = 0;  // of tile st
+    int turn = 0;  // of the flags
     // The part of a step that loads and waits; the runs of keys missing in the tile, and 16 where the request ends.
     auto begin = [&](int st) {
       const int k0 = st * 64, n = st - lo;
@@ -234,7 +277,29 @@ __device__ __forceinline__ void large_tile(const AttnArgs& a, const Tile& t, int
       bads |= bad_of(n + 3, k0 + 192) << 24;
       const int bad = bads & 31;
       bads = (int)((unsigned)bads >> 8);
-      if (rare(bad != 0)) {  // V of keys that do not exist may hold anything, and 0 * NaN is not 0
+      // V of keys that do not exist may hold anything, and 0 * NaN is not 0
+      if constexpr (TREE) {
+        // Nor may what a new key's holds reach the rows that do not see it: such values go, and rows that see the key
+        // become NaN by its score.
+        if (rare(bad != 0 || k0 + 63 > wfirst)) {
+          // (the flags of the tile looked through before were last read ahead of this tile's barrier, and are set behind a later one's)
+          turn ^= 1;
+          int x = tid;
+          asm volatile("" : "+v"(x));  // rarely run: nothing of it is kept in registers over the loop
+          if (x < 2) flags[2 * (turn ^ 1) + x] = 0;
+#pragma unroll
+          for (int i = 0; i < D / 64; ++i, x += 512) {  // 8 keys of one channel
+            const int u = x / (2 * D), key = u * 16 + (((x ^ (x >> 4)) & 1) << 3);
+            const int left = (bad >> u) & 1 ? 0 : clampi(t.kv - (k0 + key), 0, 8), there = (1 << left) - 1;
+            v4i* const v = reinterpret_cast<v4i*>(lds + slot + HALF) + x;
+            const v4i w = *v;
+            const int f = not_finite(w);
+            if (f & there) atomicOr(&flags[2 * turn + (key >> 5)], (unsigned)(f & there) << (key & 31));
+            if (f | (there ^ 255)) *v = without(w, f | (there ^ 255));
+          }
+          lds_barrier();
+        }
+      } else if (rare(bad != 0)) {
         uint16_t* v = reinterpret_cast<uint16_t*>(lds + slot + HALF);
         int first = tid;
         asm volatile("" : "+v"(first));  // rarely run: nothing of it is kept in registers over the loop
@@ -277,7 +342,23 @@ __device__ __forceinline__ void large_tile(const AttnArgs& a, const Tile& t, int
 #pragma unroll
         for (int d = 0; d < DB; ++d) vf[y][d] = value(y, d);
       __builtin_amdgcn_sched_barrier(0);
-      if (k0 + 63 > wfirst || bad) {
+      if constexpr (TREE) {
+        if (k0 + 63 > wfirst || bad) {
+          unsigned long long see = words.window(k0 - base);
+          if (k0 + 64 > t.kv) see &= k0 < t.kv ? ~0ull >> (64 - (t.kv - k0)) : 0;
+          see &= ~(((bad & 1 ? 0xFFFFull : 0) | (bad & 2 ? 0xFFFFull << 16 : 0)) | ((bad & 4 ? 0xFFFFull << 32 : 0) | (bad & 8 ? 0xFFFFull << 48 : 0)));
+          const unsigned long long odd = see & ((unsigned long long)flags[2 * turn + 1] << 32 | flags[2 * turn]);
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const unsigned seen = (unsigned)(see >> (16 * y + 8 * half)) & 255, nan = (unsigned)(odd >> (16 * y + 8 * half)) & 255;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float x = s[y >> 1][8 * (y & 1) + i];
+              s[y >> 1][8 * (y & 1) + i] = (nan >> i) & 1 ? __builtin_nanf("") : (seen >> i) & 1 ? x : neg_inf();
+            }
+          }
+        }
+      } else if (k0 + 63 > wfirst || bad) {
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
           const int end = (bad >> y) & 1 ? -1 : last - k0;
@@ -338,6 +419,15 @@ __device__ __forceinline__ void large_tile(const AttnArgs& a, const Tile& t, int
       }
   } else {
     const long at = t.part + wave * 32 + col;
+    if constexpr (TREE) {  // as the lanes hold them: 16 bytes a lane, 1024 a store
+      v4f* out = reinterpret_cast<v4f*>(a.PO + (t.part + wave * 32) * D) + lane;
+#pragma unroll
+      for (int d = 0; d < DB; ++d)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) out[(4 * d + i) * 64] = v4f{o[d][4 * i], o[d][4 * i + 1], o[d][4 * i + 2], o[d][4 * i + 3]};
+      if (half == 0) *reinterpret_cast<float2*>(a.PM + at * 2) = float2{m, l};
+      return;
+    }
     float* out = a.PO + at * D;
 #pragma unroll
     for (int d = 0; d < DB; ++d)

@@ -13,23 +13,6 @@ namespace {
 
 typedef unsigned long long u64;
 
-// Bits j0 .. j0 + 63 of what a row sees of the new keys, whose words are at m: all of the context ahead of them, nothing behind.
-__device__ __forceinline__ u64 window(const u64* m, int W, int j0) {
-  const int w = j0 >> 6, s = j0 & 63;
-  const u64 lo = w < 0 ? ~0ull : w < W ? m[w] : 0;
-  const u64 hi = w + 1 < 0 ? ~0ull : w + 1 < W ? m[w + 1] : 0;
-  return s ? lo >> s | hi << (64 - s) : lo;
-}
-
-// which of 8 values are not finite
-__device__ __forceinline__ int not_finite(v8bf v) {
-  const v4i w = __builtin_bit_cast(v4i, v);
-  int f = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) f |= (((w[i >> 1] >> (i & 1 ? 16 : 0)) & 0x7F80) == 0x7F80 ? 1 : 0) << i;
-  return f;
-}
-
 // A bit pattern over the 16 lanes of a row
 __device__ __forceinline__ int or_row(int v) {
   v |= __builtin_amdgcn_update_dpp(0, v, 0xB1, 0xF, 0xF, false);
@@ -52,12 +35,12 @@ __device__ __forceinline__ void tree_tile(const TreeArgs& a, const Tile& t, int 
   const __bf16* Vc = static_cast<const __bf16*>(a.VC);
   const int nb = RB == 1 ? 1 : t.rows - t.row0 >= 16 * RB ? RB : (t.rows - t.row0 + 15) >> 4;  // blocks with rows
   v8bf q[RB][DK];
-  const u64* words[RB];  // the row's mask
+  u64 word[RB];  // the row's mask (a tile of so few rows has nodes of one word)
 #pragma unroll
   for (int b = 0; b < RB; ++b) {
     const int row = t.row0 + 16 * b + col, tok = row / g;
     const bool live = row < t.rows;
-    words[b] = live ? a.MASK + (long)(t.tok0 + tok) * a.W : nullptr;
+    word[b] = live ? a.MASK[(long)(t.tok0 + tok) * a.W] : 0;
     const long out_row = (long)(t.tok0 + tok) * a.HQ + h * g + (row - tok * g);
 #pragma unroll
     for (int s = 0; s < DK; ++s) {
@@ -106,10 +89,10 @@ __device__ __forceinline__ void tree_tile(const TreeArgs& a, const Tile& t, int 
       there = (1 << nv) - 1;
 #pragma unroll
       for (int d = 0; d < DB; ++d) {  // 0 * NaN is not 0: such values go, and rows that see the key become NaN by its score
-        const int f = not_finite(vf[d]) | ~there;
+        const v4i w = __builtin_bit_cast(v4i, vf[d]);
+        const int f = not_finite(w);
         bad |= f & there;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) vf[d][i] = (f >> i) & 1 ? (__bf16)0.0f : vf[d][i];
+        vf[d] = __builtin_bit_cast(v8bf, without(w, f | (there ^ 255)));
       }
       bad = or_row(bad);
     }
@@ -125,7 +108,8 @@ __device__ __forceinline__ void tree_tile(const TreeArgs& a, const Tile& t, int 
       }
       // scores of keys k0 + 8 grp + 4 x + i; the masked ones are selected away, whatever they hold
       if (masked) {
-        const int see = words[b] ? (int)window(words[b], a.W, k0 + 8 * grp - t.first) & there : 0;
+        const int j0 = k0 + 8 * grp - t.first;  // of the lane's first key among the new ones
+        const int see = (int)(j0 >= 64 ? 0 : j0 >= 0 ? word[b] >> j0 : j0 <= -8 ? 255 : word[b] << -j0 | ((1 << -j0) - 1)) & there;
 #pragma unroll
         for (int x = 0; x < 2; ++x)
 #pragma unroll
@@ -222,7 +206,8 @@ __device__ __forceinline__ void tree_tile(const TreeArgs& a, const Tile& t, int 
 // A request's tiles of ROWS rows, each as long as its keys (in steps of 64; 1 at least, so that rows without a key get their zeros).
 template <int ROWS>
 struct TreeRequest {
-  int c0, n, first, kv, tiles, steps;
+  int c0 = 0, n = 0, first = 0, kv = 0, tiles = 0, steps = 1;
+  __device__ __forceinline__ TreeRequest() {}
   __device__ __forceinline__ TreeRequest(const AttnArgs& a, int r) {
     c0 = clampi(a.CU[r], 0, a.S);
     const int c1 = clampi(a.CU[r + 1], 0, a.S);
@@ -236,6 +221,14 @@ struct TreeRequest {
     steps = kv > 0 ? (kv + 63) >> 6 : 1;
   }
   __device__ __forceinline__ long all() const { return (long)tiles * steps; }
+  // a lane's, in scalar registers
+  __device__ __forceinline__ TreeRequest of(int lane) const {
+    TreeRequest q;
+    q.c0 = __builtin_amdgcn_readlane(c0, lane), q.n = __builtin_amdgcn_readlane(n, lane);
+    q.first = __builtin_amdgcn_readlane(first, lane), q.kv = __builtin_amdgcn_readlane(kv, lane);
+    q.tiles = __builtin_amdgcn_readlane(tiles, lane), q.steps = __builtin_amdgcn_readlane(steps, lane);
+    return q;
+  }
 };
 
 // Steps that a workgroup's part has at least
@@ -253,11 +246,13 @@ __device__ __forceinline__ void each_tree_tile(const TreeArgs& a, Body body) {
   const int per = (a.R + 63) >> 6;
   int r = 0, i = 0, parts = 1, over = 0;
   long begin = 0, first = 0, end = 0, each = 0, all;
+  // A lane has `per` requests; where that is one, it keeps it, and nobody reads the lengths again.
+  const int r0 = lane * per < a.R ? lane * per : a.R, r1 = r0 + per < a.R ? r0 + per : a.R;
+  Req own = r0 < r1 ? Req(a, r0) : Req();
   {
-    const int r0 = lane * per < a.R ? lane * per : a.R, r1 = r0 + per < a.R ? r0 + per : a.R;
-    long mine = 0;
+    long mine = own.all();
 #pragma unroll 4
-    for (int x = r0; x < r1; ++x) mine += Req(a, x).all();
+    for (int x = r0 + 1; x < r1; ++x) mine += Req(a, x).all();
     long upto = mine;
     const int lanes = (a.R + per - 1) / per;
     for (int d = 1; d < lanes; d <<= 1) {
@@ -275,37 +270,31 @@ __device__ __forceinline__ void each_tree_tile(const TreeArgs& a, Body body) {
       // the tile at `first`: its request, its number there, and where it begins
       const int src = __ffsll(__ballot(first < upto)) - 1;
       long from = upto - mine;
-      int hit = r0, num = 0;
-      for (int x = r0; x < r1; ++x) {
-        const Req q(a, x);
-        const long len = q.all();
-        if (first - from < len) {
-          num = (int)divide(first - from > 0 ? first - from : 0, q.steps);
-          from += (long)num * q.steps;
-          hit = x;
-          break;
-        }
-        from += len;
+      int hit = r0;
+      Req q = own;
+      while (hit + 1 < r1 && first - from >= q.all()) {  // (what the lanes but src find is not used)
+        from += q.all();
+        q = Req(a, ++hit);
       }
+      const int num = (int)divide(first > from ? first - from : 0, q.steps);
       r = __builtin_amdgcn_readlane(hit, src);
       i = __builtin_amdgcn_readlane(num, src);
-      begin = lane_of(from, src);
+      begin = lane_of(from + (long)num * q.steps, src);
     }
   }
   if (w >= parts || all == 0) {
     if (threadIdx.x == 0 && w < a.target) a.NOTE[h * a.target + w] = int4{0, 0, 0, 0};
     return;
   }
+  const unsigned long long has = __ballot(own.n > 0);
   for (;;) {
-    const Req q(a, r);
+    const Req q = per == 1 ? own.of(r) : Req(a, r).of(0);
     Tile t;
-    t.tok0 = __builtin_amdgcn_readfirstlane(q.c0);
-    t.first = __builtin_amdgcn_readfirstlane(q.first);
-    t.kv = __builtin_amdgcn_readfirstlane(q.kv);
+    t.tok0 = q.c0, t.first = q.first, t.kv = q.kv;
     t.pages = a.TABLE + (long)r * a.MB;
-    t.rows = __builtin_amdgcn_readfirstlane(q.n) * a.g;
+    t.rows = q.n * a.g;
     t.row0 = i * ROWS;
-    const int len = __builtin_amdgcn_readfirstlane(q.steps), tiles = __builtin_amdgcn_readfirstlane(q.tiles);
+    const int len = q.steps;
     t.lo = begin < first ? (int)(first - begin) : 0;
     t.hi = begin + len > end ? (int)(end - begin) : len;
     const bool last = begin + len >= end;
@@ -325,7 +314,7 @@ __device__ __forceinline__ void each_tree_tile(const TreeArgs& a, Body body) {
       if (threadIdx.x == 0) a.NOTE[h * a.target + w] = int4{ns, t.row0, t.rows, t.tok0};
     } else {
       begin += len;
-      if (++i == tiles) i = 0, r = next_request(a, r);
+      if (++i == q.tiles) i = 0, r = per > 1 ? next_request(a, r) : r + __ffsll(has >> r >> 1);
     }
     body(t, h);
     if (last) return;
@@ -333,79 +322,156 @@ __device__ __forceinline__ void each_tree_tile(const TreeArgs& a, Body body) {
 }
 
 template <int D, int RB>
-__global__ __launch_bounds__(256, 2) void k_attn_tree(TreeArgs a) {
+__global__ __launch_bounds__(256, RB > 2 && D == 128 ? 1 : 2) void k_attn_tree(TreeArgs a) {
   __shared__ __align__(16) float lds[128 + 4 * 16 * (D + 4)];
   each_tree_tile<16 * RB>(a, [&](const Tile& t, int h) { tree_tile<D, RB>(a, t, h, lds); });
 }
 
-// Joins the parts of the tile that part w noted: o = sum_k 2^(m_k - m) o_k / sum_k 2^(m_k - m) l_k with m the largest
-// m_k, in the order of the parts.  A row a wavefront: its lanes hold D / 64 values of the row each.
 template <int D>
-__global__ __launch_bounds__(256) void k_attn_tree_join(TreeArgs a, int rows) {
-  constexpr int E = D / 64, FLY = 8;
-  typedef float vE __attribute__((ext_vector_type(E)));
-  __shared__ float weight[4][2 * kCUs + 8];  // of a row's parts: as many as workgroups, at most
+__global__ __launch_bounds__(512, 2) void k_attn_tree_large(TreeArgs a) {
+  extern __shared__ __align__(16) uint8_t dlds[];
+  each_tree_tile<kLargeRows>(a, [&](const Tile& t, int h) { large_tile<D, true>(a, t, h, dlds); });
+}
+
+// Joins the parts of the tile that part w noted: o = sum_k 2^(m_k - m) o_k / sum_k 2^(m_k - m) l_k with m the largest
+// m_k, in a fixed order.  A lane has a piece of 16 bytes of a row's outputs, and reads its parts and their maxima and sums
+// FLY at once: the parts lie far apart, and a load that waits for another takes 2 to 3 us.
+// SHARE > 1, for few tiles of many parts each: that many wavefronts take parts of the same pieces in turn and join theirs through LDS
+// (else a wavefront's chain is long and the card empty), and workgroup j of a head looks for its j-th noted tile (a workgroup for
+// each part, most of them with nothing to do, took 19 us to come and go).
+template <int D, int ROWS, int SHARE>
+__global__ __launch_bounds__(512) void k_attn_tree_join(TreeArgs a) {
+  constexpr int FLY = 4, P = D / 4;  // pieces of a row
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int h = blockIdx.x % a.HKV, w = blockIdx.x / a.HKV;
+  const int h = blockIdx.x % a.HKV;
+  int w = blockIdx.x / a.HKV;
+  if constexpr (SHARE > 1) {
+    constexpr int MOST = 2 * kCUs / 64;  // a lane's notes
+    int noted[MOST], left = w;
+#pragma unroll
+    for (int i = 0; i < MOST; ++i) noted[i] = i * 64 + lane < a.target ? a.NOTE[h * a.target + i * 64 + lane].x : 0;
+    w = -1;
+#pragma unroll
+    for (int i = 0; i < MOST; ++i) {
+      u64 has = __ballot(noted[i] > 0);
+      const int n = __popcll(has);
+      if (w < 0 && left < n) {
+        for (; left > 0; --left) has &= has - 1;
+        w = i * 64 + __ffsll(has) - 1;
+      }
+      left -= n;
+    }
+    if (w < 0) return;
+  }
   const int4 note = a.NOTE[h * a.target + w];
   const int ns = __builtin_amdgcn_readfirstlane(note.x < a.target - w ? note.x : a.target - w);
-  const int x = blockIdx.y * 4 + wave, row = note.y + x, tok = row / a.g;
-  if (ns <= 0 || x >= rows || row >= note.z) return;  // no barrier below: a wavefront keeps to itself
-  if (row < 0 || note.w < 0 || note.w >= a.S || tok >= a.S - note.w) return;  // a workspace that another call is writing: no row of this one
-  // row x of the tile in part w + k: in that workgroup's second place for k = 0, in its first for the others
-  auto place = [&](int k) { return (((long)h * a.target + w + k) * 2 + (k == 0 ? 1 : 0)) * rows + x; };
-  float m = neg_inf();
-  for (int k = lane; k < ns; k += 64) {
-    const float2 ml = *reinterpret_cast<const float2*>(a.PM + place(k) * 2);
-    if (ml.y != 0.0f) m = fmaxf(m, ml.x);  // a part of no keys has a sum of 0, and its output does not count
-  }
-  m = max_wave(m);
-  float l = 0.0f;
-  for (int k = lane; k < ns; k += 64) {
-    const float2 ml = *reinterpret_cast<const float2*>(a.PM + place(k) * 2);
-    const float f = ml.y != 0.0f ? __builtin_amdgcn_exp2f(ml.x - m) : 0.0f;
-    weight[wave][k] = f;
-    l += f * ml.y;
-  }
-  l = sum_wave(l);
-  __builtin_amdgcn_wave_barrier();
-  const float* src = a.PO + lane * E;
-  vE acc = {};
-  for (int k = 0; k < ns; k += FLY) {
-    vE v[FLY];
+  if (ns <= 0) return;
+  // Which row of the tile, and which of its channels, the lane's piece holds: in order, or (tiles of 256 rows) 4 channels from 32 d + 8 i +
+  // 4 half of row `col` of a wavefront's 32, where d, i come from the piece's store and half, col from its lane.
+  const int piece = (SHARE > 1 ? blockIdx.y : blockIdx.y * 8 + wave) * 64 + lane;
+  const int x = ROWS == kLargeRows ? piece / (32 * P) * 32 + (lane & 31) : piece / P;
+  const int c = ROWS == kLargeRows ? (piece / 64 % (P / 2)) * 8 + 4 * (lane >> 5) : piece % P * 4;
+  const int row = note.y + x, tok = row / a.g;
+  // (a workspace that another call is writing as well may note anything: no row but the call's own)
+  const bool mine = x < ROWS && row >= 0 && row < note.z && note.w >= 0 && note.w < a.S && tok < a.S - note.w;
+  if (SHARE == 1 && !mine) return;
+  // part w + k: in that workgroup's second place for k = 0, in its first for the others
+  auto place = [&](int k) { return (((long)h * a.target + w + k) * 2 + (k == 0 ? 1 : 0)) * ROWS; };
+  float m = neg_inf(), l = 0.0f;
+  v4f acc = {};
+  if (mine)
+    for (int k0 = SHARE > 1 ? wave : 0; k0 < ns; k0 += SHARE * FLY) {
+      float2 v[FLY];
+      v4f o[FLY];
 #pragma unroll
-    for (int i = 0; i < FLY; ++i) v[i] = *reinterpret_cast<const vE*>(src + place(k + i < ns ? k + i : ns - 1) * D);
+      for (int i = 0; i < FLY; ++i) {
+        v[i] = float2{0.0f, 0.0f}, o[i] = v4f{};
+        if (k0 + i * SHARE < ns) {
+          const long at = place(k0 + i * SHARE);
+          v[i] = *reinterpret_cast<const float2*>(a.PM + (at + x) * 2);
+          o[i] = reinterpret_cast<const v4f*>(a.PO + at * D)[piece];
+        }
+      }
+      float mn = m;
 #pragma unroll
-    for (int i = 0; i < FLY; ++i) {
-      const float wt = k + i < ns ? weight[wave][k + i] : 0.0f;
+      for (int i = 0; i < FLY; ++i) mn = v[i].y != 0.0f ? fmaxf(mn, v[i].x) : mn;  // a part of no keys has a sum of 0, and its output does not count
+      const float z = mn == neg_inf() ? 0.0f : mn, fm = __builtin_amdgcn_exp2f(m - z);
+      l *= fm, acc *= fm;
+      m = mn;
 #pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] += wt != 0.0f ? v[i][e] * wt : 0.0f;
+      for (int i = 0; i < FLY; ++i) {
+        const bool counts = v[i].y != 0.0f;
+        const float f = counts ? __builtin_amdgcn_exp2f(v[i].x - z) : 0.0f;
+        l += counts ? f * v[i].y : 0.0f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[e] += counts ? o[i][e] * f : 0.0f;
+      }
+    }
+  if constexpr (SHARE > 1) {
+    __shared__ float2 ml[SHARE][64];
+    __shared__ v4f out[SHARE][64];
+    ml[wave][lane] = float2{m, l}, out[wave][lane] = acc;
+    __syncthreads();
+    if (wave != 0 || !mine) return;
+#pragma unroll
+    for (int k = 1; k < SHARE; ++k) m = fmaxf(m, ml[k][lane].x);
+    const float z = m == neg_inf() ? 0.0f : m;
+    l = 0.0f, acc = v4f{};
+#pragma unroll
+    for (int k = 0; k < SHARE; ++k) {
+      const float f = __builtin_amdgcn_exp2f(ml[k][lane].x - z);
+      l += f * ml[k][lane].y, acc += f * out[k][lane];
     }
   }
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  __bf16* out = static_cast<__bf16*>(a.O) + ((long)(note.w + tok) * a.HQ + h * a.g + (row - tok * a.g)) * D + lane * E;
+  v4bf out4;
 #pragma unroll
-  for (int e = 0; e < E; ++e) out[e] = (__bf16)(acc[e] * inv);
+  for (int e = 0; e < 4; ++e) out4[e] = (__bf16)(acc[e] * inv);
+  *reinterpret_cast<v4bf*>(static_cast<__bf16*>(a.O) + ((long)(note.w + tok) * a.HQ + h * a.g + (row - tok * a.g)) * D + c) = out4;
 }
 
 }  // namespace
 
 TreePlan attn_tree_plan(int R, int HQ, int HKV, int D, int N) {
   TreePlan p;
-  (void)R, (void)N, (void)HQ;
-  p.rows = 16;
-  p.target = (2 * kCUs + HKV - 1) / HKV;  // workgroups that run at once
+  (void)R;
+  p.N = N;
+  const int rows = N * (HQ / HKV);
+  p.rows = rows <= 16 ? 16 : rows <= 32 ? 32 : kLargeRows;
+  p.target = ((p.rows > 32 ? 1 : 2) * kCUs + HKV - 1) / HKV;  // workgroups that run at once
   const long kept = (long)HKV * p.target * 2 * p.rows;
   p.ws_bytes = kept * (D + 2) * 4 + (long)HKV * p.target * (long)sizeof(int4);
   return p;
 }
 
+template <int D, int ROWS>
+static hipError_t launch_rows(const TreeArgs& a, int N, hipStream_t st) {
+  const unsigned grid = (unsigned)a.target * (unsigned)a.HKV;
+  if constexpr (ROWS == kLargeRows) {
+    constexpr int bytes = kRing * 64 * D * 4 + 16;
+    const hipError_t e =
+        hipFuncSetAttribute(reinterpret_cast<const void*>(k_attn_tree_large<D>), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(k_attn_tree_large<D>, dim3(grid), dim3(512), bytes, st, a);
+  } else {
+    hipLaunchKernelGGL((k_attn_tree<D, ROWS / 16>), dim3(grid), dim3(256), 0, st, a);
+  }
+  // the 64 pieces of a tile that a wavefront joins; no more rows than the call has tokens
+  const long most = ((long)a.S * a.g + 31) / 32 * 32, pieces = (most < ROWS ? most : ROWS) * (D / 4) / 64;
+  // Tiles of 24 parts and more, were all requests alike, are joined by 8 wavefronts each.
+  const long tiles = (long)a.R * ((N * a.g + ROWS - 1) / ROWS);
+  if (24 * tiles <= a.target) {
+    const long all = (long)a.S * a.g / ROWS + (a.R < a.S ? a.R : a.S);  // tiles that there can be, whatever the lengths
+    hipLaunchKernelGGL((k_attn_tree_join<D, ROWS, 8>), dim3((unsigned)((all < a.target ? all : a.target) * a.HKV), (unsigned)pieces), dim3(512), 0, st, a);
+    return hipGetLastError();
+  }
+  hipLaunchKernelGGL((k_attn_tree_join<D, ROWS, 1>), dim3(grid, (unsigned)((pieces + 7) / 8)), dim3(512), 0, st, a);
+  return hipGetLastError();
+}
+
 template <int D>
 static hipError_t launch_d(const TreeArgs& a, const TreePlan& p, hipStream_t st) {
-  const unsigned grid = (unsigned)p.target * (unsigned)a.HKV;
-  hipLaunchKernelGGL((k_attn_tree<D, 1>), dim3(grid), dim3(256), 0, st, a);
-  hipLaunchKernelGGL(k_attn_tree_join<D>, dim3(grid, (unsigned)p.rows / 4), dim3(256), 0, st, a, p.rows);
-  return hipGetLastError();
+  return p.rows == 16 ? launch_rows<D, 16>(a, p.N, st) : p.rows == 32 ? launch_rows<D, 32>(a, p.N, st) : launch_rows<D, kLargeRows>(a, p.N, st);
 }
 
 hipError_t launch_attn_tree(const TreeArgs& a, int D, const TreePlan& p, hipStream_t st) {

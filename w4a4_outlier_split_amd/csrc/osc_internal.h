@@ -158,7 +158,8 @@ OSC_STEP hipError_t launch_attn(const AttnArgs& a, int D, const AttnPlan& p, hip
 
 // Attention with a mask among a request's new tokens (osc_attn_tree): MASK [S][W].
 struct TreePlan {
-  int rows;      // of a tile: 16, 32, 64 or 256
+  int N;         // nodes of a tree, at most
+  int rows;      // of a tile: 16, 32 or 256
   int target;    // workgroups for each key head
   long ws_bytes;
 };
