@@ -13,6 +13,7 @@
 // seldom a few more, are read once more and their values put in order.  (Noting the values: 2048 rows of 151936, K = 5 and 64, 154 and
 // 250 us, see below.)
 #include "osc_internal.h"
+#include "osc_lanes.h"
 
 namespace osc {
 namespace {
@@ -28,8 +29,6 @@ constexpr int kVectors = 4 * kList, kValues = 8 * kThreads;
 constexpr int kParts = 64 * OSC_MAX_TOP;  // values of a row's parts
 constexpr float kSlack = 4.0f;
 constexpr int kNone = 0x007FFFFF;  // the key of -inf
-
-__device__ __forceinline__ float neg_inf() { return -__builtin_inff(); }
 
 // values in the order of unsigned numbers (no NaN; both zeros alike), and back
 __device__ __forceinline__ unsigned key_of(float x) {
@@ -53,70 +52,60 @@ __device__ __forceinline__ Sum join(Sum a, Sum b) {
   return {r, fa * a.l + fb * b.l, fa * (a.t + (fa == 0.0f ? 0.0f : da) * a.l) + fb * (b.t + (fb == 0.0f ? 0.0f : db) * b.l)};
 }
 
+// A noted value or vector: its key, and the lower index first.  0 is none.
+__device__ __forceinline__ u64 entry(unsigned key, int idx) { return (u64)key << 32 | (unsigned)~idx; }
+__device__ __forceinline__ unsigned key_in(u64 e) { return (unsigned)(e >> 32); }
+__device__ __forceinline__ int index_in(u64 e) { return (int)~(unsigned)e; }
+
+constexpr int kAhead = 8;  // entries that in_order reads at once
 template <int CAP>
-struct Lds {  // CAP: values, or vectors, noted
-  unsigned key[CAP];
-  int idx[CAP];
+struct Lds {
+  u64 list[CAP + kAhead];
   Sum sums[4];
   unsigned top[kThreads];
   int votes[2][4];
-  unsigned worst;
+  u64 differ[4];
 };
 
-// how many threads' flags are set, over the workgroup; `turn` alternates from call to call
+// Cuts the n entries of the list to the K best (n >= K); the worst of those.  All threads, behind a barrier.  Run where values are
+// alike, rows of zeros in a padded step for instance, so the bits that all entries share are left out.
 template <int CAP>
-__device__ __forceinline__ int vote(Lds<CAP>& s, int mine, int& turn) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) mine += __shfl_xor(mine, d);
-  if ((threadIdx.x & 63) == 0) s.votes[turn][threadIdx.x >> 6] = mine;
-  __syncthreads();
-  const int all = s.votes[turn][0] + s.votes[turn][1] + s.votes[turn][2] + s.votes[turn][3];
-  turn ^= 1;
-  return all;
-}
-
-// Cuts the n noted values to the K best (n >= K).  All threads, behind a barrier.
-template <int CAP>
-__device__ __attribute__((noinline)) void prune(Lds<CAP>& s, int n, int K) {
+__device__ __attribute__((noinline)) u64 prune(Lds<CAP>& s, int n, int K) {
   constexpr int PER = CAP / kThreads;
-  unsigned k[PER];
-  int ix[PER];
+  const int wave = threadIdx.x >> 6;
+  const u64 first = s.list[0];
+  u64 e[PER], differ = 0;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int j = threadIdx.x + i * kThreads;
-    k[i] = j < n ? s.key[j] : 0, ix[i] = j < n ? s.idx[j] : 0x7FFFFFFF;
+    e[i] = j < n ? s.list[j] : 0;
+    differ |= j < n ? e[i] ^ first : 0;
   }
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) differ |= __shfl_xor(differ, d);
+  if ((threadIdx.x & 63) == 0) s.differ[wave] = differ;
   __syncthreads();
+  differ = s.differ[0] | s.differ[1] | s.differ[2] | s.differ[3];
+  u64 low = first & ~differ;  // the largest entry that K reach, bit by bit
   int turn = 0;
-  unsigned low = 0;  // the largest key that K values reach
-  for (int bit = 31; bit >= 0; --bit) {
-    const unsigned trial = low | 1u << bit;
+  while (differ != 0) {
+    const u64 bit = 1ull << (63 - __clzll(differ)), trial = low | bit;
+    differ ^= bit;
     int mine = 0;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) mine += k[i] >= trial;
-    if (vote(s, mine, turn) >= K) low = trial;
-  }
-  int above = 0;
-#pragma unroll
-  for (int i = 0; i < PER; ++i) above += k[i] > low;
-  const int need = K - vote(s, above, turn);
-  int last = 0;  // the smallest index up to which `need` values have that key: one below it has not
-  for (int bit = 23; bit >= 0; --bit) {
-    const int trial = last | 1 << bit;
-    int mine = 0;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) mine += k[i] == low && ix[i] < trial;
-    if (vote(s, mine, turn) < need) last = trial;
+    for (int i = 0; i < PER; ++i) mine += __popcll(__ballot(e[i] >= trial));
+    if ((threadIdx.x & 63) == 0) s.votes[turn][wave] = mine;
+    __syncthreads();
+    if (s.votes[turn][0] + s.votes[turn][1] + s.votes[turn][2] + s.votes[turn][3] >= K) low = trial;
+    turn ^= 1;  // (read ahead of the next barrier, written behind it)
   }
   if (threadIdx.x == 0) s.votes[turn][0] = 0;
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < PER; ++i)
-    if (k[i] > low || (k[i] == low && ix[i] <= last)) {
-      const int at = atomicAdd(&s.votes[turn][0], 1);
-      s.key[at] = k[i], s.idx[at] = ix[i];
-    }
+    if (e[i] >= low && e[i] > 0) s.list[atomicAdd(&s.votes[turn][0], 1)] = e[i];
   __syncthreads();
+  return low;
 }
 
 // A key that at least K of the workgroup's values reach: the K-th largest of the threads' largest keys (0 if there are fewer).
@@ -138,21 +127,25 @@ __device__ __forceinline__ unsigned reached(Lds<CAP>& s, unsigned mine, int K) {
   return low;
 }
 
-// The best of the entries k[], ix[] that the threads hold (0: none) into the list, from its start: those that reach a bound that K of
-// them do, K at least if there are as many, and seldom more than 256.  Returns their number.  All threads.
+// The best of the entries that the threads hold into the list, from its start: those whose key reaches a bound that K of
+// them do, K at least if there are as many, and seldom more than 256.  Returns their number, and the bound.  All threads.
 template <int BITS, int PER, int CAP>
-__device__ __forceinline__ int gather(Lds<CAP>& s, const unsigned (&k)[PER], const int (&ix)[PER], int K) {
-  unsigned most = 0;
+__device__ __forceinline__ int gather(Lds<CAP>& s, const u64 (&e)[PER], int K, unsigned& bound) {
+  u64 most = 0;
 #pragma unroll
-  for (int i = 0; i < PER; ++i) most = most > k[i] ? most : k[i];
+  for (int i = 0; i < PER; ++i) most = most > e[i] ? most : e[i];
   if (threadIdx.x == 0) s.votes[0][0] = 0;
-  const unsigned bound = reached<BITS>(s, most, K);
+  bound = reached<BITS>(s, key_in(most), K);
+  const u64 low = bound > 0 ? (u64)bound << 32 : 1;
+  int mine = 0;
 #pragma unroll
-  for (int i = 0; i < PER; ++i)
-    if (k[i] >= bound && k[i] > 0) {
-      const int at = atomicAdd(&s.votes[0][0], 1);
-      s.key[at] = k[i], s.idx[at] = ix[i];
-    }
+  for (int i = 0; i < PER; ++i) mine += e[i] >= low;
+  if (mine > 0) {
+    int at = atomicAdd(&s.votes[0][0], mine);
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (e[i] >= low) s.list[at++] = e[i];
+  }
   __syncthreads();
   const int n = s.votes[0][0];
   __syncthreads();
@@ -166,50 +159,46 @@ struct Kept {
   float bound;  // all that is as large as that, and
   int last;     // where it is that large, up to this index
 };
-__device__ __attribute__((noinline)) Kept cut(unsigned* key, int* idx, int n, int K, Kept old) {
+__device__ __attribute__((noinline)) Kept cut(u64* list, int n, int K, Kept old) {
   constexpr int PER = kList / 64;
   const int lane = threadIdx.x & 63;
-  unsigned k[PER], most = 0;
-  int ix[PER];
+  u64 e[PER], most = 0;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int j = lane + 64 * i;
-    k[i] = j < n ? key[j] : 0, ix[i] = j < n ? idx[j] : 0x7FFFFFFF;
-    most = most > k[i] ? most : k[i];
+    e[i] = j < n ? list[j] : 0;
+    most = most > e[i] ? most : e[i];
   }
-  auto count = [&](auto&& holds) {
+  auto count = [&](u64 least) {
     int c = 0;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) c += __popcll(__ballot(holds(i)));
+    for (int i = 0; i < PER; ++i) c += __popcll(__ballot(e[i] >= least));
     return c;
   };
-  unsigned low = 0;
-  for (int bit = 31; bit >= 0; --bit)
-    if (__popcll(__ballot(most >= (low | 1u << bit))) >= K) low |= 1u << bit;
+  u64 low = 0;
+  for (int bit = 63; bit >= 32; --bit)
+    if (__popcll(__ballot(most >= (low | 1ull << bit))) >= K) low |= 1ull << bit;
   int last = 0x7FFFFFFF;
-  if (count([&](int i) { return k[i] >= low; }) > kList / 2) {
+  if (count(low) > kList / 2) {
     low = 0;
-    for (int bit = 31; bit >= 0; --bit)
-      if (count([&](int i) { return k[i] >= (low | 1u << bit); }) >= K) low |= 1u << bit;
-    const int need = K - count([&](int i) { return k[i] > low; });
-    last = 0;  // the smallest index up to which `need` values have that key
-    for (int bit = 23; bit >= 0; --bit)
-      if (count([&](int i) { return k[i] == low && ix[i] < (last | 1 << bit); }) < need) last |= 1 << bit;
+    for (int bit = 63; bit >= 0; --bit)
+      if (count(low | 1ull << bit) >= K) low |= 1ull << bit;
+    last = index_in(low);
   }
   int have = 0;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    const bool keep = k[i] > low || (k[i] == low && ix[i] <= last && k[i] > 0);
+    const bool keep = e[i] >= low && e[i] > 0;
     const u64 who = __ballot(keep);
-    const int at = have + __popcll(who & ((1ull << lane) - 1));
-    if (keep) key[at] = k[i], idx[at] = ix[i];
+    if (keep) list[have + __popcll(who & ((1ull << lane) - 1))] = e[i];
     have += __popcll(who);
   }
-  const float bound = value_of(low);
+  const float bound = value_of(key_in(low));
   return {have, bound, bound > old.bound || last < old.last ? last : old.last};
 }
 
-// The K best of the n noted values in order: write(place, key, index) for each, then none(place) for places without one.
+// The K best of the list's n entries in order: write(place, entry) for each, then none(place) for places without one.  All
+// threads, behind a barrier.
 template <int CAP, typename Write, typename None>
 __device__ __forceinline__ void in_order(Lds<CAP>& s, int n, int K, Write write, None none) {
   if (n > kThreads) {  // as many are alike
@@ -217,11 +206,19 @@ __device__ __forceinline__ void in_order(Lds<CAP>& s, int n, int K, Write write,
     n = K;
   }
   const int i = threadIdx.x;
+  if (i < kAhead) s.list[n + i] = 0;
+  __syncthreads();
   if (i < n) {
-    const u64 mine = (u64)s.key[i] << 32 | (unsigned)~s.idx[i];
+    const u64 mine = s.list[i];
     int place = 0;
-    for (int j = 0; j < n; ++j) place += ((u64)s.key[j] << 32 | (unsigned)~s.idx[j]) > mine;
-    if (place < K) write(place, s.key[i], s.idx[i]);
+    for (int j = 0; j < n; j += kAhead) {
+      u64 e[kAhead];
+#pragma unroll
+      for (int x = 0; x < kAhead; ++x) e[x] = s.list[j + x];
+#pragma unroll
+      for (int x = 0; x < kAhead; ++x) place += e[x] > mine;
+    }
+    if (place < K) write(place, mine);
   }
   if (i >= n && i < K) none(i);
 }
@@ -237,44 +234,54 @@ __device__ __forceinline__ float logit(const LogprobsArgs& a, long at) {
   return F32 ? static_cast<const float*>(a.X)[at] : (float)static_cast<const __bf16*>(a.X)[at];
 }
 
+// The first of a row's given tokens that the thread has, asked for ahead of the row's sums.
+template <bool F32>
+struct Given {
+  int id = -1;
+  float x = 0.0f;
+  __device__ __forceinline__ Given(const LogprobsArgs& a, int row, int i) {
+    if (i >= a.M) return;
+    id = a.ID[(long)row * a.M + i];
+    if (id >= a.V) id = -1;
+    if (id >= 0) x = logit<F32>(a, (long)row * a.ld + id);
+  }
+};
+
 // A row's outputs, from its sums and the n noted values.
 template <bool F32, int CAP>
-__device__ __forceinline__ void finish(const LogprobsArgs& a, int row, const Sum& s, Lds<CAP>& lds, int n) {
+__device__ __forceinline__ void finish(const LogprobsArgs& a, int row, const Sum& s, Given<F32> given, Lds<CAP>& lds, int n) {
   const bool none = is_none(s);
   const float c = a.scale_log2, nan = __builtin_nanf(""), log2l = none ? nan : log2f(s.l);
   for (int i = threadIdx.x; i < a.M; i += kThreads) {
-    const long at = (long)row * a.M + i;
-    const int id = a.ID[at];
-    a.LP[at] = none ? nan : id < 0 || id >= a.V ? neg_inf() : logp(s, log2l, logit<F32>(a, (long)row * a.ld + id), c);
+    if (i >= kThreads) given = Given<F32>(a, row, i);
+    a.LP[(long)row * a.M + i] = none ? nan : given.id < 0 ? neg_inf() : logp(s, log2l, given.x, c);
   }
   if (a.ENT && threadIdx.x == 0) a.ENT[row] = none ? nan : (log2l - s.t / s.l) * 0.6931471805599453f;
   if (a.K == 0) return;
   const long out = (long)row * a.K;
   in_order(
       lds, n, a.K,
-      [&](int at, unsigned key, int idx) {
-        a.TOPV[out + at] = none ? nan : logp(s, log2l, value_of(key), c);
-        a.TOPI[out + at] = none ? -1 : idx;
+      [&](int at, u64 e) {
+        a.TOPV[out + at] = none ? nan : logp(s, log2l, value_of(key_in(e)), c);
+        a.TOPI[out + at] = none ? -1 : index_in(e);
       },
       [&](int at) { a.TOPV[out + at] = none ? nan : neg_inf(), a.TOPI[out + at] = -1; });
 }
 
+// The threads' sums joined, the same in all: around the largest R, lanes by a tree, then the wavefronts.
 template <int CAP>
 __device__ __forceinline__ Sum join_all(Sum s, Lds<CAP>& lds) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const Sum o = {__shfl_xor(s.r, d), __shfl_xor(s.l, d), __shfl_xor(s.t, d)};
-    s = (threadIdx.x & d) ? join(o, s) : join(s, o);  // the same on both sides
-  }
+  const Sum at = join(Sum{max_wave(s.r), 0.0f, 0.0f}, s);  // (what lies at 0 adds nothing)
+  s = Sum{at.r, sum_wave(at.l), sum_wave(at.t)};
   if ((threadIdx.x & 63) == 0) lds.sums[threadIdx.x >> 6] = s;
   __syncthreads();
   return join(join(lds.sums[0], lds.sums[1]), join(lds.sums[2], lds.sums[3]));
 }
 
-// A part's record in the workspace: its sums, the number of its best values, and them.
+// A part's record in the workspace: its sums, and its K best values (0: fewer).
 struct Record {
   Sum s;
-  int n;
+  int unused;
 };
 __host__ __device__ inline long record_bytes(int K) { return (long)sizeof(Record) + 8l * K; }
 
@@ -316,6 +323,7 @@ __global__ __launch_bounds__(kThreads, 4) void k_logprobs(LogprobsArgs a) {
     return __builtin_bit_cast(float, F32 ? w : i & 1 ? w & 0xFFFF0000u : w << 16);
   };
 
+  const Given<F32> given(a, row, a.chunks == 1 ? tid : a.M);
   Sum s = {neg_inf(), 0.0f, 0.0f};
   float z = 0.0f;              // - R, or 0
   float limit = neg_inf();     // the largest logit that R need not move for
@@ -352,8 +360,7 @@ __global__ __launch_bounds__(kThreads, 4) void k_logprobs(LogprobsArgs a) {
     return most;
   };
   // the wavefront's list, its bound (no more than the K-th best of its values and the workgroup's first ones), and how many there are
-  unsigned* const keys = lds.key + (tid >> 6) * kList;
-  int* const idxs = lds.idx + (tid >> 6) * kList;
+  u64* const list = lds.list + (tid >> 6) * kList;
   float bound = a.K > 0 ? neg_inf() : __builtin_nanf("");
   int bound_idx = 0x7FFFFFFF, have = 0;
   auto note = [&](float most, int v) {
@@ -361,10 +368,10 @@ __global__ __launch_bounds__(kThreads, 4) void k_logprobs(LogprobsArgs a) {
     const u64 who = __ballot(takes);
     if (who == 0) return;
     const int at = have + __popcll(who & ((1ull << (tid & 63)) - 1));
-    if (takes) keys[at] = key_of(most), idxs[at] = v;
+    if (takes) list[at] = entry(key_of(most), v);
     have += __popcll(who);
     if (have > kCut) {
-      const Kept kept = cut(keys, idxs, have, a.K, Kept{have, bound, bound_idx});
+      const Kept kept = cut(list, have, a.K, Kept{have, bound, bound_idx});
       have = __builtin_amdgcn_readfirstlane(kept.n), bound = kept.bound, bound_idx = kept.last;
     }
   };
@@ -438,60 +445,62 @@ __global__ __launch_bounds__(kThreads, 4) void k_logprobs(LogprobsArgs a) {
   }
   int n = 0;
   if (a.K > 0) {
+    auto noted = [&](float most, int v) { return most > neg_inf() ? entry(key_of(most), v) : 0; };
+    unsigned worst;  // of the vectors' largest values
     if (rounds == 0) {  // what the threads hold is all
-      unsigned k[kRound + 1];
-      int ix[kRound + 1];
+      u64 e[kRound + 1];
 #pragma unroll
-      for (int u = 0; u < kRound; ++u) k[u] = most[u] > neg_inf() ? key_of(most[u]) : 0, ix[u] = v + u * kThreads;
-      k[kRound] = edge_most > neg_inf() ? key_of(edge_most) : 0, ix[kRound] = edge;
-      n = gather<BITS>(lds, k, ix, a.K);
+      for (int u = 0; u < kRound; ++u) e[u] = noted(most[u], v + u * kThreads);
+      e[kRound] = noted(edge_most, edge);
+      n = gather<BITS>(lds, e, a.K, worst);
     } else {
 #pragma unroll
       for (int u = 0; u < kRound; ++u) note(most[u], v + u * kThreads);
       constexpr int PER = kList / 64;
-      unsigned k[PER];
-      int ix[PER];
+      u64 e[PER];
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
         const int j = (tid & 63) + 64 * i;
-        k[i] = j < have ? keys[j] : 0, ix[i] = j < have ? idxs[j] : 0;
+        e[i] = j < have ? list[j] : 0;
       }
-      n = gather<BITS>(lds, k, ix, a.K);
+      n = gather<BITS>(lds, e, a.K, worst);
     }
     if (n > kThreads) {  // as many are alike
-      prune(lds, n, a.K);
+      worst = key_in(prune(lds, n, a.K));
       n = a.K;
     }
-    // the vectors' values that reach the worst of their largest, if there are K of them
-    const unsigned mine = tid < n ? lds.key[tid] : 0xFFFFFFFFu;
-    const u4 best = load(tid < n ? lds.idx[tid] : v1);
-    const int e0 = tid < n ? lds.idx[tid] * E - skew : 0;
-    if (tid == 0) lds.worst = 0xFFFFFFFFu, lds.votes[0][0] = 0;
-    __syncthreads();
-    atomicMin(&lds.worst, mine);
-    __syncthreads();
-    const float worst = n < a.K ? neg_inf() : value_of(lds.worst);
+    // the vectors' values that reach as much, of which there are K unless there are not as many at all
+    const int at = tid < n ? index_in(lds.list[tid]) : v1;
+    const u4 best = load(at);
+    if (tid == 0) lds.votes[0][0] = 0;
+    u64 e[E];
+    int mine = 0;
 #pragma unroll
     for (int i = 0; i < E; ++i) {
       const float x = value(best, i);
-      if (x > neg_inf() && x >= worst) {
-        const int at = atomicAdd(&lds.votes[0][0], 1);
-        lds.key[at] = key_of(x), lds.idx[at] = e0 + i;
-      }
+      e[i] = x > neg_inf() && key_of(x) >= worst ? entry(key_of(x), at * E - skew + i) : 0;
+      mine += e[i] > 0;
+    }
+    __syncthreads();
+    if (mine > 0) {
+      int to = atomicAdd(&lds.votes[0][0], mine);
+#pragma unroll
+      for (int i = 0; i < E; ++i)
+        if (e[i] > 0) lds.list[to++] = e[i];
     }
     __syncthreads();
     n = lds.votes[0][0];
   }
   s = join_all(s, lds);
   if (a.chunks == 1) {
-    finish<F32>(a, row, s, lds, n);
+    finish<F32>(a, row, s, given, lds, n);
     return;
   }
   uint8_t* rec = static_cast<uint8_t*>(a.WS) + blockIdx.x * record_bytes(a.K);
-  if (tid == 0) *reinterpret_cast<Record*>(rec) = Record{s, n < a.K ? n : a.K};
+  if (tid == 0) *reinterpret_cast<Record*>(rec) = Record{s, 0};
   if (a.K == 0) return;
-  uint2* best = reinterpret_cast<uint2*>(rec + sizeof(Record));
-  in_order(lds, n, a.K, [&](int at, unsigned key, int idx) { best[at] = uint2{key, (unsigned)idx}; }, [&](int at) { best[at] = uint2{0, 0}; });
+  u64* kept = reinterpret_cast<u64*>(rec + sizeof(Record));
+  in_order(lds, n, a.K, [&](int at, u64 e) { kept[at] = e; }, [&](int at) { kept[at] = 0; });
 }
 
 // A row's parts in their order, from one batch of loads: the sums, and the parts' best values, of which those that reach the
@@ -505,27 +514,28 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_join(LogprobsArgs a) {
   auto at = [&](int c) { return rec + c * record_bytes(K); };
   Sum s = {neg_inf(), 0.0f, 0.0f};
   if (tid < a.chunks) s = reinterpret_cast<const Record*>(at(tid))->s;  // at most as many as a wavefront's lanes
-  unsigned k[PER];
-  int ix[PER];
+  u64 e[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int j = tid + i * kThreads, ch = K > 0 ? j / K : 0;
-    k[i] = 0, ix[i] = 0;
-    if (i * kThreads < a.chunks * K && ch < a.chunks) {
-      const uint2 v = reinterpret_cast<const uint2*>(at(ch) + sizeof(Record))[j - ch * K];
-      k[i] = v.x, ix[i] = (int)v.y;
-    }
+    e[i] = 0;
+    // (the parts' best go to different threads, or few threads' largest would be much larger than the others')
+    if (i * kThreads < a.chunks * K && ch < a.chunks) e[i] = reinterpret_cast<const u64*>(at(ch) + sizeof(Record))[(j - ch * K + ch) % K];
   }
+  const Given<F32> given(a, row, tid);
   s = join_all(s, lds);
-  finish<F32>(a, row, s, lds, K > 0 ? gather<F32 ? 32 : 16>(lds, k, ix, K) : 0);
+  unsigned bound;
+  finish<F32>(a, row, s, given, lds, K > 0 ? gather<F32 ? 32 : 16>(lds, e, K, bound) : 0);
 }
 
 }  // namespace
 
-// Rows are cut where there are fewer than workgroups that the card needs (4 a CU), into parts of 2048 values at least.
+// Rows are cut where there are fewer than workgroups that keep the memory busy: one a CU, two where rows are cut anyway, in parts of
+// 2048 values at least.  (Rows of 151936, 8 alternatives, for 512 and 256 workgroups: 128 rows 26 and 28 us, 256 rows 32 and 31, 384 rows 40 and 37;
+// 1024 workgroups: 512 rows 48 us, 40 in one part each.)
 LogprobsPlan logprobs_plan(int S, int V, int K) {
   LogprobsPlan p;
-  long want = S > 0 ? (1024 + S - 1) / S : 1;
+  long want = S >= 256 || S == 0 ? 1 : (512 + S - 1) / S;
   const long most = V / 2048;
   if (want > most) want = most;
   if (want > 64) want = 64;  // 64 parts of at most OSC_MAX_TOP values are what the join holds
