@@ -62,7 +62,7 @@ template <int CAP>
 struct Lds {
   u64 list[CAP + kAhead];
   Sum sums[4];
-  unsigned top[kThreads];
+  unsigned top[2][kThreads];  // for two bounds: none is written while the other may be read
   int votes[2][4];
   u64 differ[4];
 };
@@ -111,12 +111,12 @@ __device__ __attribute__((noinline)) u64 prune(Lds<CAP>& s, int n, int K) {
 // A key that at least K of the workgroup's values reach: the K-th largest of the threads' largest keys (0 if there are fewer).
 // BITS: how many of a key's upper bits count.  Every wavefront takes all 256 keys, four a lane, and settles a bit at a time.
 template <int BITS, int CAP>
-__device__ __forceinline__ unsigned reached(Lds<CAP>& s, unsigned mine, int K) {
-  s.top[threadIdx.x] = mine;
+__device__ __forceinline__ unsigned reached(Lds<CAP>& s, int which, unsigned mine, int K) {
+  s.top[which][threadIdx.x] = mine;
   __syncthreads();
   unsigned k[4], low = 0;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) k[j] = s.top[64 * j + (threadIdx.x & 63)];
+  for (int j = 0; j < 4; ++j) k[j] = s.top[which][64 * j + (threadIdx.x & 63)];
   for (int bit = 31; bit >= 32 - BITS; --bit) {
     const unsigned trial = low | 1u << bit;
     int n = 0;
@@ -135,7 +135,7 @@ __device__ __forceinline__ int gather(Lds<CAP>& s, const u64 (&e)[PER], int K, u
 #pragma unroll
   for (int i = 0; i < PER; ++i) most = most > e[i] ? most : e[i];
   if (threadIdx.x == 0) s.votes[0][0] = 0;
-  bound = reached<BITS>(s, key_in(most), K);
+  bound = reached<BITS>(s, 1, key_in(most), K);
   const u64 low = bound > 0 ? (u64)bound << 32 : 1;
   int mine = 0;
 #pragma unroll
@@ -396,7 +396,7 @@ __global__ __launch_bounds__(kThreads, 4) void k_logprobs(LogprobsArgs a) {
 #pragma unroll
     for (int u = 0; u < kRound; ++u) most[u] = add(q[u]), all = fmaxf(all, most[u]);
     if (a.K > 0) {
-      const unsigned low = reached<BITS>(lds, key_of(all), a.K);
+      const unsigned low = reached<BITS>(lds, 0, key_of(all), a.K);
       bound = low <= (unsigned)kNone ? neg_inf() : value_of(low);
     }
     const int more = rounds > 1 ? STEP : 0;
