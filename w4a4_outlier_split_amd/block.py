@@ -5,7 +5,8 @@ that follows it, §4 for W2).
 Host-side orchestration only: buffers are torch tensors (device memory), every step of every
 layer runs in the library's kernels through the C ABI.  ``Linear`` and ``MLP`` are the projections;
 ``Pages``, ``LayerCache``, ``Attention`` and ``Block`` put the residual adds, the norms and the attention
-over the paged cache between them.
+over the paged cache between them, ``Drafts`` lets a step's tokens be trees of drafted ones, and ``Head`` gives
+log probabilities behind the last block.
 
 Per-module rule (§2.3): a module input's clustering density C is the share of a group's outlier
 events captured by its statically indexed channel (§2.2), averaged over the groups that saw an
@@ -22,10 +23,11 @@ from typing import Optional
 
 import numpy as np
 
-from . import (OSC_MAX_GROUPS, OSC_MXFP4, OSC_MXFP8, OSC_Y_BF16, code_bytes, osc_attn_paged, osc_attn_workspace,
-               osc_build_table_multi, osc_gemm_fp8, osc_gemm_multi, osc_pack_weights_multi, osc_page_plan,
-               osc_qkv_append, osc_quant_act_multi, osc_rmsnorm_quant, osc_swiglu, osc_swiglu_quant, scale_bytes,
-               side_elems)
+from . import (OSC_MAX_GROUPS, OSC_MAX_LAYERS, OSC_MAX_TREE, OSC_MXFP4, OSC_MXFP8, OSC_Y_BF16, LayerCaches, code_bytes,
+               osc_attn_paged, osc_attn_tree, osc_attn_tree_workspace, osc_attn_workspace, osc_build_table_multi, osc_gemm_fp8,
+               osc_gemm_multi, osc_logprobs, osc_logprobs_workspace, osc_pack_weights_multi, osc_page_plan, osc_qkv_append,
+               osc_quant_act_multi, osc_rmsnorm_quant, osc_swiglu, osc_swiglu_quant, osc_tree_accept, osc_tree_commit, osc_tree_plan,
+               scale_bytes, side_elems)
 
 DENSITY_THRESHOLD = 0.35  # §2.3: below it the module falls back to FP8 microscaling
 ALPHA, RHO = 5.0, 0.35    # table-builder defaults (§3.1 / §5.2; rho: the 35 % line of §2.3)
@@ -316,6 +318,72 @@ class LayerCache:
         self.VC = torch.zeros((pages.NP, HKV, D, pages.page), dtype=torch.bfloat16, device=device)
 
 
+class Drafts:
+    """Trees of drafted tokens for steps on ``pages``, of at most N nodes a request, over the LayerCache of each layer.  A
+    tree's node 0 is the request's last certain token, which is not in the cache yet.  One step: set ``pages.new`` to the trees' sizes,
+    ``token`` and ``parent`` (int32 [T], request by request as the plan has them; a parent is a node's number in its request, -1
+    the context); call ``pages.plan`` and ``plan``; run the blocks with ``drafts``; call ``accept`` with the token chosen behind
+    each node, ``commit`` and ``advance`` (not the pages' own), all on one stream.  All of it is captureable in a graph.
+
+    ``acc`` (int32 [R]) nodes of each request are in the cache then, those of ``path`` [R, N] in order, and ``next`` [R] is the
+    token behind them, the next tree's node 0 (-1 for a request without a tree, or whose node 0 found no row, page, room
+    or position: ``pages.lost`` counts those, and the tree is to be given again)."""
+
+    def __init__(self, torch, pages: Pages, N: int, caches, device):
+        if not 1 <= N <= OSC_MAX_TREE:
+            raise ValueError(f"a tree of {N} nodes, 1 to {OSC_MAX_TREE} are possible")
+        self.torch, self.pages, self.N = torch, pages, N
+        i32 = lambda *n: torch.zeros(n, dtype=torch.int32, device=device)
+        self.token, self.parent = i32(pages.T), i32(pages.T)
+        self.mask = torch.zeros((pages.T, (N + 63) // 64), dtype=torch.int64, device=device)
+        self.acc, self.path, self.next = i32(pages.R), i32(pages.R, N), i32(pages.R)
+        self.at = torch.arange(pages.free.numel(), dtype=torch.int32, device=device)
+        self.layers = list(caches)
+        self.groups = [LayerCaches([c.KC for c in g], [c.VC for c in g], pages.NP, g[0].KC.shape[1], g[0].KC.shape[3], pages.page)
+                       for g in (self.layers[i:i + OSC_MAX_LAYERS] for i in range(0, len(self.layers), OSC_MAX_LAYERS))]
+
+    def plan(self, stream=None) -> None:
+        """Behind the pages' plan: the nodes' positions into ``pages.pos``, and their masks."""
+        p = self.pages
+        osc_tree_plan(self.parent, p.cu, p.ctx, p.R, p.T, self.N, p.pos, self.mask, stream)
+
+    def accept(self, choice, ldc: int = 1, stream=None) -> None:
+        """choice: int32, the token chosen behind row t at choice[t * ldc] (Head's ``topi`` with ldc = K: the most likely one)."""
+        p = self.pages
+        end = p.positions if p.positions < p.MB * p.page else 0  # of the rotary table, if it is the shorter
+        osc_tree_accept(self.token, self.parent, choice, ldc, p.slot, p.pos, end, p.cu, p.R, p.rows, self.N, self.acc, self.path, self.next, stream)
+
+    def commit(self, stream=None) -> None:
+        p = self.pages
+        for g in self.groups:
+            osc_tree_commit(g, p.slot, p.cu, self.acc, self.path, p.R, p.rows, self.N, stream)
+
+    def advance(self, stream=None) -> None:
+        """The accepted nodes are in the cache now; pages that the step took for others go back to the free list."""
+        torch, p = self.torch, self.pages
+        sh = p.page.bit_length() - 1
+        with _on(torch, stream):
+            new = p.new.clamp(min=0)
+            pages_of = lambda n: (n + (p.page - 1)) >> sh
+            had = pages_of(p.ctx)
+            # 32-bit sums do: a table row holds fewer than 2^31 tokens
+            took = pages_of(torch.minimum(new, p.MB * p.page - p.ctx) + p.ctx) - had
+            kept = pages_of(p.ctx + self.acc) - had
+            ends = torch.stack([took, kept]).cumsum(1, dtype=torch.int32)
+            # The step's pages stand in the free list request by request, from its head on: those kept come first now.  (They may be more
+            # than the list has: what is behind its end was never taken.)
+            j = self.at - p.head
+            r = torch.searchsorted(ends[0], j, right=True).clamp(max=p.R - 1)
+            e, k, t = ends[:, r], kept[r], took[r]
+            nth = j - (e[0] - t)  # of its request's pages
+            to = torch.where(nth < k, e[1] - k + nth, ends[1, -1:] + j - e[1])
+            to = torch.where((j >= 0) & (j < ends[0, -1:]), to + p.head, self.at)
+            p.free.copy_(torch.empty_like(p.free).index_copy_(0, to.long(), p.free))
+            p.head.add_(ends[1, -1:])
+            p.ctx.add_(self.acc)
+            p.lost.add_(((new > 0) & (self.acc == 0)).sum(0, keepdim=True, dtype=torch.int32))
+
+
 class Attention:
     """QKV projection -> head norms, rotary embedding, cache write -> attention over the paged cache
     -> output projection.  qkv: [(HQ + 2 HKV) D, H], out: [H, HQ D]; wq, wk: [D] bf16 head norm weights
@@ -328,17 +396,19 @@ class Attention:
         self.wq, self.wk, self.cs, self.eps = wq, wk, cs, eps
         self.scale = D ** -0.5
 
-    def buffers(self, S: int, pages: Pages, device):
-        """Buffers for steps of up to S rows."""
+    def buffers(self, S: int, pages: Pages, device, N: int = 0):
+        """Buffers for steps of up to S rows, with trees of up to N nodes (0: without)."""
         t = self.qkv.torch
         bf = lambda *n: t.zeros(n, dtype=t.bfloat16, device=device)  # padding rows stay finite through the output projection
         # steps of fewer rows may need more of a workspace than those of many: single tokens, and the fewest rows of the other kernel
         ws = max(osc_attn_workspace(s, pages.R, self.HQ, self.HKV, self.D, pages.page, pages.MB) for s in {S, min(S, pages.R), min(S, pages.R + 1)})
+        if N > 0:
+            ws = max(ws, osc_attn_tree_workspace(S, pages.R, self.HQ, self.HKV, self.D, pages.page, pages.MB, N))
         return {"x": self.qkv.act_buffers(S, device), "qkv": bf(S, self.qkv.N), "q": bf(S, self.HQ, self.D), "o": bf(S, self.HQ, self.D),
                 "ws": t.empty((ws,), dtype=t.uint8, device=device), "ox": self.out.act_buffers(S, device)}
 
-    def forward_quantized(self, S: int, pages: Pages, cache: LayerCache, bufs, Y, stream=None) -> None:
-        """From the QKV projection's quantized input in bufs["x"], by the plan in ``pages``."""
+    def forward_quantized(self, S: int, pages: Pages, cache: LayerCache, bufs, Y, stream=None, drafts=None) -> None:
+        """From the QKV projection's quantized input in bufs["x"], by the plan in ``pages``, and that of the trees in ``drafts``."""
         if S > pages.T:
             raise ValueError(f"{S} rows, and a plan of {pages.T}")
         pages.rows = min(pages.rows, S)
@@ -348,8 +418,12 @@ class Attention:
         osc_qkv_append(bufs["qkv"], S, self.HQ, self.HKV, self.D, self.wq, self.wk, self.eps, self.cs,
                        0 if self.cs is None else self.cs.shape[0], pages.pos, pages.slot, bufs["q"], cache.KC, cache.VC, pages.NP,
                        pages.page, stream)
-        osc_attn_paged(bufs["q"], cache.KC, cache.VC, S, pages.R, self.HQ, self.HKV, self.D, pages.page, pages.MB, pages.NP, pages.table,
-                       pages.cu, pages.kv, self.scale, bufs["o"], bufs["ws"], stream)
+        if drafts is None:
+            osc_attn_paged(bufs["q"], cache.KC, cache.VC, S, pages.R, self.HQ, self.HKV, self.D, pages.page, pages.MB, pages.NP, pages.table,
+                           pages.cu, pages.kv, self.scale, bufs["o"], bufs["ws"], stream)
+        else:
+            osc_attn_tree(bufs["q"], cache.KC, cache.VC, S, pages.R, self.HQ, self.HKV, self.D, pages.page, pages.MB, pages.NP, pages.table,
+                          pages.cu, pages.kv, drafts.mask, drafts.N, self.scale, bufs["o"], bufs["ws"], stream)
         self.out.forward(bufs["o"], S, bufs["ox"], Y, OSC_Y_BF16, stream)
 
 
@@ -368,20 +442,53 @@ class Block:
             raise ValueError("the projections do not share the residual stream's width")
         self.attention, self.mlp, self.w_attn, self.w_mlp, self.eps = attention, mlp, w_attn, w_mlp, eps
 
-    def buffers(self, S: int, pages: Pages, device):
+    def buffers(self, S: int, pages: Pages, device, N: int = 0):
         t = self.mlp.up.torch
-        return {"attn": self.attention.buffers(S, pages, device), "mlp": self.mlp.buffers(S, device),
+        return {"attn": self.attention.buffers(S, pages, device, N), "mlp": self.mlp.buffers(S, device),
                 "y": t.empty((S, self.mlp.up.H), dtype=t.bfloat16, device=device)}
 
-    def forward(self, X, res, S: int, pages: Pages, cache: LayerCache, bufs, Y, stream=None):
+    def forward(self, X, res, S: int, pages: Pages, cache: LayerCache, bufs, Y, stream=None, drafts=None):
         """X: [S, H] bf16, the block before's Y; res: the residual stream, updated in place.  The first
         block takes res = None: X is the stream then, and is updated in place.  Writes the MLP's
-        output to Y (neither X nor res) and returns the stream."""
+        output to Y (neither X nor res) and returns the stream.  drafts: the Drafts whose trees the step's tokens are."""
         if any(t is not None and _meet(Y, t) for t in (X, res)):
             raise ValueError("Y is written while X and the residual stream are in use")
         self.attention.qkv.norm_quantize(X, res, self.w_attn, self.eps, S, bufs["attn"]["x"], stream)
         stream_rows = X if res is None else res
-        self.attention.forward_quantized(S, pages, cache, bufs["attn"], bufs["y"], stream)
+        self.attention.forward_quantized(S, pages, cache, bufs["attn"], bufs["y"], stream, drafts)
         self.mlp.up.norm_quantize(bufs["y"], stream_rows, self.w_mlp, self.eps, S, bufs["mlp"]["x"], stream)
         self.mlp.forward_quantized(S, bufs["mlp"], Y, OSC_Y_BF16, stream)
         return stream_rows
+
+
+class Head:
+    """Behind the last block: its output joins the residual stream, the final norm (w: [H] bf16), the projection onto the vocabulary, and
+    from its logits log probabilities.  V: tokens that there are, if the projection has rows behind them."""
+
+    def __init__(self, proj: Linear, w, eps: float = 1e-6, V: Optional[int] = None):
+        self.proj, self.w, self.eps, self.V = proj, w, eps, proj.N if V is None else V
+        if not 1 <= self.V <= proj.N:
+            raise ValueError(f"{self.V} tokens from a projection of {proj.N} rows")
+
+    def buffers(self, S: int, device, M: int = 0, K: int = 1):
+        """For steps of up to S rows, with M given tokens a row and the K most likely ones."""
+        t = self.proj.torch
+        f32 = lambda *n: t.zeros(n, dtype=t.float32, device=device)
+        # steps of fewer rows may need more of a workspace: rows are cut then
+        ws = max((osc_logprobs_workspace(s, self.V, K) for s in range(1, min(S, 255) + 1)), default=0)
+        return {"x": self.proj.act_buffers(S, device), "logits": t.empty((S, self.proj.N), dtype=t.bfloat16, device=device), "M": M, "K": K,
+                "lp": f32(S, M), "ent": f32(S), "topv": f32(S, K), "topi": t.zeros((S, K), dtype=t.int32, device=device),
+                "ws": t.empty((ws,), dtype=t.uint8, device=device)}
+
+    def forward(self, X, res, S: int, bufs, stream=None) -> None:
+        """X: [S, H] bf16, the last block's Y; res: the residual stream, updated in place (None: X is the stream).  Logits to
+        bufs["logits"]."""
+        self.proj.norm_quantize(X, res, self.w, self.eps, S, bufs["x"], stream)
+        self.proj.gemm(bufs["x"], S, bufs["logits"], OSC_Y_BF16, stream)
+
+    def logprobs(self, S: int, bufs, ids=None, scale: float = 1.0, stream=None) -> None:
+        """Of p = softmax(scale logits): log p of the tokens ids (int32 [S, M]) to bufs["lp"], the entropy to bufs["ent"], the most likely
+        tokens' log p and ids to bufs["topv"] and bufs["topi"] [S, K]."""
+        M = bufs["M"] if ids is not None else 0
+        osc_logprobs(bufs["logits"], OSC_Y_BF16, S, self.V, self.proj.N, scale, ids, M, bufs["K"], bufs["lp"], bufs["ent"], bufs["topv"],
+                     bufs["topi"], bufs["ws"], stream)
