@@ -441,7 +441,7 @@ osc_status osc_tree_plan(const int32_t* PARENT, const int32_t* CU, const int32_t
  * osc_attn_tree -- osc_attn_paged with a mask of each token's own among the new ones: token i of the n new tokens of request r
  * sees the keys j < KV[r] - n, its context, and of the new keys KV[r] - n + b those with bit b of MASK[CU[r] + i] set,
  *   O = sum_j softmax_j(scale q . k_j) v_j,
- * with scores, softmax and sums in binary32.  The weights are rounded to bf16 for the second product where N * HQ / HKV > 32, and to
+ * with scores, softmax and sums in binary32.  The weights are rounded to bf16 for the second product where N * HQ / HKV > 16, and to
  * two bf16 (2^-16 of each) otherwise.
  *   MASK uint64 [S][W], 8-byte aligned, as osc_tree_plan writes it, or any other: bits of tokens that the request does not have, and of keys
  *   that do not exist, count for nothing.  Everything else is as osc_attn_paged has it.

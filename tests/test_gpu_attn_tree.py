@@ -72,9 +72,9 @@ def check(p, got, S=None, what=""):
     S = p["S"] if S is None else S
     HQ, HKV, D, page, W = p["HQ"], p["HKV"], p["D"], p["page"], p["mask"].shape[1]
     g, cap = HQ // HKV, p["MB"] * p["page"]
-    # The weights are two bf16 (2^-16) up to 32 rows a tree, else one (2^-8); scores and exponents as D products of the terms' size in
+    # The weights are two bf16 (2^-16) up to 16 rows a tree, else one (2^-8); scores and exponents as D products of the terms' size in
     # binary32 (2^-24 each), the sums as much again; the output is rounded to bf16 (2^-8 of it).
-    wide = 2.0 ** -8 if p["N"] * g > 32 else 2.0 ** -16
+    wide = 2.0 ** -8 if p["N"] * g > 16 else 2.0 ** -16
     raw, got = got.view(torch.int16), got.double()
     covered = torch.zeros(p["S"], dtype=torch.bool, device=DEV)
     for r in range(p["R"]):

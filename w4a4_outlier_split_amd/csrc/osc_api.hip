@@ -467,7 +467,7 @@ osc_status osc_attn_tree_workspace(int S, int R, int HQ, int HKV, int D, int pag
   if (!valid_tree(R, S, N)) return OSC_E_SHAPE;
   if (!bytes) return OSC_E_NULL;
   if (!osc::attn_tree_plan) return OSC_E_DEVICE;
-  *bytes = S == 0 || R == 0 ? 0 : osc::attn_tree_plan(R, HQ, HKV, D, N).ws_bytes;
+  *bytes = S == 0 || R == 0 ? 0 : osc::attn_tree_plan(HQ, HKV, D, N).ws_bytes;
   return OSC_OK;
 }
 
@@ -484,7 +484,7 @@ osc_status osc_attn_tree(const void* Q, const void* KC, const void* VC, int S, i
   if (S == 0 || R == 0) return OSC_OK;
   if (!Q || !KC || !VC || !TABLE || !CU || !KV || !MASK || !O) return OSC_E_NULL;
   if (!osc::attn_tree_plan || !osc::launch_attn_tree) return OSC_E_DEVICE;
-  const osc::TreePlan p = osc::attn_tree_plan(R, HQ, HKV, D, N);
+  const osc::TreePlan p = osc::attn_tree_plan(HQ, HKV, D, N);
   if (p.ws_bytes > 0 && !WS) return OSC_E_NULL;
   if (ws_bytes < p.ws_bytes) return OSC_E_SHAPE;
   if (!aligned16(Q) || !aligned16(KC) || !aligned16(VC) || !aligned16(O) || !aligned16(WS) || !aligned4(TABLE) ||

@@ -13,6 +13,8 @@ namespace {
 
 typedef unsigned long long u64;
 
+constexpr int kSmallRows = 16;
+
 // A bit pattern over the 16 lanes of a row
 __device__ __forceinline__ int or_row(int v) {
   v |= __builtin_amdgcn_update_dpp(0, v, 0xB1, 0xF, 0xF, false);
@@ -22,10 +24,10 @@ __device__ __forceinline__ int or_row(int v) {
   return v;
 }
 
-// ------------------------------------------------------------------ tiles of up to 64 rows
-// RB blocks of 16 rows; the four wavefronts take 32 keys each in turn, straight from memory into the registers that the
-// products want, every byte once, and are merged at the end.
-template <int D, int RB>
+// ------------------------------------------------------------------ tiles of up to 16 rows
+// The four wavefronts take 32 keys each in turn, straight from memory into the registers that the products want, every byte
+// once, and are merged at the end.
+template <int D>
 __device__ __forceinline__ void tree_tile(const TreeArgs& a, const Tile& t, int h, float* lds) {
   constexpr int DK = D / 32, DB = D / 16;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -33,32 +35,24 @@ __device__ __forceinline__ void tree_tile(const TreeArgs& a, const Tile& t, int 
   const int g = a.g;
   const __bf16* Kc = static_cast<const __bf16*>(a.KC);
   const __bf16* Vc = static_cast<const __bf16*>(a.VC);
-  const int nb = RB == 1 ? 1 : t.rows - t.row0 >= 16 * RB ? RB : (t.rows - t.row0 + 15) >> 4;  // blocks with rows
-  v8bf q[RB][DK];
-  u64 word[RB];  // the row's mask (a tile of so few rows has nodes of one word)
+  const int row = t.row0 + col, tok = row / g;
+  const bool live = row < t.rows;
+  const u64 word = live ? a.MASK[(long)(t.tok0 + tok) * a.W] : 0;  // (a tile of so few rows has nodes of one word)
+  v8bf q[DK];
 #pragma unroll
-  for (int b = 0; b < RB; ++b) {
-    const int row = t.row0 + 16 * b + col, tok = row / g;
-    const bool live = row < t.rows;
-    word[b] = live ? a.MASK[(long)(t.tok0 + tok) * a.W] : 0;
-    const long out_row = (long)(t.tok0 + tok) * a.HQ + h * g + (row - tok * g);
+  for (int s = 0; s < DK; ++s) {
 #pragma unroll
-    for (int s = 0; s < DK; ++s) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) q[b][s][i] = (__bf16)0.0f;
-      if (live) q[b][s] = *reinterpret_cast<const v8bf*>(static_cast<const __bf16*>(a.Q) + out_row * D + s * 32 + grp * 8);
-    }
+    for (int i = 0; i < 8; ++i) q[s][i] = (__bf16)0.0f;
+    if (live)
+      q[s] = *reinterpret_cast<const v8bf*>(static_cast<const __bf16*>(a.Q) + ((long)(t.tok0 + tok) * a.HQ + h * g + (row - tok * g)) * D + s * 32 +
+                                            grp * 8);
   }
   const int lo = 2 * t.lo, hi = clampi((t.kv + 31) >> 5, lo, 2 * t.hi);  // steps of 32 keys
 
-  v4f o[RB][DB];
-  float m[RB], mc[RB], l[RB];
+  v4f o[DB];
 #pragma unroll
-  for (int b = 0; b < RB; ++b) {
-#pragma unroll
-    for (int d = 0; d < DB; ++d) o[b][d] = v4f{0, 0, 0, 0};
-    m[b] = neg_inf(), mc[b] = 0.0f, l[b] = 0.0f;
-  }
+  for (int d = 0; d < DB; ++d) o[d] = v4f{0, 0, 0, 0};
+  float m = neg_inf(), mc = 0.0f, l = 0.0f;
   const float c = a.scale_log2;
   // the pages of the wavefront's next 32 steps, a run of 16 keys a lane (a page holds at least one)
   int ids = 0;
@@ -82,11 +76,17 @@ __device__ __forceinline__ void tree_tile(const TreeArgs& a, const Tile& t, int 
     }
 #pragma unroll
     for (int d = 0; d < DB; ++d) vf[d] = *reinterpret_cast<const v8bf*>(vp + ((long)(16 * d) << a.sh));
-    const bool masked = !whole || k0 + 32 > t.first;
-    int there = 255, bad = 0;  // which of the lane's keys k0 + 8 grp .. exist, and have a value that is not finite
-    if (masked) {
-      const int nv = idl < 0 ? 0 : clampi(t.kv - (k0 + 8 * grp), 0, 8);
-      there = (1 << nv) - 1;
+    v4f sc[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      sc[x] = v4f{0, 0, 0, 0};
+#pragma unroll
+      for (int s = 0; s < DK; ++s) sc[x] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf[x][s], q[s], sc[x], 0, 0, 0);
+    }
+    // scores of keys k0 + 8 grp + 4 x + i; the masked ones are selected away, whatever they hold
+    if (!whole || k0 + 32 > t.first) {
+      const int nv = idl < 0 ? 0 : clampi(t.kv - (k0 + 8 * grp), 0, 8), there = (1 << nv) - 1;  // which of the lane's keys exist
+      int bad = 0;
 #pragma unroll
       for (int d = 0; d < DB; ++d) {  // 0 * NaN is not 0: such values go, and rows that see the key become NaN by its score
         const v4i w = __builtin_bit_cast(v4i, vf[d]);
@@ -95,110 +95,92 @@ __device__ __forceinline__ void tree_tile(const TreeArgs& a, const Tile& t, int 
         vf[d] = __builtin_bit_cast(v8bf, without(w, f | (there ^ 255)));
       }
       bad = or_row(bad);
-    }
-#pragma unroll
-    for (int b = 0; b < RB; ++b) {
-      if (b >= nb) break;
-      v4f sc[2];
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        sc[x] = v4f{0, 0, 0, 0};
-#pragma unroll
-        for (int s = 0; s < DK; ++s) sc[x] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf[x][s], q[b][s], sc[x], 0, 0, 0);
-      }
-      // scores of keys k0 + 8 grp + 4 x + i; the masked ones are selected away, whatever they hold
-      if (masked) {
-        const int j0 = k0 + 8 * grp - t.first;  // of the lane's first key among the new ones
-        const int see = (int)(j0 >= 64 ? 0 : j0 >= 0 ? word[b] >> j0 : j0 <= -8 ? 255 : word[b] << -j0 | ((1 << -j0) - 1)) & there;
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if (((see & bad) >> (4 * x + i)) & 1) sc[x][i] = __builtin_nanf("");
-            if (!((see >> (4 * x + i)) & 1)) sc[x][i] = neg_inf();
-          }
-      }
-      float mx = neg_inf();
-#pragma unroll
-      for (int x = 0; x < 2; ++x)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) mx = fmaxf(mx, sc[x][i]);
-      if (__any(mx * c > mc[b] + kSlack || (m[b] == neg_inf() && mx > neg_inf()))) {
-        const float mn = fmaxf(m[b], max_groups(mx));
-        const float ms = mn == neg_inf() ? 0.0f : mn;
-        const float f = __builtin_amdgcn_exp2f(m[b] * c - ms * c);
-        l[b] *= f;
-#pragma unroll
-        for (int d = 0; d < DB; ++d) o[b][d] *= f;
-        m[b] = mn;
-        mc[b] = ms * c;
-      }
-      v8bf p, rest;  // the weights, and what their rounding leaves out
+      const int j0 = k0 + 8 * grp - t.first;  // of the lane's first key among the new ones
+      const int see = (int)(j0 >= 64 ? 0 : j0 >= 0 ? word >> j0 : j0 <= -8 ? 255 : word << -j0 | ((1 << -j0) - 1)) & there;
 #pragma unroll
       for (int x = 0; x < 2; ++x)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[x][i], c, -mc[b]));
-          l[b] += e;
-          p[4 * x + i] = (__bf16)e;
-          rest[4 * x + i] = (__bf16)(e - (float)p[4 * x + i]);
+          if (((see & bad) >> (4 * x + i)) & 1) sc[x][i] = __builtin_nanf("");
+          if (!((see >> (4 * x + i)) & 1)) sc[x][i] = neg_inf();
         }
+    }
+    float mx = neg_inf();
 #pragma unroll
-      for (int d = 0; d < DB; ++d) {
-        o[b][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf[d], p, o[b][d], 0, 0, 0);
-        o[b][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf[d], rest, o[b][d], 0, 0, 0);
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) mx = fmaxf(mx, sc[x][i]);
+    if (__any(mx * c > mc + kSlack || (m == neg_inf() && mx > neg_inf()))) {
+      const float mn = fmaxf(m, max_groups(mx));
+      const float ms = mn == neg_inf() ? 0.0f : mn;
+      const float f = __builtin_amdgcn_exp2f(m * c - ms * c);
+      l *= f;
+#pragma unroll
+      for (int d = 0; d < DB; ++d) o[d] *= f;
+      m = mn;
+      mc = ms * c;
+    }
+    v8bf p, rest;  // the weights, and what their rounding leaves out
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[x][i], c, -mc));
+        l += e;
+        p[4 * x + i] = (__bf16)e;
+        rest[4 * x + i] = (__bf16)(e - (float)p[4 * x + i]);
       }
+#pragma unroll
+    for (int d = 0; d < DB; ++d) {
+      o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf[d], p, o[d], 0, 0, 0);
+      o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf[d], rest, o[d], 0, 0, 0);
     }
   }
-  // merge the wavefronts, a block of 16 rows at a time: m, l and O^T of each through LDS
+  l += __shfl_xor(l, 16);
+  l += __shfl_xor(l, 32);
+  // merge the wavefronts: m, l and O^T of each through LDS
   float* ml = lds;                   // [4][2][16]
   float* ob = lds + 128;             // [4][16][D + 4]
   constexpr int PT = 16 * D / 256;  // values a thread joins
   const int orow = threadIdx.x / (D / PT), d0 = (threadIdx.x % (D / PT)) * PT;
+  __syncthreads();  // the tile before is merged
+  if (grp == 0) ml[wave * 32 + col] = m, ml[wave * 32 + 16 + col] = l;
 #pragma unroll
-  for (int b = 0; b < RB; ++b) {
-    if (b >= nb) break;
-    l[b] += __shfl_xor(l[b], 16);
-    l[b] += __shfl_xor(l[b], 32);
-    __syncthreads();  // the block before is merged
-    if (grp == 0) ml[wave * 32 + col] = m[b], ml[wave * 32 + 16 + col] = l[b];
+  for (int d = 0; d < DB; ++d) *reinterpret_cast<v4f*>(ob + (wave * 16 + col) * (D + 4) + 16 * d + 4 * grp) = o[d];
+  __syncthreads();
+  float mm = neg_inf();
 #pragma unroll
-    for (int d = 0; d < DB; ++d) *reinterpret_cast<v4f*>(ob + (wave * 16 + col) * (D + 4) + 16 * d + 4 * grp) = o[b][d];
-    __syncthreads();
-    float mm = neg_inf();
+  for (int w = 0; w < 4; ++w) mm = fmaxf(mm, ml[w * 32 + orow]);
+  const float ms = mm == neg_inf() ? 0.0f : mm;
+  float ll = 0.0f, acc[PT];
 #pragma unroll
-    for (int w = 0; w < 4; ++w) mm = fmaxf(mm, ml[w * 32 + orow]);
-    const float ms = mm == neg_inf() ? 0.0f : mm;
-    float ll = 0.0f, acc[PT];
+  for (int i = 0; i < PT; ++i) acc[i] = 0.0f;
 #pragma unroll
-    for (int i = 0; i < PT; ++i) acc[i] = 0.0f;
+  for (int w = 0; w < 4; ++w) {
+    const float f = __builtin_amdgcn_exp2f((ml[w * 32 + orow] - ms) * c);
+    ll += f * ml[w * 32 + 16 + orow];
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      const float f = __builtin_amdgcn_exp2f((ml[w * 32 + orow] - ms) * c);
-      ll += f * ml[w * 32 + 16 + orow];
+    for (int i = 0; i < PT; ++i) acc[i] += f * ob[(w * 16 + orow) * (D + 4) + d0 + i];
+  }
+  const int r = t.row0 + orow;
+  if (r >= t.rows) return;
+  if (t.part < 0) {
+    const int tk = r / g;
+    const long at = (long)(t.tok0 + tk) * a.HQ + h * g + (r - tk * g);
+    const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;  // no key: zeros
 #pragma unroll
-      for (int i = 0; i < PT; ++i) acc[i] += f * ob[(w * 16 + orow) * (D + 4) + d0 + i];
+    for (int i = 0; i < PT; i += 4) {
+      v4bf b;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) b[j] = (__bf16)(acc[i + j] * inv);
+      *reinterpret_cast<v4bf*>(static_cast<__bf16*>(a.O) + at * D + d0 + i) = b;
     }
-    const int r = t.row0 + 16 * b + orow;
-    if (r >= t.rows) continue;
-    if (t.part < 0) {
-      const int tk = r / g;
-      const long at = (long)(t.tok0 + tk) * a.HQ + h * g + (r - tk * g);
-      const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;  // no key: zeros
+  } else {
+    const long at = t.part + orow;
 #pragma unroll
-      for (int i = 0; i < PT; i += 4) {
-        v4bf w4;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) w4[j] = (__bf16)(acc[i + j] * inv);
-        *reinterpret_cast<v4bf*>(static_cast<__bf16*>(a.O) + at * D + d0 + i) = w4;
-      }
-    } else {
-      const long at = t.part + 16 * b + orow;
-#pragma unroll
-      for (int i = 0; i < PT; i += 4)
-        *reinterpret_cast<v4f*>(a.PO + at * D + d0 + i) = v4f{acc[i], acc[i + 1], acc[i + 2], acc[i + 3]};
-      if (d0 == 0) *reinterpret_cast<float2*>(a.PM + at * 2) = float2{ms * c, ll};
-    }
+    for (int i = 0; i < PT; i += 4)
+      *reinterpret_cast<v4f*>(a.PO + at * D + d0 + i) = v4f{acc[i], acc[i + 1], acc[i + 2], acc[i + 3]};
+    if (d0 == 0) *reinterpret_cast<float2*>(a.PM + at * 2) = float2{ms * c, ll};
   }
 }
 
@@ -321,10 +303,10 @@ __device__ __forceinline__ void each_tree_tile(const TreeArgs& a, Body body) {
   }
 }
 
-template <int D, int RB>
-__global__ __launch_bounds__(256, RB > 2 && D == 128 ? 1 : 2) void k_attn_tree(TreeArgs a) {
+template <int D>
+__global__ __launch_bounds__(256, 2) void k_attn_tree_small(TreeArgs a) {
   __shared__ __align__(16) float lds[128 + 4 * 16 * (D + 4)];
-  each_tree_tile<16 * RB>(a, [&](const Tile& t, int h) { tree_tile<D, RB>(a, t, h, lds); });
+  each_tree_tile<kSmallRows>(a, [&](const Tile& t, int h) { tree_tile<D>(a, t, h, lds); });
 }
 
 template <int D>
@@ -432,13 +414,14 @@ __global__ __launch_bounds__(512) void k_attn_tree_join(TreeArgs a) {
 
 }  // namespace
 
-TreePlan attn_tree_plan(int R, int HQ, int HKV, int D, int N) {
+// Small tiles where a tree's rows fit into one.  (64 trees of 4 nodes over 2000 keys: 95 us, 102 in large tiles; of 8 nodes, whose tiles would be
+// two: 102 in large ones, 99 in a third kernel with tiles of 32 rows, which took 96 where large ones take 91, see attn_r32_n8, and was not kept.)
+TreePlan attn_tree_plan(int HQ, int HKV, int D, int N) {
   TreePlan p;
-  (void)R;
   p.N = N;
-  const int rows = N * (HQ / HKV);
-  p.rows = rows <= 16 ? 16 : rows <= 32 ? 32 : kLargeRows;
-  p.target = ((p.rows > 32 ? 1 : 2) * kCUs + HKV - 1) / HKV;  // workgroups that run at once
+  const bool small = N * (HQ / HKV) <= kSmallRows;
+  p.rows = small ? kSmallRows : kLargeRows;
+  p.target = ((small ? 2 : 1) * kCUs + HKV - 1) / HKV;  // workgroups that run at once
   const long kept = (long)HKV * p.target * 2 * p.rows;
   p.ws_bytes = kept * (D + 2) * 4 + (long)HKV * p.target * (long)sizeof(int4);
   return p;
@@ -454,7 +437,7 @@ static hipError_t launch_rows(const TreeArgs& a, int N, hipStream_t st) {
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(k_attn_tree_large<D>, dim3(grid), dim3(512), bytes, st, a);
   } else {
-    hipLaunchKernelGGL((k_attn_tree<D, ROWS / 16>), dim3(grid), dim3(256), 0, st, a);
+    hipLaunchKernelGGL(k_attn_tree_small<D>, dim3(grid), dim3(256), 0, st, a);
   }
   // the 64 pieces of a tile that a wavefront joins; no more rows than the call has tokens
   const long most = ((long)a.S * a.g + 31) / 32 * 32, pieces = (most < ROWS ? most : ROWS) * (D / 4) / 64;
@@ -471,7 +454,7 @@ static hipError_t launch_rows(const TreeArgs& a, int N, hipStream_t st) {
 
 template <int D>
 static hipError_t launch_d(const TreeArgs& a, const TreePlan& p, hipStream_t st) {
-  return p.rows == 16 ? launch_rows<D, 16>(a, p.N, st) : p.rows == 32 ? launch_rows<D, 32>(a, p.N, st) : launch_rows<D, kLargeRows>(a, p.N, st);
+  return p.rows == kSmallRows ? launch_rows<D, kSmallRows>(a, p.N, st) : launch_rows<D, kLargeRows>(a, p.N, st);
 }
 
 hipError_t launch_attn_tree(const TreeArgs& a, int D, const TreePlan& p, hipStream_t st) {

@@ -159,11 +159,11 @@ OSC_STEP hipError_t launch_attn(const AttnArgs& a, int D, const AttnPlan& p, hip
 // Attention with a mask among a request's new tokens (osc_attn_tree): MASK [S][W].
 struct TreePlan {
   int N;         // nodes of a tree, at most
-  int rows;      // of a tile: 16, 32 or 256
+  int rows;      // of a tile: 16 or 256
   int target;    // workgroups for each key head
   long ws_bytes;
 };
-OSC_STEP TreePlan attn_tree_plan(int R, int HQ, int HKV, int D, int N);
+OSC_STEP TreePlan attn_tree_plan(int HQ, int HKV, int D, int N);
 struct TreeArgs : AttnArgs {
   const unsigned long long* MASK;
   int W;
