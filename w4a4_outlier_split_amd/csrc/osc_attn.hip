@@ -44,165 +44,10 @@
 namespace osc {
 namespace {
 
-constexpr int kSmallRows = 16;
 constexpr int kMaxCuts = 61;    // of one tile: its parts, two more at most, are the lanes of the join
 // Keys that a workgroup's part has at least.  (A prompt of 300 cut at 64, 128, 256: 24, 30, 38 us; 200 tokens on one key
 // head behind 800: 35, 31, 34.)
 constexpr int kMinKeys = 128;
-
-// ------------------------------------------------------------------ small tiles
-// Rows are the query heads of a token (and the next tokens'), so a decode with 4 heads to a key head uses 4 of 16:
-// the products are idle anyway where every key is read once.  No LDS on the way: a key's row and a channel's run of
-// keys are 16-byte pieces in the very lanes that the products want, and four wavefronts with a step each in flight
-// and 512 workgroups cover the latency.  (64 decodes: 284 us with pages looked up in the step, 191 so, 5.6 TB/s.)
-template <int D>
-__device__ __forceinline__ void small_tile(const AttnArgs& a, const Tile& t, int h, float* lds) {
-  constexpr int DK = D / 32, DB = D / 16;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int col = lane & 15, grp = lane >> 4;
-  const int g = a.g;
-  const __bf16* Kc = static_cast<const __bf16*>(a.KC);
-  const __bf16* Vc = static_cast<const __bf16*>(a.VC);
-  const int row = t.row0 + col;
-  const bool live = row < t.rows;
-  const int tok = row / g;
-  const long out_row = (long)(t.tok0 + tok) * a.HQ + h * g + (row - tok * g);
-  v8bf q[DK];
-#pragma unroll
-  for (int s = 0; s < DK; ++s) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) q[s][i] = (__bf16)0.0f;
-    if (live) q[s] = *reinterpret_cast<const v8bf*>(static_cast<const __bf16*>(a.Q) + out_row * D + s * 32 + grp * 8);
-  }
-  const int last = live ? t.first + tok : -1;  // the last key of the lane's row
-  const int tok_end = ((t.row0 + 16 < t.rows ? t.row0 + 16 : t.rows) - 1) / g;
-  const int kend = clampi(t.first + tok_end + 1, 0, t.kv);
-  const int lo = 2 * t.lo, hi = clampi((kend + 31) >> 5, lo, 2 * t.hi);  // steps of 32 keys
-
-  v4f o[DB];
-#pragma unroll
-  for (int d = 0; d < DB; ++d) o[d] = v4f{0, 0, 0, 0};
-  float m = neg_inf(), mc = 0.0f, l = 0.0f;
-  const float c = a.scale_log2;
-  // the pages of the wavefront's next 32 steps, a run of 16 keys a lane (a page holds at least one)
-  int ids = 0;
-  for (int st = lo + wave, n = 0; st < hi; st += 4, ++n) {
-    const int k0 = st * 32;
-    if ((n & 31) == 0) ids = page_of(a, t, k0 + (lane >> 1) * 128 + (lane & 1) * 16);
-    const int id0 = __builtin_amdgcn_readlane(ids, 2 * (n & 31)), id1 = __builtin_amdgcn_readlane(ids, 2 * (n & 31) + 1);
-    const bool whole = k0 + 32 <= t.kv && id0 >= 0 && id1 >= 0;
-    const int idl = (grp & 2) ? id1 : id0;  // V's keys 8 * grp ..
-    const int u = k0 + (grp & 2) * 8;
-    const __bf16* vp = Vc + block_at<D>(a, idl < 0 ? 0 : idl, h) + ((long)col << a.sh) + (u & a.mask) + (grp & 1) * 8;
-    v8bf kf[2][DK], vf[DB];
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int kr = 8 * (col >> 2) + 4 * x + (col & 3);  // the key (of 32) in row col of score tile x
-      const int id = kr < 16 ? id0 : id1;
-      const int uk = k0 + (kr & 16);
-      const __bf16* kp = Kc + block_at<D>(a, id < 0 ? 0 : id, h) + (long)((uk & a.mask) + (kr & 15)) * D + grp * 8;
-#pragma unroll
-      for (int s = 0; s < DK; ++s) kf[x][s] = *reinterpret_cast<const v8bf*>(kp + s * 32);
-    }
-#pragma unroll
-    for (int d = 0; d < DB; ++d) vf[d] = *reinterpret_cast<const v8bf*>(vp + ((long)(16 * d) << a.sh));
-    v4f sc[2];
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      sc[x] = v4f{0, 0, 0, 0};
-#pragma unroll
-      for (int s = 0; s < DK; ++s) sc[x] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf[x][s], q[s], sc[x], 0, 0, 0);
-    }
-    // scores of keys k0 + 8 grp + 4 x + i; the masked ones are selected away, whatever they hold
-    const int limit = idl < 0 ? -1 : last;
-    float mx = neg_inf();
-#pragma unroll
-    for (int x = 0; x < 2; ++x)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (k0 + 8 * grp + 4 * x + i > limit) sc[x][i] = neg_inf();
-        mx = fmaxf(mx, sc[x][i]);
-      }
-    if (!whole) {  // V of keys that do not exist may hold anything, and 0 * NaN is not 0
-      const int nv = idl < 0 ? 0 : t.kv - (k0 + 8 * grp);
-#pragma unroll
-      for (int d = 0; d < DB; ++d)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) vf[d][i] = i < nv ? vf[d][i] : (__bf16)0.0f;
-    }
-    if (__any(mx * c > mc + kSlack || (m == neg_inf() && mx > neg_inf()))) {
-      const float mn = fmaxf(m, max_groups(mx));
-      const float ms = mn == neg_inf() ? 0.0f : mn;
-      const float f = __builtin_amdgcn_exp2f(m * c - ms * c);
-      l *= f;
-#pragma unroll
-      for (int d = 0; d < DB; ++d) o[d] *= f;
-      m = mn;
-      mc = ms * c;
-    }
-    v8bf p, rest;  // the weights, and what their rounding leaves out
-#pragma unroll
-    for (int x = 0; x < 2; ++x)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[x][i], c, -mc));
-        l += e;
-        p[4 * x + i] = (__bf16)e;
-        rest[4 * x + i] = (__bf16)(e - (float)p[4 * x + i]);
-      }
-#pragma unroll
-    for (int d = 0; d < DB; ++d) {
-      o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf[d], p, o[d], 0, 0, 0);
-      o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf[d], rest, o[d], 0, 0, 0);
-    }
-  }
-  l += __shfl_xor(l, 16);
-  l += __shfl_xor(l, 32);
-  // merge the wavefronts: m, l and O^T of each through LDS
-  float* ml = lds;                   // [4][2][16]
-  float* ob = lds + 128;             // [4][16][D + 4]
-  __syncthreads();  // the tile before is merged
-  if (grp == 0) ml[wave * 32 + col] = m, ml[wave * 32 + 16 + col] = l;
-#pragma unroll
-  for (int d = 0; d < DB; ++d) *reinterpret_cast<v4f*>(ob + (wave * 16 + col) * (D + 4) + 16 * d + 4 * grp) = o[d];
-  __syncthreads();
-  constexpr int PT = 16 * D / 256;  // values a thread joins
-  const int orow = threadIdx.x / (D / PT), d0 = (threadIdx.x % (D / PT)) * PT;
-  float mm = neg_inf();
-#pragma unroll
-  for (int w = 0; w < 4; ++w) mm = fmaxf(mm, ml[w * 32 + orow]);
-  const float ms = mm == neg_inf() ? 0.0f : mm;
-  float ll = 0.0f, acc[PT];
-#pragma unroll
-  for (int i = 0; i < PT; ++i) acc[i] = 0.0f;
-#pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    const float f = __builtin_amdgcn_exp2f((ml[w * 32 + orow] - ms) * c);
-    ll += f * ml[w * 32 + 16 + orow];
-#pragma unroll
-    for (int i = 0; i < PT; ++i) acc[i] += f * ob[(w * 16 + orow) * (D + 4) + d0 + i];
-  }
-  const int r = t.row0 + orow;
-  if (r >= t.rows) return;
-  if (t.part < 0) {
-    const int tk = r / g;
-    const long at = (long)(t.tok0 + tk) * a.HQ + h * g + (r - tk * g);
-    const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;  // no key: zeros
-#pragma unroll
-    for (int i = 0; i < PT; i += 4) {
-      v4bf b;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) b[j] = (__bf16)(acc[i + j] * inv);
-      *reinterpret_cast<v4bf*>(static_cast<__bf16*>(a.O) + at * D + d0 + i) = b;
-    }
-  } else {
-    const long at = t.part + orow;
-#pragma unroll
-    for (int i = 0; i < PT; i += 4)
-      *reinterpret_cast<v4f*>(a.PO + at * D + d0 + i) = v4f{acc[i], acc[i + 1], acc[i + 2], acc[i + 3]};
-    if (d0 == 0) *reinterpret_cast<float2*>(a.PM + at * 2) = float2{ms * c, ll};
-  }
-}
 
 // ------------------------------------------------------------------ the cuts
 // The tiles of ROWS rows of a request and their lengths: tile i sees the keys up to its last token, base + (i +
@@ -424,7 +269,7 @@ __device__ __forceinline__ void each_tile(const AttnArgs& a, Body body) {
 template <int D>
 __global__ __launch_bounds__(256, 2) void k_attn_small(AttnArgs a) {
   __shared__ __align__(16) float lds[128 + 4 * 16 * (D + 4)];
-  each_tile<kSmallRows, kCut>(a, [&](const Tile& t, int h) { small_tile<D>(a, t, h, lds); });
+  each_tile<kSmallRows, kCut>(a, [&](const Tile& t, int h) { small_tile<D, false>(a, t, h, lds); });
 }
 
 // Heads of 64 need half the LDS and may have two workgroups a CU, if 128 registers do.  (8192 tokens in a table of 40960 keys:

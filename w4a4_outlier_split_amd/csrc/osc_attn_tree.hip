@@ -13,177 +13,6 @@ namespace {
 
 typedef unsigned long long u64;
 
-constexpr int kSmallRows = 16;
-
-// A bit pattern over the 16 lanes of a row
-__device__ __forceinline__ int or_row(int v) {
-  v |= __builtin_amdgcn_update_dpp(0, v, 0xB1, 0xF, 0xF, false);
-  v |= __builtin_amdgcn_update_dpp(0, v, 0x4E, 0xF, 0xF, false);
-  v |= __builtin_amdgcn_update_dpp(0, v, 0x141, 0xF, 0xF, false);
-  v |= __builtin_amdgcn_update_dpp(0, v, 0x140, 0xF, 0xF, false);
-  return v;
-}
-
-// ------------------------------------------------------------------ tiles of up to 16 rows
-// The four wavefronts take 32 keys each in turn, straight from memory into the registers that the products want, every byte
-// once, and are merged at the end.
-template <int D>
-__device__ __forceinline__ void tree_tile(const TreeArgs& a, const Tile& t, int h, float* lds) {
-  constexpr int DK = D / 32, DB = D / 16;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int col = lane & 15, grp = lane >> 4;
-  const int g = a.g;
-  const __bf16* Kc = static_cast<const __bf16*>(a.KC);
-  const __bf16* Vc = static_cast<const __bf16*>(a.VC);
-  const int row = t.row0 + col, tok = row / g;
-  const bool live = row < t.rows;
-  const u64 word = live ? a.MASK[(long)(t.tok0 + tok) * a.W] : 0;  // (a tile of so few rows has nodes of one word)
-  v8bf q[DK];
-#pragma unroll
-  for (int s = 0; s < DK; ++s) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) q[s][i] = (__bf16)0.0f;
-    if (live)
-      q[s] = *reinterpret_cast<const v8bf*>(static_cast<const __bf16*>(a.Q) + ((long)(t.tok0 + tok) * a.HQ + h * g + (row - tok * g)) * D + s * 32 +
-                                            grp * 8);
-  }
-  const int lo = 2 * t.lo, hi = clampi((t.kv + 31) >> 5, lo, 2 * t.hi);  // steps of 32 keys
-
-  v4f o[DB];
-#pragma unroll
-  for (int d = 0; d < DB; ++d) o[d] = v4f{0, 0, 0, 0};
-  float m = neg_inf(), mc = 0.0f, l = 0.0f;
-  const float c = a.scale_log2;
-  // the pages of the wavefront's next 32 steps, a run of 16 keys a lane (a page holds at least one)
-  int ids = 0;
-  for (int st = lo + wave, n = 0; st < hi; st += 4, ++n) {
-    const int k0 = st * 32;
-    if ((n & 31) == 0) ids = page_of(a, t, k0 + (lane >> 1) * 128 + (lane & 1) * 16);
-    const int id0 = __builtin_amdgcn_readlane(ids, 2 * (n & 31)), id1 = __builtin_amdgcn_readlane(ids, 2 * (n & 31) + 1);
-    const bool whole = k0 + 32 <= t.kv && id0 >= 0 && id1 >= 0;
-    const int idl = (grp & 2) ? id1 : id0;  // V's keys 8 * grp ..
-    const int u = k0 + (grp & 2) * 8;
-    const __bf16* vp = Vc + block_at<D>(a, idl < 0 ? 0 : idl, h) + ((long)col << a.sh) + (u & a.mask) + (grp & 1) * 8;
-    v8bf kf[2][DK], vf[DB];
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int kr = 8 * (col >> 2) + 4 * x + (col & 3);  // the key (of 32) in row col of score tile x
-      const int id = kr < 16 ? id0 : id1;
-      const int uk = k0 + (kr & 16);
-      const __bf16* kp = Kc + block_at<D>(a, id < 0 ? 0 : id, h) + (long)((uk & a.mask) + (kr & 15)) * D + grp * 8;
-#pragma unroll
-      for (int s = 0; s < DK; ++s) kf[x][s] = *reinterpret_cast<const v8bf*>(kp + s * 32);
-    }
-#pragma unroll
-    for (int d = 0; d < DB; ++d) vf[d] = *reinterpret_cast<const v8bf*>(vp + ((long)(16 * d) << a.sh));
-    v4f sc[2];
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      sc[x] = v4f{0, 0, 0, 0};
-#pragma unroll
-      for (int s = 0; s < DK; ++s) sc[x] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf[x][s], q[s], sc[x], 0, 0, 0);
-    }
-    // scores of keys k0 + 8 grp + 4 x + i; the masked ones are selected away, whatever they hold
-    if (!whole || k0 + 32 > t.first) {
-      const int nv = idl < 0 ? 0 : clampi(t.kv - (k0 + 8 * grp), 0, 8), there = (1 << nv) - 1;  // which of the lane's keys exist
-      int bad = 0;
-#pragma unroll
-      for (int d = 0; d < DB; ++d) {  // 0 * NaN is not 0: such values go, and rows that see the key become NaN by its score
-        const v4i w = __builtin_bit_cast(v4i, vf[d]);
-        const int f = not_finite(w);
-        bad |= f & there;
-        vf[d] = __builtin_bit_cast(v8bf, without(w, f | (there ^ 255)));
-      }
-      bad = or_row(bad);
-      const int j0 = k0 + 8 * grp - t.first;  // of the lane's first key among the new ones
-      const int see = (int)(j0 >= 64 ? 0 : j0 >= 0 ? word >> j0 : j0 <= -8 ? 255 : word << -j0 | ((1 << -j0) - 1)) & there;
-#pragma unroll
-      for (int x = 0; x < 2; ++x)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (((see & bad) >> (4 * x + i)) & 1) sc[x][i] = __builtin_nanf("");
-          if (!((see >> (4 * x + i)) & 1)) sc[x][i] = neg_inf();
-        }
-    }
-    float mx = neg_inf();
-#pragma unroll
-    for (int x = 0; x < 2; ++x)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) mx = fmaxf(mx, sc[x][i]);
-    if (__any(mx * c > mc + kSlack || (m == neg_inf() && mx > neg_inf()))) {
-      const float mn = fmaxf(m, max_groups(mx));
-      const float ms = mn == neg_inf() ? 0.0f : mn;
-      const float f = __builtin_amdgcn_exp2f(m * c - ms * c);
-      l *= f;
-#pragma unroll
-      for (int d = 0; d < DB; ++d) o[d] *= f;
-      m = mn;
-      mc = ms * c;
-    }
-    v8bf p, rest;  // the weights, and what their rounding leaves out
-#pragma unroll
-    for (int x = 0; x < 2; ++x)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[x][i], c, -mc));
-        l += e;
-        p[4 * x + i] = (__bf16)e;
-        rest[4 * x + i] = (__bf16)(e - (float)p[4 * x + i]);
-      }
-#pragma unroll
-    for (int d = 0; d < DB; ++d) {
-      o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf[d], p, o[d], 0, 0, 0);
-      o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf[d], rest, o[d], 0, 0, 0);
-    }
-  }
-  l += __shfl_xor(l, 16);
-  l += __shfl_xor(l, 32);
-  // merge the wavefronts: m, l and O^T of each through LDS
-  float* ml = lds;                   // [4][2][16]
-  float* ob = lds + 128;             // [4][16][D + 4]
-  constexpr int PT = 16 * D / 256;  // values a thread joins
-  const int orow = threadIdx.x / (D / PT), d0 = (threadIdx.x % (D / PT)) * PT;
-  __syncthreads();  // the tile before is merged
-  if (grp == 0) ml[wave * 32 + col] = m, ml[wave * 32 + 16 + col] = l;
-#pragma unroll
-  for (int d = 0; d < DB; ++d) *reinterpret_cast<v4f*>(ob + (wave * 16 + col) * (D + 4) + 16 * d + 4 * grp) = o[d];
-  __syncthreads();
-  float mm = neg_inf();
-#pragma unroll
-  for (int w = 0; w < 4; ++w) mm = fmaxf(mm, ml[w * 32 + orow]);
-  const float ms = mm == neg_inf() ? 0.0f : mm;
-  float ll = 0.0f, acc[PT];
-#pragma unroll
-  for (int i = 0; i < PT; ++i) acc[i] = 0.0f;
-#pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    const float f = __builtin_amdgcn_exp2f((ml[w * 32 + orow] - ms) * c);
-    ll += f * ml[w * 32 + 16 + orow];
-#pragma unroll
-    for (int i = 0; i < PT; ++i) acc[i] += f * ob[(w * 16 + orow) * (D + 4) + d0 + i];
-  }
-  const int r = t.row0 + orow;
-  if (r >= t.rows) return;
-  if (t.part < 0) {
-    const int tk = r / g;
-    const long at = (long)(t.tok0 + tk) * a.HQ + h * g + (r - tk * g);
-    const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;  // no key: zeros
-#pragma unroll
-    for (int i = 0; i < PT; i += 4) {
-      v4bf b;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) b[j] = (__bf16)(acc[i + j] * inv);
-      *reinterpret_cast<v4bf*>(static_cast<__bf16*>(a.O) + at * D + d0 + i) = b;
-    }
-  } else {
-    const long at = t.part + orow;
-#pragma unroll
-    for (int i = 0; i < PT; i += 4)
-      *reinterpret_cast<v4f*>(a.PO + at * D + d0 + i) = v4f{acc[i], acc[i + 1], acc[i + 2], acc[i + 3]};
-    if (d0 == 0) *reinterpret_cast<float2*>(a.PM + at * 2) = float2{ms * c, ll};
-  }
-}
-
 // ------------------------------------------------------------------ the cuts
 // A request's tiles of ROWS rows, each as long as its keys (in steps of 64; 1 at least, so that rows without a key get their zeros).
 template <int ROWS>
@@ -306,7 +135,7 @@ __device__ __forceinline__ void each_tree_tile(const TreeArgs& a, Body body) {
 template <int D>
 __global__ __launch_bounds__(256, 2) void k_attn_tree_small(TreeArgs a) {
   __shared__ __align__(16) float lds[128 + 4 * 16 * (D + 4)];
-  each_tree_tile<kSmallRows>(a, [&](const Tile& t, int h) { tree_tile<D>(a, t, h, lds); });
+  each_tree_tile<kSmallRows>(a, [&](const Tile& t, int h) { small_tile<D, true>(a, t, h, lds); });
 }
 
 template <int D>
