@@ -55,7 +55,7 @@ __device__ __forceinline__ void each_tree_tile(const TreeArgs& a, Body body) {
   const int h = blockIdx.x % a.HKV, w = blockIdx.x / a.HKV;
   const int lane = threadIdx.x & 63;
   const int per = (a.R + 63) >> 6;
-  int r = 0, i = 0, parts = 1, over = 0;
+  int r = 0, i = 0, parts = 1, over = 0;  // over < parts <= 512: their products fit into 32 bits
   long begin = 0, first = 0, end = 0, each = 0, all;
   // A lane has `per` requests; where that is one, it keeps it, and nobody reads the lengths again.
   const int r0 = lane * per < a.R ? lane * per : a.R, r1 = r0 + per < a.R ? r0 + per : a.R;
@@ -77,7 +77,7 @@ __device__ __forceinline__ void each_tree_tile(const TreeArgs& a, Body body) {
     each = uniform(divide(all, parts));
     over = (int)(all - each * parts);
     if (w < parts && all > 0) {
-      first = each * w + (long)over * w / parts, end = each * (w + 1) + (long)over * (w + 1) / parts;
+      first = each * w + over * w / parts, end = each * (w + 1) + over * (w + 1) / parts;
       // the tile at `first`: its request, its number there, and where it begins
       const int src = __ffsll(__ballot(first < upto)) - 1;
       long from = upto - mine;
@@ -117,7 +117,7 @@ __device__ __forceinline__ void each_tree_tile(const TreeArgs& a, Body body) {
         ns = 1;
         for (int p0 = w + 1;; p0 += 64) {
           const int p = p0 + lane;
-          const int more = __popcll(__ballot(p < parts && each * p + (long)over * p / parts < begin + len));
+          const int more = __popcll(__ballot(p < parts && each * p + over * p / parts < begin + len));
           ns += more;
           if (more < 64) break;
         }
