@@ -270,3 +270,27 @@ def test_attn_tree_replayed():
         for p, out, *_ in ps:
             assert torch.equal(out.view(torch.int16), attend(p).view(torch.int16)), it
             check(p, out, what=it)
+
+
+@pytest.mark.parametrize("N,HQ,HKV", [(4, 4, 1), (64, 32, 8)])
+def test_attn_tree_idle_requests(N, HQ, HKV):
+    """Requests without a token among others, and no other at all: nothing of O is written for them."""
+    rng = np.random.default_rng(N)
+    for reqs in ([(50, 0)] * 70, [(50, 0)] * 70 + [(300, N)] + [(0, 0)] * 200, [(0, 0)]):
+        p = build([(c, tree_ref.tree(rng, n, "near")) for c, n in reqs], HQ, HKV, 128, 32, N, 6, pad=5)
+        check(p, attend(p))
+
+
+def test_attn_tree_on_another_stream():
+    rng = np.random.default_rng(8)
+    for N in (4, 40):
+        p = build([(700, tree_ref.tree(rng, N, "near")), (64, tree_ref.tree(rng, N, "near"))], 16, 4, 128, 64, N, 6)
+        p["dev"] = [torch.from_numpy(p["table"]).to(DEV), i32(p["cu"]), i32(p["kv"])]
+        want = attend(p)
+        ws = poisoned((osc.osc_attn_tree_workspace(p["S"], 2, 16, 4, 128, 64, p["MB"], N),), torch.uint8)
+        out = poisoned((p["S"], 16, 128), torch.bfloat16)
+        torch.cuda.synchronize()
+        side = torch.cuda.Stream()
+        attend(p, ws=ws, out=out, stream=side)
+        side.synchronize()
+        assert torch.equal(out.view(torch.int16), want.view(torch.int16))

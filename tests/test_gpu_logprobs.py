@@ -76,7 +76,9 @@ def check(x, dt, scale, M, K, pad, seed):
     size = y[torch.isfinite(y)].abs().max()
     eps, n = 2.0 ** -24, V / 256 + 22
     tol = eps * (n + 8 + 8 * size)
+    assert bool((ENT >= 0).all())
     if M:
+        assert bool((LP <= 0).all())
         want = torch.gather(y, 1, ids.clamp(0, V - 1).long()) - lse
         want[(ids < 0) | (ids >= V)] = -INF
         assert torch.equal(torch.isinf(LP), torch.isinf(want))
@@ -205,3 +207,37 @@ def test_logprobs_replayed():
         torch.cuda.synchronize()
         for a, b in zip(out, want):
             assert torch.equal(a, b)
+
+
+def test_logprobs_behind_32_bits():
+    """More than 2^32 bytes of logits: rows at both ends against 64 bits, all of them against rows with the same logits."""
+    V, S = 151936, 15000
+    few = torch.from_numpy(rows_of("normal", 8, V, 3)).to(DEV).bfloat16()
+    x = torch.empty((S, V), dtype=torch.bfloat16, device=DEV)
+    for s in range(0, S, 8):
+        x[s:s + 8] = few[:min(8, S - s)]
+    ids = torch.full((S, 1), V - 1, dtype=torch.int32, device=DEV)
+    LP, ENT, TV, TI = run(x, osc.OSC_Y_BF16, S, V, V, 1.0, ids, 3)
+    want = torch.log_softmax(few.double(), 1)
+    size = float(few.double().abs().max())
+    tol = 2.0 ** -24 * (V / 256 + 22 + 8 + 8 * size)
+    assert bool(((LP[:8, 0].double() - want[:, -1]).abs() <= tol).all())
+    for t in (LP, ENT, TV, TI):
+        for s in range(8):
+            assert bool((t[s::8] == t[s]).all())
+
+
+@pytest.mark.parametrize("S", [3, 300])
+def test_logprobs_on_another_stream(S):
+    V, K = 30001, 9
+    x = torch.from_numpy(rows_of("normal", S, V, 3)).to(DEV).bfloat16()
+    ids = torch.zeros((S, 1), dtype=torch.int32, device=DEV)
+    want = run(x, osc.OSC_Y_BF16, S, V, V, 1.0, ids, K)
+    out = [torch.zeros_like(t) for t in want]
+    ws = torch.zeros((max(osc.osc_logprobs_workspace(S, V, K), 16),), dtype=torch.uint8, device=DEV)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    osc.osc_logprobs(x, osc.OSC_Y_BF16, S, V, V, 1.0, ids, 1, K, *out, ws.data_ptr(), stream=side)
+    side.synchronize()
+    for a, b in zip(out, want):
+        assert torch.equal(a, b)

@@ -225,8 +225,10 @@ __device__ __forceinline__ void in_order(Lds<CAP>& s, int n, int K, Write write,
 
 __device__ __forceinline__ bool is_none(const Sum& s) { return !(s.l > 0.0f) || !(s.r < __builtin_inff()); }
 
+// (no probability is over 1, nor an entropy below 0, by rounding)
 __device__ __forceinline__ float logp(const Sum& s, float log2l, float x, float c) {
-  return (__builtin_fmaf(x, c, -base_of(s.r)) - log2l) * 0.6931471805599453f;
+  const float p = (__builtin_fmaf(x, c, -base_of(s.r)) - log2l) * 0.6931471805599453f;
+  return p > 0.0f ? 0.0f : p;
 }
 
 template <bool F32>
@@ -256,7 +258,7 @@ __device__ __forceinline__ void finish(const LogprobsArgs& a, int row, const Sum
     if (i >= kThreads) given = Given<F32>(a, row, i);
     a.LP[(long)row * a.M + i] = none ? nan : given.id < 0 ? neg_inf() : logp(s, log2l, given.x, c);
   }
-  if (a.ENT && threadIdx.x == 0) a.ENT[row] = none ? nan : (log2l - s.t / s.l) * 0.6931471805599453f;
+  if (a.ENT && threadIdx.x == 0) a.ENT[row] = none ? nan : fmaxf((log2l - s.t / s.l) * 0.6931471805599453f, 0.0f);
   if (a.K == 0) return;
   const long out = (long)row * a.K;
   in_order(
