@@ -156,25 +156,34 @@ __global__ __launch_bounds__(512) void k_attn_tree_join(TreeArgs a) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int h = blockIdx.x % a.HKV;
   int w = blockIdx.x / a.HKV;
+  int4 note;
   if constexpr (SHARE > 1) {
     constexpr int MOST = 2 * kCUs / 64;  // a lane's notes
-    int noted[MOST], left = w;
+    int4 noted[MOST];
+    int left = w;
 #pragma unroll
-    for (int i = 0; i < MOST; ++i) noted[i] = i * 64 + lane < a.target ? a.NOTE[h * a.target + i * 64 + lane].x : 0;
+    for (int i = 0; i < MOST; ++i) {
+      noted[i] = int4{0, 0, 0, 0};
+      if (i * 64 < a.target && i * 64 + lane < a.target) noted[i] = a.NOTE[h * a.target + i * 64 + lane];
+    }
     w = -1;
 #pragma unroll
     for (int i = 0; i < MOST; ++i) {
-      u64 has = __ballot(noted[i] > 0);
+      u64 has = __ballot(noted[i].x > 0);
       const int n = __popcll(has);
       if (w < 0 && left < n) {
         for (; left > 0; --left) has &= has - 1;
-        w = i * 64 + __ffsll(has) - 1;
+        const int src = __ffsll(has) - 1;
+        w = i * 64 + src;
+        note = int4{__builtin_amdgcn_readlane(noted[i].x, src), __builtin_amdgcn_readlane(noted[i].y, src),
+                    __builtin_amdgcn_readlane(noted[i].z, src), __builtin_amdgcn_readlane(noted[i].w, src)};
       }
       left -= n;
     }
     if (w < 0) return;
+  } else {
+    note = a.NOTE[h * a.target + w];
   }
-  const int4 note = a.NOTE[h * a.target + w];
   const int ns = __builtin_amdgcn_readfirstlane(note.x < a.target - w ? note.x : a.target - w);
   if (ns <= 0) return;
   // Which row of the tile, and which of its channels, the lane's piece holds: in order, or (tiles of 256 rows) 4 channels from 32 d + 8 i +
