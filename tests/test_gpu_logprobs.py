@@ -127,6 +127,13 @@ def test_logprobs_rows_in_one_part(kind, dt, V):
     assert torch.equal(TV[16::16], TV[:1].expand(TV[16::16].shape))  # rows that begin at the same place of 16 bytes are summed in the same order
 
 
+@pytest.mark.parametrize("kind", ["equal", "zeros", "up"])
+@pytest.mark.parametrize("dt,V", [(torch.bfloat16, 2047 * 8 + 2), (torch.bfloat16, 2047 * 8 + 9), (torch.float32, 2047 * 4 + 2), (torch.float32, 2047 * 4 + 5)])
+def test_logprobs_most_that_a_part_holds(kind, dt, V):
+    """rows that begin and end inside a vector, of 2047 whole ones: the most that are chosen from at once"""
+    check(rows_of(kind, 260, V, V), dt, 1.0, 2, 64, 1, V)
+
+
 @pytest.mark.parametrize("V", [1, 2, 7, 8, 9, 63, 64, 65, 255, 256, 2047, 2048, 2049, 4096, 4097, 16384, 16400])
 @pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
 def test_logprobs_vocabularies(V, dt):

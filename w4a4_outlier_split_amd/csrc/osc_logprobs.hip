@@ -6,12 +6,17 @@
 // Threads keep R, l and t of their own and move R where a value exceeds it by more than kSlack.
 //
 // The K largest come along.  They stand in the K vectors (of 16 bytes) whose largest values are the best, so vectors are noted, not
-// values: a comparison a vector, where it holds a list entry.  The first 8 vectors of each thread (one, where a part is short) give 256
-// maxima, whose K-th largest is a bound that at least K vectors reach.  From then on a vector that reaches the bound
-// is noted by its wavefront, in a list of its own in LDS, so that none waits for another: a few times K of a row in usual orders.
-// A list that is nearly full is cut to the vectors that reach a better bound.  At the end the best K vectors of all lists, and
-// seldom a few more, are read once more and their values put in order.  (Noting the values: 2048 rows of 151936, K = 5 and 64, 154 and
-// 250 us, see below.)
+// values: a comparison a vector, where it holds a list entry.  The first 8 vectors of each thread give 256 maxima, whose K-th largest
+// is a bound that at least K vectors reach.  From then on a vector that reaches the bound is noted by its wavefront, in a list of its
+// own in LDS, so that none waits for another: a few times K of a row in usual orders.  A list that is nearly full is cut to the
+// vectors that reach a better bound.  A part of fewer than 8 vectors a thread stays in registers, and is chosen from there.  At the
+// end the best K vectors, and seldom a few more, are read once more and their values put in order.  (Noting the values instead:
+// 2048 rows of 151936, K = 5 and 64, 154 and 250 us; vectors 117 and 131.)
+//
+// Many rows are bound by HBM: 2048 bf16 rows of 151936 with 5 alternatives take 117 us, 5.3 TB/s, 512 take 39, and the rounds' loads
+// are under way while the round before is summed up.  One row is bound by latency: 14.5 us, 8 for a part's loads, maxima and choice, one
+// behind the other, and 6.4 for the parts' join.  Equal logits, which reach every bound, are the slow order: 2048 rows of zeros 124 to 132 us,
+// one 27 to 37.
 #include "osc_internal.h"
 #include "osc_lanes.h"
 
@@ -25,9 +30,10 @@ constexpr int kThreads = 256;
 constexpr int kRound = 8;        // vectors of 16 bytes a thread and round
 constexpr int kList = 256;       // vectors that a wavefront notes
 constexpr int kCut = kList - 64; // from here on a vector of each lane may not find room
-constexpr int kVectors = 4 * kList, kValues = 8 * kThreads;
+constexpr int kHeld = (kRound + 1) * kThreads;  // vectors of a part that stays in registers, with the row's first and last; 8 values of 256 vectors
+static_assert(kHeld >= 4 * kList && kHeld >= 8 * kThreads, "the wavefronts' lists and the best vectors' values have room");
 constexpr int kParts = 64 * OSC_MAX_TOP;  // values of a row's parts
-constexpr float kSlack = 4.0f;
+constexpr float kSlack = 4.0f;  // (terms up to 2^4: the sums lose nothing by the factor)
 constexpr int kNone = 0x007FFFFF;  // the key of -inf
 
 // values in the order of unsigned numbers (no NaN; both zeros alike), and back
@@ -290,7 +296,7 @@ __host__ __device__ inline long record_bytes(int K) { return (long)sizeof(Record
 template <bool F32>
 __global__ __launch_bounds__(kThreads, 4) void k_logprobs(LogprobsArgs a) {
   constexpr int E = F32 ? 4 : 8;  // values of a vector
-  __shared__ Lds<(kValues > kVectors ? kValues : kVectors)> lds;
+  __shared__ Lds<kHeld> lds;
   const int row = blockIdx.x / a.chunks, chunk = blockIdx.x - row * a.chunks;
   const int tid = threadIdx.x;
   const uint8_t* x0 = static_cast<const uint8_t*>(a.X) + (long)row * a.ld * (F32 ? 4 : 2);
