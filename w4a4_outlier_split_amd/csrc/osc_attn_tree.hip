@@ -4,8 +4,15 @@
 //                                                        bits of MASK[t] name
 //
 // with the running maximum and sum, the transposed products and the layouts of osc_attn.hip.  A tree's rows all see the
-// context, which is nearly all of the keys: a tile's length is that of its request, and a mask is needed in the last
-// steps only.
+// context, which is nearly all of the keys: a tile's length is that of its request, and a mask is needed in the last steps only.
+//
+// Two kernels: tiles of 16 rows from registers where a tree's rows (nodes times the query heads of a key head) fit into one, tiles of 256
+// on the ring of keys in LDS otherwise, so that a request's keys are read from memory once.  Every row of tiles is cut evenly among as
+// many workgroups as run at once, since a step's few trees have no tiles to fill the card with; a second launch joins the cut ones.
+// Measured with 32 query and 8 key heads of 128, both launches: 8 nodes in each of 32 requests, 109 thousand keys, 96 us, bound by HBM
+// (441 MB, 4.8 TB/s); 64 nodes there 123, where the tiles' steps of 2 us run beside the same bytes and 35 MB of partial outputs are written
+// and read again; 256 nodes over 32700 keys 146, bound by the steps (2 us, of which the matrix unit works 0.85 to 1); 16 nodes over 4000 keys
+// 17, a chain of latencies: lengths and cuts 1.4, the request 0.8, pages, queries and masks 1.3, first keys 2.1, steps 4, stores 0.5, and two launches.
 #include "osc_attn_dev.h"
 
 namespace osc {
@@ -42,7 +49,7 @@ struct TreeRequest {
   }
 };
 
-// Steps that a workgroup's part has at least
+// Steps that a workgroup's part has at least: a part costs the join 2 to 3 us, a step 2
 constexpr int kMinSteps = 2;
 
 // Workgroup: key head h = blockIdx % HKV, part w = blockIdx / HKV of the row in which all tiles of the head stand, cut into equal
@@ -252,8 +259,9 @@ __global__ __launch_bounds__(512) void k_attn_tree_join(TreeArgs a) {
 
 }  // namespace
 
-// Small tiles where a tree's rows fit into one.  (64 trees of 4 nodes over 2000 keys: 95 us, 102 in large tiles; of 8 nodes, whose tiles would be
-// two: 102 in large ones, 99 in a third kernel with tiles of 32 rows, which took 96 where large ones take 91, see attn_r32_n8, and was not kept.)
+// Small tiles where a tree's rows fit into one.  (4 query heads to a key head, 64 trees over 2000 keys each: of 4 nodes 95 us, 102 in large tiles;
+// of 8 nodes, which would be two small tiles, 102 in large ones.  A third kernel, with tiles of 32 rows from registers, took 99 there, and 96 where large
+// tiles take 91, 32 trees of 8 nodes over 109 thousand keys: not kept.)
 TreePlan attn_tree_plan(int HQ, int HKV, int D, int N) {
   TreePlan p;
   p.N = N;
