@@ -73,6 +73,26 @@ struct Lds {
   u64 differ[4];
 };
 
+// Those of the threads' entries that reach `low` (> 0) behind the s.votes[0][0] that the list has, which count on.  (An atomic
+// addition for each lane: the compiler takes the lanes one by one, and one row with 64 alternatives 18.5 us.)
+template <int PER, int CAP>
+__device__ __forceinline__ void append(Lds<CAP>& s, const u64 (&e)[PER], u64 low) {
+  const int lane = threadIdx.x & 63;
+  u64 who[PER];
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) who[i] = __ballot(e[i] >= low), n += __popcll(who[i]);
+  if (n == 0) return;
+  int at = 0;
+  if (lane == 0) at = atomicAdd(&s.votes[0][0], n);
+  at = __builtin_amdgcn_readfirstlane(at);
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    if (e[i] >= low) s.list[at + __popcll(who[i] & ((1ull << lane) - 1))] = e[i];
+    at += __popcll(who[i]);
+  }
+}
+
 // Cuts the n entries of the list to the K best (n >= K); the worst of those.  All threads, behind a barrier.  Run where values are
 // alike, rows of zeros in a padded step for instance, so the bits that all entries share are left out.
 template <int CAP>
@@ -105,25 +125,24 @@ __device__ __attribute__((noinline)) u64 prune(Lds<CAP>& s, int n, int K) {
     if (s.votes[turn][0] + s.votes[turn][1] + s.votes[turn][2] + s.votes[turn][3] >= K) low = trial;
     turn ^= 1;  // (read ahead of the next barrier, written behind it)
   }
-  if (threadIdx.x == 0) s.votes[turn][0] = 0;
+  __syncthreads();  // (the votes are read)
+  if (threadIdx.x == 0) s.votes[0][0] = 0;
   __syncthreads();
-#pragma unroll
-  for (int i = 0; i < PER; ++i)
-    if (e[i] >= low && e[i] > 0) s.list[atomicAdd(&s.votes[turn][0], 1)] = e[i];
+  append(s, e, low > 0 ? low : 1);
   __syncthreads();
   return low;
 }
 
-// A key that at least K of the workgroup's values reach: the K-th largest of the threads' largest keys (0 if there are fewer).
-// BITS: how many of a key's upper bits count.  Every wavefront takes all 256 keys, four a lane, and settles a bit at a time.
-template <int BITS, int CAP>
+// A key that at least K of the workgroup's values reach: the K-th largest of the threads' largest keys (0 if there are fewer), of
+// which the upper 16 bits count.  Every wavefront takes all 256 keys, four a lane, and settles a bit at a time.
+template <int CAP>
 __device__ __forceinline__ unsigned reached(Lds<CAP>& s, int which, unsigned mine, int K) {
   s.top[which][threadIdx.x] = mine;
   __syncthreads();
   unsigned k[4], low = 0;
 #pragma unroll
   for (int j = 0; j < 4; ++j) k[j] = s.top[which][64 * j + (threadIdx.x & 63)];
-  for (int bit = 31; bit >= 32 - BITS; --bit) {
+  for (int bit = 31; bit >= 16; --bit) {
     const unsigned trial = low | 1u << bit;
     int n = 0;
 #pragma unroll
@@ -135,23 +154,14 @@ __device__ __forceinline__ unsigned reached(Lds<CAP>& s, int which, unsigned min
 
 // The best of the entries that the threads hold into the list, from its start: those whose key reaches a bound that K of
 // them do, K at least if there are as many, and seldom more than 256.  Returns their number, and the bound.  All threads.
-template <int BITS, int PER, int CAP>
+template <int PER, int CAP>
 __device__ __forceinline__ int gather(Lds<CAP>& s, const u64 (&e)[PER], int K, unsigned& bound) {
   u64 most = 0;
 #pragma unroll
   for (int i = 0; i < PER; ++i) most = most > e[i] ? most : e[i];
   if (threadIdx.x == 0) s.votes[0][0] = 0;
-  bound = reached<BITS>(s, 1, key_in(most), K);
-  const u64 low = bound > 0 ? (u64)bound << 32 : 1;
-  int mine = 0;
-#pragma unroll
-  for (int i = 0; i < PER; ++i) mine += e[i] >= low;
-  if (mine > 0) {
-    int at = atomicAdd(&s.votes[0][0], mine);
-#pragma unroll
-    for (int i = 0; i < PER; ++i)
-      if (e[i] >= low) s.list[at++] = e[i];
-  }
+  bound = reached(s, 1, key_in(most), K);
+  append(s, e, bound > 0 ? (u64)bound << 32 : 1);
   __syncthreads();
   const int n = s.votes[0][0];
   __syncthreads();
@@ -385,7 +395,7 @@ __global__ __launch_bounds__(kThreads, 4) void k_logprobs(LogprobsArgs a) {
   };
   // Rounds of vectors that are the row's throughout, the next one's asked for as this one's are done with; then what is left of such
   // vectors.  The row's first and last vector, if they are not, go to the threads 0 .. E - 1 and E .. 2 E - 1, a value each.
-  constexpr int STEP = kRound * kThreads, BITS = F32 ? 32 : 16;  // BITS: of a key, that differ
+  constexpr int STEP = kRound * kThreads;
   const int w0 = v0 > whole0 ? v0 : whole0, w1 = v1 < whole1 ? v1 : whole1;
   const int rounds = w1 > w0 ? (w1 - w0) / STEP : 0;
   const bool edges = v0 < w0 || v1 > w1;
@@ -404,7 +414,7 @@ __global__ __launch_bounds__(kThreads, 4) void k_logprobs(LogprobsArgs a) {
 #pragma unroll
     for (int u = 0; u < kRound; ++u) most[u] = add(q[u]), all = fmaxf(all, most[u]);
     if (a.K > 0) {
-      const unsigned low = reached<BITS>(lds, 0, key_of(all), a.K);
+      const unsigned low = reached(lds, 0, key_of(all), a.K);
       bound = low <= (unsigned)kNone ? neg_inf() : value_of(low);
     }
     const int more = rounds > 1 ? STEP : 0;
@@ -460,7 +470,7 @@ __global__ __launch_bounds__(kThreads, 4) void k_logprobs(LogprobsArgs a) {
 #pragma unroll
       for (int u = 0; u < kRound; ++u) e[u] = noted(most[u], v + u * kThreads);
       e[kRound] = noted(edge_most, edge);
-      n = gather<BITS>(lds, e, a.K, worst);
+      n = gather(lds, e, a.K, worst);
     } else {
 #pragma unroll
       for (int u = 0; u < kRound; ++u) note(most[u], v + u * kThreads);
@@ -471,7 +481,7 @@ __global__ __launch_bounds__(kThreads, 4) void k_logprobs(LogprobsArgs a) {
         const int j = (tid & 63) + 64 * i;
         e[i] = j < have ? list[j] : 0;
       }
-      n = gather<BITS>(lds, e, a.K, worst);
+      n = gather(lds, e, a.K, worst);
     }
     if (n > kThreads) {  // as many are alike
       worst = key_in(prune(lds, n, a.K));
@@ -482,20 +492,13 @@ __global__ __launch_bounds__(kThreads, 4) void k_logprobs(LogprobsArgs a) {
     const u4 best = load(at);
     if (tid == 0) lds.votes[0][0] = 0;
     u64 e[E];
-    int mine = 0;
 #pragma unroll
     for (int i = 0; i < E; ++i) {
       const float x = value(best, i);
       e[i] = x > neg_inf() && key_of(x) >= worst ? entry(key_of(x), at * E - skew + i) : 0;
-      mine += e[i] > 0;
     }
     __syncthreads();
-    if (mine > 0) {
-      int to = atomicAdd(&lds.votes[0][0], mine);
-#pragma unroll
-      for (int i = 0; i < E; ++i)
-        if (e[i] > 0) lds.list[to++] = e[i];
-    }
+    append(lds, e, 1);
     __syncthreads();
     n = lds.votes[0][0];
   }
@@ -533,7 +536,7 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_join(LogprobsArgs a) {
   const Given<F32> given(a, row, tid);
   s = join_all(s, lds);
   unsigned bound;
-  finish<F32>(a, row, s, given, lds, K > 0 ? gather<F32 ? 32 : 16>(lds, e, K, bound) : 0);
+  finish<F32>(a, row, s, given, lds, K > 0 ? gather(lds, e, K, bound) : 0);
 }
 
 }  // namespace
