@@ -406,33 +406,47 @@ __global__ __launch_bounds__(kThreads, 4) void k_logprobs(LogprobsArgs a) {
     if (e >= 0 && e < a.V) edge_value = logit<F32>(a, (long)row * a.ld + e);
   }
   int v = w0 + tid;
-  if (rounds > 0) {
-    u4 q[kRound];
-    float most[kRound], all = neg_inf();
+  u4 q[kRound];
+  auto ask = [&](bool rest) {  // the vectors from v on; what lies behind the last of the rest is not used
 #pragma unroll
-    for (int u = 0; u < kRound; ++u) q[u] = xv[v + u * kThreads];
+    for (int u = 0; u < kRound; ++u) {
+      const int x = v + u * kThreads;
+      q[u] = xv[rest && x >= w1 ? w1 - 1 : x];
+    }
+  };
+  if (rounds > 0) {
+    float most[kRound], all = neg_inf();
+    ask(false);
 #pragma unroll
     for (int u = 0; u < kRound; ++u) most[u] = add(q[u]), all = fmaxf(all, most[u]);
+    v += STEP;
+    if (rounds > 1) ask(false);
+    else ask(true);
     if (a.K > 0) {
       const unsigned low = reached(lds, 0, key_of(all), a.K);
       bound = low <= (unsigned)kNone ? neg_inf() : value_of(low);
     }
-    const int more = rounds > 1 ? STEP : 0;
 #pragma unroll
-    for (int u = 0; u < kRound; ++u) {
-      note(most[u], v + u * kThreads);
-      q[u] = xv[v + more + u * kThreads];
-    }
-    for (int r = 1; r < rounds; ++r) {
-      v += STEP;
-      const int next = r + 1 < rounds ? STEP : 0;
+    for (int u = 0; u < kRound; ++u) note(most[u], v - STEP + u * kThreads);
+    for (int r = 2; r < rounds; ++r) {
 #pragma unroll
       for (int u = 0; u < kRound; ++u) {
         note(add(q[u]), v + u * kThreads);
-        q[u] = xv[v + next + u * kThreads];
+        q[u] = xv[v + STEP + u * kThreads];
       }
+      v += STEP;
     }
-    v += STEP;
+    if (rounds > 1) {
+#pragma unroll
+      for (int u = 0; u < kRound; ++u) {
+        note(add(q[u]), v + u * kThreads);
+        const int x = v + STEP + u * kThreads;
+        q[u] = xv[x < w1 ? x : w1 - 1];
+      }
+      v += STEP;
+    }
+  } else if (w1 > w0) {
+    ask(true);
   }
   float edge_most = neg_inf();  // in the first of a vector's threads
   if (edges) {
@@ -446,19 +460,13 @@ __global__ __launch_bounds__(kThreads, 4) void k_logprobs(LogprobsArgs a) {
     if (rounds > 0) note(edge_most, edge);
   }
   float most[kRound];
-  {
-    u4 q[kRound];
-    const u4 none = {ninf, ninf, ninf, ninf};
 #pragma unroll
-    for (int u = 0; u < kRound; ++u) {
-      const int x = v + u * kThreads;
-      q[u] = none;
-      if (x < w1) q[u] = xv[x];
-    }
+  for (int u = 0; u < kRound; ++u) {
+    most[u] = neg_inf();
+    if (w0 + rounds * STEP + u * kThreads < w1) {  // (the same for all)
 #pragma unroll
-    for (int u = 0; u < kRound; ++u) {
-      most[u] = neg_inf();
-      if (w0 + rounds * STEP + u * kThreads < w1) most[u] = add(q[u]);  // (the same for all)
+      for (int i = 0; i < 4; ++i) q[u][i] = v + u * kThreads < w1 ? q[u][i] : ninf;
+      most[u] = add(q[u]);
     }
   }
   int n = 0;
