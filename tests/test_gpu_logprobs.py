@@ -248,3 +248,27 @@ def test_logprobs_on_another_stream(S):
     side.synchronize()
     for a, b in zip(out, want):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("S,V,M", [(2, 30001, 700), (257, 900, 257), (3, 200, 1000)])
+def test_logprobs_many_given_tokens(S, V, M):
+    """more given tokens than a workgroup has threads"""
+    check(rows_of("normal", S, V, M), torch.bfloat16, 1.0, M, 4, 3, M)
+
+
+def test_logprobs_most_rows():
+    """2^24 - 1 rows of one token: its log probability is 0 but for roundings, whatever the logit, and no workspace is needed"""
+    S = 2 ** 24 - 1
+    x = torch.arange(S, dtype=torch.int32, device=DEV).remainder_(251).float()
+    assert osc.osc_logprobs_workspace(S, 1, 1) == 0
+    x[S - 2] = -INF
+    ids = torch.zeros((S, 1), dtype=torch.int32, device=DEV)
+    ids[S - 1] = 1
+    LP, ENT, TV, TI = run(x, osc.OSC_Y_F32, S, 1, 1, 1.0, ids, 1)
+    assert bool(torch.isnan(LP[S - 2]).all()) and float(LP[S - 1]) == -INF and int(TI[S - 2]) == -1
+    keep = torch.ones(S, dtype=torch.bool, device=DEV)
+    keep[S - 2] = False
+    tol = 2.0 ** -24 * (1 + 22 + 8 + 8 * 250)  # as in check()
+    assert bool((TI[keep] == 0).all())
+    for t, most in ((TV[keep], tol), (LP[:S - 2], tol), (ENT[keep], 10 * tol)):
+        assert bool((t.abs() <= most).all())

@@ -201,3 +201,25 @@ def test_layer_caches_are_checked():
     with pytest.raises(osc.OscError) as e:  # a layer twice
         osc.osc_tree_commit(osc.LayerCaches([KC[0], KC[0]], list(VC), 3, 2, 64, 16), i32([0]), i32([0, 1]), i32([1]), i32([[0]]), 1, 1, 1)
     assert e.value.status == 2
+
+
+def test_tree_commit_all_layers_replayed():
+    """128 layers, whose addresses a captured call keeps; other paths in each replay, with eager work between."""
+    L, NP, HKV, page, D, N, R = 128, 6, 2, 16, 64, 16, 2
+    KC, VC = caches(L, NP, HKV, page, D, 5)
+    slot, cu = i32([16 * 3 + (5 + i) % 16 if i < 11 else 16 + i for i in range(16)] + list(range(64, 80))), i32([0, 16, 32])
+    acc, path = i32([0, 0]), i32([[-1] * N] * R)
+    held = osc.LayerCaches(list(KC), list(VC), NP, HKV, D, page)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        osc.osc_tree_commit(held, slot, cu, acc, path, R, 32, N)
+    del held  # the call read the addresses; the caches live
+    rng = np.random.default_rng(1)
+    for it in range(4):
+        took = [[0] + sorted(rng.choice(np.arange(1, 16), 7, replace=False).tolist()) for _ in range(R)]
+        acc.copy_(i32([8, 8 - it])), path.copy_(i32([t + [-1] * 8 for t in took]))
+        k, v = KC.clone(), VC.clone()
+        osc.osc_tree_commit(osc.LayerCaches(list(k), list(v), NP, HKV, D, page), slot, cu, acc, path, R, 32, N)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(KC, k) and torch.equal(VC, v)
