@@ -11,7 +11,7 @@
 // many workgroups as run at once, since a step's few trees have no tiles to fill the card with; a second launch joins the cut ones.
 // Measured with 32 query and 8 key heads of 128, both launches: 8 nodes in each of 32 requests, 109 thousand keys, 96 us, bound by HBM
 // (441 MB, 4.8 TB/s); 64 nodes there 123, where the tiles' steps of 2 us run beside the same bytes and 35 MB of partial outputs are written
-// and read again; 256 nodes over 32700 keys 146, bound by the steps (2 us, of which the matrix unit works 0.85 to 1); 16 nodes over 4000 keys
+// and read again; 256 nodes over 32700 keys 144, bound by the steps (2 us, of which the matrix unit works 0.85 to 1); 16 nodes over 4000 keys
 // 17, a chain of latencies: lengths and cuts 1.4, the request 0.8, pages, queries and masks 1.3, first keys 2.1, steps 4, stores 0.5, and two launches.
 #include "osc_attn_dev.h"
 
@@ -154,17 +154,18 @@ __global__ __launch_bounds__(512, 2) void k_attn_tree_large(TreeArgs a) {
 // Joins the parts of the tile that part w noted: o = sum_k 2^(m_k - m) o_k / sum_k 2^(m_k - m) l_k with m the largest
 // m_k, in a fixed order.  A lane has a piece of 16 bytes of a row's outputs, and reads its parts and their maxima and sums
 // FLY at once: the parts lie far apart, and a load that waits for another takes 2 to 3 us.
+// FIND, where there are fewer tiles than parts: workgroup j of a head looks for its j-th noted tile.  (A workgroup for each part, most of them
+// with nothing to do: 256 nodes over 32700 keys 13.7 us, 9.3 so; 16 over 4000 19 and 4.)
 // SHARE > 1, for few tiles of many parts each: that many wavefronts take parts of the same pieces in turn and join theirs through LDS
-// (else a wavefront's chain is long and the card empty), and workgroup j of a head looks for its j-th noted tile (a workgroup for
-// each part, most of them with nothing to do, took 19 us to come and go).
-template <int D, int ROWS, int SHARE>
+// (else a wavefront's chain is long and the card empty).
+template <int D, int ROWS, int SHARE, bool FIND>
 __global__ __launch_bounds__(512) void k_attn_tree_join(TreeArgs a) {
   constexpr int FLY = 4, P = D / 4;  // pieces of a row
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int h = blockIdx.x % a.HKV;
   int w = blockIdx.x / a.HKV;
   int4 note;
-  if constexpr (SHARE > 1) {
+  if constexpr (FIND) {
     constexpr int MOST = 2 * kCUs / 64;  // a lane's notes
     int4 noted[MOST];
     int left = w;
@@ -287,14 +288,17 @@ static hipError_t launch_rows(const TreeArgs& a, int N, hipStream_t st) {
   }
   // the 64 pieces of a tile that a wavefront joins; no more rows than the call has tokens
   const long most = ((long)a.S * a.g + 31) / 32 * 32, pieces = (most < ROWS ? most : ROWS) * (D / 4) / 64;
-  // Tiles of 24 parts and more, were all requests alike, are joined by 8 wavefronts each.
-  const long tiles = (long)a.R * ((N * a.g + ROWS - 1) / ROWS);
-  if (24 * tiles <= a.target) {
-    const long all = (long)a.S * a.g / ROWS + (a.R < a.S ? a.R : a.S);  // tiles that there can be, whatever the lengths
-    hipLaunchKernelGGL((k_attn_tree_join<D, ROWS, 8>), dim3((unsigned)((all < a.target ? all : a.target) * a.HKV), (unsigned)pieces), dim3(512), 0, st, a);
-    return hipGetLastError();
+  const long all = (long)a.S * a.g / ROWS + (a.R < a.S ? a.R : a.S);  // tiles that there can be, whatever the lengths
+  const unsigned found = (unsigned)((all < a.target ? all : a.target) * a.HKV), eights = (unsigned)((pieces + 7) / 8);
+  // Tiles of 24 parts and more, were all requests alike, are joined by 8 wavefronts each.  The search pays where at most half of the parts can
+  // begin a tile (8 trees of 64 nodes, 32 parts a head: 8.9 us with it, 14.8 without; 15 trees 15.6 and 13.0, 32 of 8 nodes 11.4 and 4.9).
+  if (24 * (long)a.R * ((N * a.g + ROWS - 1) / ROWS) <= a.target) {
+    hipLaunchKernelGGL((k_attn_tree_join<D, ROWS, 8, true>), dim3(found, (unsigned)pieces), dim3(512), 0, st, a);
+  } else if (2 * all <= a.target) {
+    hipLaunchKernelGGL((k_attn_tree_join<D, ROWS, 1, true>), dim3(found, eights), dim3(512), 0, st, a);
+  } else {
+    hipLaunchKernelGGL((k_attn_tree_join<D, ROWS, 1, false>), dim3(grid, eights), dim3(512), 0, st, a);
   }
-  hipLaunchKernelGGL((k_attn_tree_join<D, ROWS, 1>), dim3(grid, (unsigned)((pieces + 7) / 8)), dim3(512), 0, st, a);
   return hipGetLastError();
 }
 
