@@ -167,6 +167,7 @@ def test_tree_commit(HKV, D, page, L):
     acc[4], path[4] = 40, list(range(40))               # all stay where they are
     acc[0], path[0] = 20, list(range(20, 40)) + [-1] * 20   # all move, from right behind what is written
     check_commit(L, HKV, D, page, slot, cu, acc, path, 6, T, N, NP, 2)
+    acc[4], path[4] = 39, [0] + list(range(2, 40)) + [-1]   # each to the slot that the one before it left
     acc[5], path[5] = 2, [0, 32] + [-1] * 38
     check_commit(L, HKV, D, page, slot, cu, acc, path, 6, T, N, NP, 3)
 

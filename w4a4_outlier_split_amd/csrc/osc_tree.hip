@@ -125,11 +125,12 @@ __global__ __launch_bounds__(64) void k_tree_accept(AcceptArgs a) {
 }
 
 // ------------------------------------------------------------------ the move in the caches
-// Node PATH[k] goes to the slot of node k <= PATH[k].  Threads own a piece of a slot (16 bytes of a key, or a channel's value) and take
-// the moves in turn, four in flight: a slot that is written was read before, since a later move reads from behind it.
+// Node PATH[k] goes to the slot of node k <= PATH[k].  Threads own a piece of a slot's keys (16 bytes), four of a wavefront a channel of the values,
+// and take the moves in turn, four in flight: a slot that is written was read before, since a later move reads from behind it.
 // Values stand 2 bytes a slot and channel, so each is a line of its own, and the lines bound it: 28 moves of 32 trees in 36 layers
-// with 8 heads of 128, 8 MB by what moves, take 39 to 44 us, 6.6 of them for the keys; a bare loop over such loads takes 12 to 15 and over
-// such stores 15.  (Four layers a thread, for more lines in flight: 44.)
+// with 8 heads of 128, 8 MB by what moves, touch 73 MB of lines and take 26 to 28 us.  Moves in flight by lanes, rather than one behind the other in a
+// thread (37 to 43): a load of 64 channels waits for 64 lines.  (Two lanes a channel 29 to 30, eight 34 to 35; two layers a
+// workgroup 25 to 28, four 30 to 32.)
 __global__ __launch_bounds__(256) void k_tree_commit(CommitArgs a, int blocks) {
   __shared__ int from[OSC_MAX_TREE], to[OSC_MAX_TREE];
   __shared__ int moves;
@@ -156,7 +157,7 @@ __global__ __launch_bounds__(256) void k_tree_commit(CommitArgs a, int blocks) {
   if (k == 255) moves = at + (move ? 1 : 0);
   __syncthreads();
   const int n = moves, mask = (1 << a.sh) - 1;
-  const int pieces = a.HKV * a.D / 8, x = part * 256 + k;  // 16-byte pieces of a token's keys; then its values' channels
+  const int pieces = a.HKV * a.D / 8, x = part * 256 + k;  // 16-byte pieces of a token's keys (8 at least); then its values' channels, four threads each
   if (x < pieces) {
     uint8_t* kc = static_cast<uint8_t*>(a.KC[layer]);
     const int row = a.D / 8, h = x / row, c = x - h * row;
@@ -169,17 +170,15 @@ __global__ __launch_bounds__(256) void k_tree_commit(CommitArgs a, int blocks) {
       for (int j = 0; j < 4; ++j)
         if (i + j < n) *reinterpret_cast<u4*>(place(to[i + j])) = v[j];
     }
-  } else if (x < pieces + a.HKV * a.D) {
+  } else if (x < pieces + 4 * a.HKV * a.D) {
     uint16_t* vc = static_cast<uint16_t*>(a.VC[layer]);
-    const int y = x - pieces, h = y / a.D, d = y - h * a.D;
+    const int y = (x - pieces) / 4, turn = (x - pieces) % 4, h = y / a.D, d = y - h * a.D;
     auto place = [&](int s) { return vc + (((((long)(s >> a.sh) * a.HKV + h) * a.D + d) << a.sh) + (s & mask)); };
-    for (int i = 0; i < n; i += 4) {
-      uint16_t v[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = *place(from[i + j < n ? i + j : n - 1]);
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (i + j < n) *place(to[i + j]) = v[j];
+    for (int i = turn; i - turn < n; i += 4) {
+      uint16_t v = 0;
+      if (i < n) v = *place(from[i]);
+      __builtin_amdgcn_wave_barrier();  // the four have read, then they write
+      if (i < n) *place(to[i]) = v;
     }
   }
 }
@@ -209,9 +208,9 @@ hipError_t launch_tree_accept(const AcceptArgs& a, hipStream_t st) {
   return hipGetLastError();
 }
 
-// At most 4096 requests times 576 parts (1024 heads of 128) by 128 layers.
+// At most 4096 requests times 2112 parts (1024 heads of 128) by 128 layers.
 hipError_t launch_tree_commit(const CommitArgs& a, hipStream_t st) {
-  const int blocks = (a.HKV * a.D / 8 + a.HKV * a.D + 255) / 256;
+  const int blocks = (a.HKV * a.D / 8 + 4 * a.HKV * a.D + 255) / 256;
   hipLaunchKernelGGL(k_tree_commit, dim3((unsigned)(a.R * blocks), (unsigned)a.layers), dim3(256), 0, st, a, blocks);
   return hipGetLastError();
 }
