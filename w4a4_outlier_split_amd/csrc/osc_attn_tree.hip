@@ -12,7 +12,7 @@
 // Measured with 32 query and 8 key heads of 128, both launches: 8 nodes in each of 32 requests, 109 thousand keys, 96 us, bound by HBM
 // (441 MB, 4.8 TB/s); 64 nodes there 123, where the tiles' steps of 2 us run beside the same bytes and 35 MB of partial outputs are written
 // and read again; 256 nodes over 32700 keys 144, bound by the steps (2 us, of which the matrix unit works 0.85 to 1); 16 nodes over 4000 keys
-// 17, a chain of latencies: lengths and cuts 1.4, the request 0.8, pages, queries and masks 1.3, first keys 2.1, steps 4, stores 0.5, and two launches.
+// 17, a chain of latencies: lengths and cuts 1.4, the request 0.8, pages, queries and masks 1.3, first keys 2.1, steps 2 to 4, stores 0.5, and two launches.
 #include "osc_attn_dev.h"
 
 namespace osc {
@@ -49,9 +49,6 @@ struct TreeRequest {
   }
 };
 
-// Steps that a workgroup's part has at least: a part costs the join 2 to 3 us, a step 2
-constexpr int kMinSteps = 2;
-
 // Workgroup: key head h = blockIdx % HKV, part w = blockIdx / HKV of the row in which all tiles of the head stand, cut into equal
 // parts, as many as workgroups run at once; body(t, h) for each tile of the part in turn.  A tile that a cut goes through has
 // its unnormalised outputs left in the workspace: in the workgroup's second place where it begins there, in the first behind a cut.
@@ -79,7 +76,7 @@ __device__ __forceinline__ void each_tree_tile(const TreeArgs& a, Body body) {
     }
     all = lane_of(upto, lanes - 1);
     long p = a.target;
-    if (p > all / kMinSteps) p = all / kMinSteps;
+    if (p > all) p = all;  // (two steps a part at least: 16 nodes over 500 keys 11.8 us, 8.9 so; 64 over 1000 16.1 and 12.7; the join is the same)
     parts = p < 1 ? 1 : (int)p;
     each = uniform(divide(all, parts));
     over = (int)(all - each * parts);
