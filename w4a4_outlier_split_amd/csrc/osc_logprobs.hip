@@ -11,12 +11,11 @@
 // own in LDS, so that none waits for another: a few times K of a row in usual orders.  A list that is nearly full is cut to the
 // vectors that reach a better bound.  A part of fewer than 8 vectors a thread stays in registers, and is chosen from there.  At the
 // end the best K vectors, and seldom a few more, are read once more and their values put in order.  (Noting the values instead:
-// 2048 rows of 151936, K = 5 and 64, 154 and 250 us; vectors 117 and 131.)
+// 2048 rows of 151936, K = 5 and 64, 154 and 250 us; vectors 117 and 125.)
 //
-// Many rows are bound by HBM: 2048 bf16 rows of 151936 with 5 alternatives take 117 us, 5.3 TB/s, 512 take 39, and the rounds' loads
-// are under way while the round before is summed up.  One row is bound by latency: 14.5 us, 8 for a part's loads, maxima and choice, one
-// behind the other, and 6.4 for the parts' join.  Equal logits, which reach every bound, are the slow order: 2048 rows of zeros 124 to 132 us,
-// one 27 to 37.
+// Many rows are bound by HBM: 2048 bf16 rows of 151936 with 5 alternatives take 117 us, 5.3 TB/s, 512 take 37, and a round's loads
+// are under way while the round before is summed up.  One row is bound by latency: 13.2 us, 7 for a part's loads, maxima and choice, one
+// behind the other, and 6.3 for the parts' join.  Equal logits, which reach every bound, are the slow order: 2048 rows of zeros 120 us, one 23 to 30.
 #include "osc_internal.h"
 #include "osc_lanes.h"
 
@@ -74,7 +73,7 @@ struct Lds {
 };
 
 // Those of the threads' entries that reach `low` (> 0) behind the s.votes[0][0] that the list has, which count on.  (An atomic
-// addition for each lane: the compiler takes the lanes one by one, and one row with 64 alternatives 18.5 us.)
+// addition for each lane: the compiler takes the lanes one by one, and one row with 64 alternatives 18.5 us, 15.2 so.)
 template <int PER, int CAP>
 __device__ __forceinline__ void append(Lds<CAP>& s, const u64 (&e)[PER], u64 low) {
   const int lane = threadIdx.x & 63;
@@ -549,9 +548,8 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_join(LogprobsArgs a) {
 
 }  // namespace
 
-// Rows are cut where there are fewer than workgroups that keep the memory busy: one a CU, two where rows are cut anyway, in parts of
-// 2048 values at least.  (Rows of 151936, 8 alternatives, for 512 and 256 workgroups: 128 rows 26 and 28 us, 256 rows 32 and 31, 384 rows 40 and 37;
-// 1024 workgroups: 512 rows 48 us, 40 in one part each.)
+// Rows are cut where there are fewer than CUs, for two workgroups a CU, in parts of 2048 values at least.  (Rows of 151936, 8 alternatives, both
+// launches: 128 rows 22 us in four parts each, 25 in two, 24 in eight; 256 rows 29 in two, 29 whole; 384 rows 37 and 35; 512 rows 46 and 37.)
 LogprobsPlan logprobs_plan(int S, int V, int K) {
   LogprobsPlan p;
   long want = S >= 256 || S == 0 ? 1 : (512 + S - 1) / S;
