@@ -8,6 +8,7 @@ import tree_ref
 from test_pages_host import HostPages
 
 blk = pytest.importorskip("w4a4_outlier_split_amd.block", reason="libosc.so not built")
+osc = pytest.importorskip("w4a4_outlier_split_amd")
 
 
 class HostDrafts(blk.Drafts):
@@ -156,3 +157,33 @@ def test_sizes_are_checked():
         with pytest.raises(ValueError):
             blk.Drafts(torch, p, N, [], "cpu")
     assert len(blk.Drafts(torch, p, 4, [blk.LayerCache(torch, p, 1, 64, "cpu") for _ in range(130)], "cpu").groups) == 2
+
+
+def test_layers_of_other_heads():
+    """Each commit is told the heads that its layers have, whatever the layers' order; caches of another layout or that share bytes are refused."""
+    p = HostPages(torch, 2, 4, 16, 2, 8, "cpu")
+    heads = [(2, 128), (4, 64), (2, 128), (4, 128), (4, 64), (1, 64)]  # (2, 128) and (4, 64) have the same bytes
+    caches = [blk.LayerCache(torch, p, h, d, "cpu") for h, d in heads]
+    d = blk.Drafts(torch, p, 4, caches, "cpu")
+    place = {t.data_ptr(): t.shape for c in caches for t in (c.KC, c.VC)}
+    assert sum(g.layers for g in d.groups) == len(caches) and len(place) == 2 * len(caches)
+    for g in d.groups:
+        for i in range(g.layers):
+            assert place.pop(g._kc[i]) == (4, g.HKV, 16, g.D) and place.pop(g._vc[i]) == (4, g.HKV, g.D, 16)
+    assert not place
+    other = HostPages(torch, 2, 4, 32, 2, 8, "cpu")  # larger pages, as many of them
+    turned = blk.LayerCache(torch, p, 2, 128, "cpu")
+    turned.VC = turned.VC.transpose(2, 3).contiguous()
+    for bad in (blk.LayerCache(torch, other, 2, 128, "cpu"), turned):
+        with pytest.raises(osc.OscError) as e:
+            blk.Drafts(torch, p, 4, [caches[0], bad], "cpu")
+        assert e.value.status == 2
+    half = blk.LayerCache(torch, p, 1, 64, "cpu")
+    half.KC = caches[5].KC.clone()
+    half.VC = caches[3].VC.view(-1)[4096:4096 + half.VC.numel()].view(half.VC.shape)  # among another layer's, of other heads
+    many = [blk.LayerCache(torch, p, 1, 64, "cpu") for _ in range(129)]
+    for bad in (caches + [half], [caches[1], caches[1]], many + [many[0]]):  # the last is of another commit than the first
+        with pytest.raises(ValueError):
+            blk.Drafts(torch, p, 4, bad, "cpu")
+    pool = blk.LayerCache(torch, HostPages(torch, 2, 9, 16, 2, 8, "cpu"), 2, 128, "cpu")  # of more pages than are dealt out
+    assert blk.Drafts(torch, p, 4, [pool], "cpu").groups[0].layers == 1

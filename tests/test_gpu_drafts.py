@@ -252,3 +252,35 @@ def test_step_binding_refuses():
                 with pytest.raises(osc.OscError) as e:
                     osc.osc_attn_tree(*[bad if j == i else a for j, a in enumerate(args)])
                 assert e.value.status == status, (i, status)
+
+
+def test_commit_in_layers_of_other_heads():
+    """Layers with heads of their own, some of as many bytes as others: in each the path's nodes move, and nothing else."""
+    pages = make_pages()
+    heads = [(2, 128), (4, 64), (4, 128), (2, 128), (1, 64)]
+    caches = [blk.LayerCache(torch, pages, h, d, DEV) for h, d in heads]
+    g = torch.Generator(device=DEV).manual_seed(3)
+    for c in caches:
+        for t in (c.KC, c.VC):
+            t.copy_(torch.randn(t.shape, generator=g, device=DEV))
+    drafts = blk.Drafts(torch, pages, N, caches, DEV)
+    sizes = (16, 9, 0)
+    pages.new.copy_(torch.tensor(sizes, dtype=torch.int32))
+    rng = np.random.default_rng(1)
+    parents, parent, token, choice = trees(rng, sizes)
+    drafts.parent.copy_(parent), drafts.token.copy_(token)
+    pages.plan(), drafts.plan()
+    drafts.accept(choice.to(DEV))
+    want = [(c.KC.clone(), c.VC.clone()) for c in caches]
+    slot, acc, path, moved = pages.slot.tolist(), drafts.acc.tolist(), drafts.path.tolist(), 0
+    for r, t0 in enumerate((0, 16, 25)):
+        for k in range(acc[r]):
+            a, b = slot[t0 + path[r][k]], slot[t0 + k]
+            moved += a != b
+            for kc, vc in want:
+                kc[b // PAGE, :, b % PAGE] = kc[a // PAGE, :, a % PAGE].clone()
+                vc[b // PAGE, :, :, b % PAGE] = vc[a // PAGE, :, :, a % PAGE].clone()
+    assert moved > 0
+    drafts.commit()
+    for i, (c, (kc, vc)) in enumerate(zip(caches, want)):
+        assert torch.equal(c.KC, kc) and torch.equal(c.VC, vc), i

@@ -396,7 +396,8 @@ def osc_tree_accept(TOKEN, PARENT, CHOICE, ldc: int, SLOT, POS, P: int, CU, R: i
 
 
 class LayerCaches:
-    """The layers' caches of osc_tree_commit, KC and VC of each (tensors, or addresses), checked once and kept."""
+    """The layers' caches of osc_tree_commit, KC and VC of each (tensors, or addresses), checked once and kept.  All have the
+    same heads and pages: a tensor of four dimensions is [NP, HKV, page, D] or [NP, HKV, D, page], NP or more, any other is taken as its bytes."""
 
     def __init__(self, KC, VC, NP: int, HKV: int, D: int, page: int):
         c = "LayerCaches"
@@ -406,6 +407,10 @@ class LayerCaches:
             raise OscError(2, c, f"{self.layers} layers of keys, {len(self.VC)} of values, at most {OSC_MAX_LAYERS}")
         n = 2 * NP * HKV * page * D
         held = [t for t in self.KC + self.VC if t is not None and type(t) is not int]
+        for ts, block in ((self.KC, (HKV, page, D)), (self.VC, (HKV, D, page))):
+            for t in ts:
+                if t is not None and type(t) is not int and t.dim() == 4 and tuple(t.shape[1:]) != block:
+                    raise OscError(2, c, f"a cache of shape {tuple(t.shape)} among those of {block} a page")
         self.device = held[0].get_device() if held else None
         at = lambda ts: (_P * max(1, self.layers))(*[_at(c, self.device, t, n, _BF16) for t in ts])
         self._kc, self._vc = at(self.KC), at(self.VC)

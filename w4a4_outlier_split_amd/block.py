@@ -319,8 +319,8 @@ class LayerCache:
 
 
 class Drafts:
-    """Trees of drafted tokens for steps on ``pages``, of at most N nodes a request, over the LayerCache of each layer.  A
-    tree's node 0 is the request's last certain token, which is not in the cache yet.  One step: set ``pages.new`` to the trees' sizes,
+    """Trees of drafted tokens for steps on ``pages``, of at most N nodes a request, over the LayerCache of each layer, whose heads may
+    differ.  A tree's node 0 is the request's last certain token, which is not in the cache yet.  One step: set ``pages.new`` to the trees' sizes,
     ``token`` and ``parent`` (int32 [T], request by request as the plan has them; a parent is a node's number in its request, -1
     the context); call ``pages.plan`` and ``plan``; run the blocks with ``drafts``; call ``accept`` with the token chosen behind
     each node, ``commit`` and ``advance`` (not the pages' own), all on one stream.  All of it is captureable in a graph.
@@ -339,8 +339,16 @@ class Drafts:
         self.acc, self.path, self.next = i32(pages.R), i32(pages.R, N), i32(pages.R)
         self.at = torch.arange(pages.free.numel(), dtype=torch.int32, device=device)
         self.layers = list(caches)
-        self.groups = [LayerCaches([c.KC for c in g], [c.VC for c in g], pages.NP, g[0].KC.shape[1], g[0].KC.shape[3], pages.page)
-                       for g in (self.layers[i:i + OSC_MAX_LAYERS] for i in range(0, len(self.layers), OSC_MAX_LAYERS))]
+        alike = {}  # one commit moves layers of the same heads
+        for c in self.layers:
+            alike.setdefault((c.KC.shape[1], c.KC.shape[3]), []).append(c)
+        self.groups = [LayerCaches([c.KC for c in g], [c.VC for c in g], pages.NP, HKV, D, pages.page)
+                       for (HKV, D), all_of in alike.items()
+                       for g in (all_of[i:i + OSC_MAX_LAYERS] for i in range(0, len(all_of), OSC_MAX_LAYERS))]
+        # a commit refuses caches that share bytes; two commits would move those twice
+        held = sorted((t for c in self.layers for t in (c.KC, c.VC)), key=lambda t: t.data_ptr())
+        if any(_meet(a, b) for a, b in zip(held, held[1:])):
+            raise ValueError("two caches share bytes; one that several layers read is given once")
 
     def plan(self, stream=None) -> None:
         """Behind the pages' plan: the nodes' positions into ``pages.pos``, and their masks."""
