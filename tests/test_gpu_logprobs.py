@@ -272,3 +272,25 @@ def test_logprobs_most_rows():
     assert bool((TI[keep] == 0).all())
     for t, most in ((TV[keep], tol), (LP[:S - 2], tol), (ENT[keep], 10 * tol)):
         assert bool((t.abs() <= most).all())
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("S,V", [(6, 4001), (300, 30001), (5, 300)])
+@pytest.mark.parametrize("scale", [1e-37, 1e-39, 1e-45])
+def test_logprobs_without_a_distribution_at_the_smallest_scales(dt, S, V, scale):
+    """+inf behind a thread's first values, where no finite logit moves the reference any more: NaN and -1, as at any scale."""
+    x = rows_of("normal", S, V, 4)
+    good = torch.from_numpy(x).to(DEV).to(dt)
+    bad = good.clone()
+    bad[0, V - 1], bad[2, V - 500 if V > 500 else 17], bad[3, V // 2] = INF, INF, float("nan")
+    xt = osc.OSC_Y_BF16 if dt == torch.bfloat16 else osc.OSC_Y_F32
+    ids = torch.tensor([[3, -1, V]] * S, dtype=torch.int32, device=DEV)
+    a, b = run(good, xt, S, V, V, scale, ids, 6), run(bad, xt, S, V, V, scale, ids, 6)
+    for r in (0, 2, 3):
+        assert bool(torch.isnan(b[0][r]).all()) and bool(torch.isnan(b[1][r])) and bool(torch.isnan(b[2][r]).all()) and bool((b[3][r] == -1).all()), r
+    for r in (1, 4):
+        for p, q in zip(a, b):
+            assert torch.equal(p[r], q[r])
+    # every token is as likely as any: sums and logarithm as in check(), the largest |scale x| below 2^-90
+    tol = 2.0 ** -24 * (V / 256 + 22 + 8 + 4 * np.log(V))
+    assert bool(((a[0][:, 0].double() + np.log(V)).abs() <= tol).all()) and bool(((a[1].double() - np.log(V)).abs() <= 2 * tol * np.log(V)).all())

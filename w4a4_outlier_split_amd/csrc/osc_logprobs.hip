@@ -238,7 +238,9 @@ __device__ __forceinline__ void in_order(Lds<CAP>& s, int n, int K, Write write,
   if (i >= n && i < K) none(i);
 }
 
-__device__ __forceinline__ bool is_none(const Sum& s) { return !(s.l > 0.0f) || !(s.r < __builtin_inff()); }
+// No value above -inf, a NaN, or +inf: that shows in R, or in the sum alone, where no finite value moves R any more (kSlack over
+// the smallest scales is +inf).
+__device__ __forceinline__ bool is_none(const Sum& s) { return !(s.l > 0.0f && s.l < __builtin_inff()) || !(s.r < __builtin_inff()); }
 
 // (no probability is over 1, nor an entropy below 0, by rounding)
 __device__ __forceinline__ float logp(const Sum& s, float log2l, float x, float c) {
