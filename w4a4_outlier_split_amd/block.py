@@ -495,8 +495,12 @@ class Head:
         self.proj.gemm(bufs["x"], S, bufs["logits"], OSC_Y_BF16, stream)
 
     def logprobs(self, S: int, bufs, ids=None, scale: float = 1.0, stream=None) -> None:
-        """Of p = softmax(scale logits): log p of the tokens ids (int32 [S, M]) to bufs["lp"], the entropy to bufs["ent"], the most likely
-        tokens' log p and ids to bufs["topv"] and bufs["topi"] [S, K]."""
+        """Of p = softmax(scale logits): log p of the tokens ids (int32 [S, M] with the buffers' M, or more rows; None: without) to bufs["lp"],
+        the entropy to bufs["ent"], the most likely tokens' log p and ids to bufs["topv"] and bufs["topi"] [S, K]."""
         M = bufs["M"] if ids is not None else 0
+        if ids is not None and not isinstance(ids, int):  # too few rows are refused by the call
+            n = ids.dim()
+            if ids.shape[1] != M if n == 2 else n != 1 or M == 0 or (M > 1 and ids.numel() > S * M):
+                raise ValueError(f"given tokens of shape {tuple(ids.shape)} where rows of {M} are read")
         osc_logprobs(bufs["logits"], OSC_Y_BF16, S, self.V, self.proj.N, scale, ids, M, bufs["K"], bufs["lp"], bufs["ent"], bufs["topv"],
                      bufs["topi"], bufs["ws"], stream)
