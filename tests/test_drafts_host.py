@@ -187,3 +187,18 @@ def test_layers_of_other_heads():
             blk.Drafts(torch, p, 4, bad, "cpu")
     pool = blk.LayerCache(torch, HostPages(torch, 2, 9, 16, 2, 8, "cpu"), 2, 128, "cpu")  # of more pages than are dealt out
     assert blk.Drafts(torch, p, 4, [pool], "cpu").groups[0].layers == 1
+
+
+def test_what_is_counted_as_lost():
+    """An ordinary step's lost tokens and the trees without a written node 0, one each, in one number; drafts without a place are none."""
+    rng = np.random.default_rng(3)
+    p, d, cache, text = make(3, 30, 16, 8, 12, 20)
+    step(p, d, cache, text, [5, 20, 4], rng)  # the second tree loses 13 drafts, the third its node 0
+    assert int(p.lost) == 1 and int(d.acc[2]) == 0 and int(d.next[2]) == -1
+    p.new.copy_(torch.tensor([8, 6, 0], dtype=torch.int32))
+    p.plan(), p.advance()  # two tokens more than rows
+    with pytest.raises(RuntimeError, match=r"^3 tokens \(of a tree of drafted ones its node 0 alone counts\) found no row"):
+        p.check()
+    p.check()
+    step(p, d, cache, [[0] * n for n in p.ctx.tolist()], [5, 5, 2], rng)
+    p.check()

@@ -235,7 +235,9 @@ class Pages:
     lost: nothing of them is written, their rows of the step's output mean nothing, ``ctx`` does not count
     them, and ``lost`` (int32 [1], device) does.  They are a request's last ones, so ``ctx`` tells what is
     left to be given again.  A request that passes the end of the blocks' rotary table cannot go on: ``ctx``
-    does count those tokens, with their pages, and so does ``lost``.  ``rows`` is how many rows the blocks
+    does count those tokens, with their pages, and so does ``lost``.  After a step with trees of drafted tokens (Drafts)
+    ``lost`` counts a tree whose node 0 was not written as one token, that node; other nodes that find no place are drafts
+    that cannot be accepted, and are not counted.  ``rows`` is how many rows the blocks
     ran with since the plan (T until then), ``positions`` how many their rotary table has.  Table entries
     behind a request's ceil(ctx / page) first mean nothing."""
 
@@ -281,7 +283,8 @@ class Pages:
         if n:
             self.lost.zero_()
             self._wait()
-            raise RuntimeError(f"{n} tokens found no row, free page, room in their request's {self.MB} pages or rotary table")
+            raise RuntimeError(f"{n} tokens (of a tree of drafted ones its node 0 alone counts) found no row, free page, "
+                               f"room in their request's {self.MB} pages or rotary table")
 
     def _wait(self) -> None:
         """For the device's work on every stream: a step may run on another than torch's current one."""
@@ -327,7 +330,7 @@ class Drafts:
 
     ``acc`` (int32 [R]) nodes of each request are in the cache then, those of ``path`` [R, N] in order, and ``next`` [R] is the
     token behind them, the next tree's node 0 (-1 for a request without a tree, or whose node 0 found no row, page, room
-    or position: ``pages.lost`` counts those, and the tree is to be given again)."""
+    or position: ``pages.lost`` counts one token for each, and the tree is to be given again)."""
 
     def __init__(self, torch, pages: Pages, N: int, caches, device):
         if not 1 <= N <= OSC_MAX_TREE:
