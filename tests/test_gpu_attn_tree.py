@@ -294,3 +294,26 @@ def test_attn_tree_on_another_stream():
         attend(p, ws=ws, out=out, stream=side)
         side.synchronize()
         assert torch.equal(out.view(torch.int16), want.view(torch.int16))
+
+
+@pytest.mark.parametrize("HQ,HKV,N,D,page", [(4, 1, 4, 128, 32), (16, 16, 16, 64, 16), (8, 8, 8, 128, 64), (8, 1, 2, 64, 32), (3, 1, 5, 128, 16), (2, 2, 1, 64, 256), (16, 1, 1, 128, 32)])
+def test_attn_tree_not_finite_in_tiles_of_16_rows(HQ, HKV, N, D, page):
+    """The same where a tree's rows fit into one tile, over contexts that leave it whole and that cut it: the join takes NaN parts too."""
+    assert N * HQ // HKV <= 16
+    rng = np.random.default_rng(N + D)
+    for kind in ("near", "star", "roots"):
+        parents = [tree_ref.tree(rng, N, kind), tree_ref.tree(rng, N, "chain"), tree_ref.tree(rng, N, kind), tree_ref.tree(rng, N, kind)]
+        p = build(list(zip((333, 64, 9000, 0), parents)), HQ, HKV, D, page, N, 7)
+        for r, j, what, value in ((0, N // 2, "VC", NAN), (0, N - 1, "VC", float("inf")), (0, N // 3, "KC", NAN), (1, N - 1, "VC", -float("inf")), (1, N // 2, "KC", NAN),
+                                  (2, N // 2, "VC", NAN), (2, N - 1, "KC", NAN), (3, N // 3, "VC", float("inf"))):
+            at = p["kv"][r] - N + j
+            t, id = p[what], p["table"][r, at // page]
+            if what == "KC":
+                t[id, :, at % page, D - 3] = value
+            else:
+                t[id, :, 5, at % page] = value
+        check(p, attend(p), what=kind)
+        # beside pages that do not exist: the first, one ahead of the new keys, and the last, of the new keys themselves
+        for r, at in ((0, 0), (2, 3000), (2, 8999), (0, 332), (2, 9000 + N - 1)):
+            p["table"][r, at // page] = -1
+            check(p, attend(p), what=(kind, r, at))
