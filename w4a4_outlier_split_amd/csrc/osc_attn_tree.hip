@@ -10,9 +10,10 @@
 // on the ring of keys in LDS otherwise, so that a request's keys are read from memory once.  Every row of tiles is cut evenly among as
 // many workgroups as run at once, since a step's few trees have no tiles to fill the card with; a second launch joins the cut ones.
 // Measured with 32 query and 8 key heads of 128, both launches: 8 nodes in each of 32 requests, 109 thousand keys, 96 us, bound by HBM
-// (441 MB, 4.8 TB/s); 64 nodes there 123 to 126, where the tiles' steps of 2 us run beside the same bytes and 35 MB of partial outputs are written
-// and read again; 256 nodes over 32700 keys 144, bound by the steps (2 us, of which the matrix unit works 0.85 to 1); 16 nodes over 4000 keys
-// 15.6, a chain of latencies: lengths and cuts 1.4, the request 0.8, pages, queries and masks 1.3, first keys 2.1, steps 2 to 4, stores 0.5, and two launches.
+// (441 MB in the first kernel's 92 us, 4.8 TB/s); 64 nodes there 123 to 129, where the tiles' steps of 2 us run beside the same bytes and 35 MB of
+// partial outputs are written and read again; 256 nodes over 32700 keys 144 to 151, bound by the steps (2 us, of which the matrix unit works 0.85
+// to 1); 16 nodes over 4000 keys 15.6, a chain of latencies: lengths and cuts 1.4, the request 0.8, pages, queries and masks 1.3, first keys 2.1, steps
+// 2 to 4, stores 0.5, and two launches.
 #include "osc_attn_dev.h"
 
 namespace osc {
